@@ -9,10 +9,13 @@ Entry points (same names as the C ABI):
   mx_quantize, mx_dequantize, fp8_quantize_pertensor, ring_fold, mx_gemm,
   mx_gemm_mx_out, mm_fp8, sf_to_mma, last_device_status; plus ``quantize`` / ``quantize_dual`` with the
   argument order of AstrAI's fp8 adapter (astrai/extension/ops/fp8.py).
+Around the products of a training step: layer_norm, mx_layer_norm,
+  layer_norm_backward, policy_loss, grad_norm, clip_grad_norm.
 """
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional
@@ -27,6 +30,7 @@ ROW, COL, DUAL = 1, 2, 3
 FLOOR_OCP, CEIL = 0, 1
 RNE, SR, SR4 = 0, 1, 2
 SF_CANONICAL, SF_MMA = 0, 1
+BF16, F32 = 0, 1
 
 class _Choices(dict):
     """Name (or code) -> library code; an unknown name is a ValueError."""
@@ -90,6 +94,18 @@ def load() -> ctypes.CDLL:
     L.mxq_gemm_noalloc.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, i32, vp, i32, vp]
     L.mxq_gemm_mx_out.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, i32, i32, i32, i32, vp, vp, vp, vp, vp]
     L.mxq_mm_fp8.argtypes = [vp, vp, i64, i64, i64, i64, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+    L.mxq_layer_norm.argtypes = [vp, i64, i64, i64, i32, vp, i32, vp, i32, f32, i32, vp, vp, vp, vp]
+    L.mxq_layer_norm_mx.argtypes = [vp, i64, i64, i64, i32, vp, i32, vp, i32, f32, i32, i32, i32, i32, vp, vp, vp, vp,
+                                    vp, vp, vp]
+    L.mxq_layer_norm_backward_workspace_size.argtypes = [i64, i64, vp]
+    L.mxq_layer_norm_backward.argtypes = [vp, i64, i32, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, vp, vp, vp,
+                                          ctypes.c_size_t, vp]
+    L.mxq_policy_loss_workspace_size.argtypes = [i64, vp]
+    L.mxq_policy_loss.argtypes = [vp, i64, i64, i64, i32, vp, i32, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp, vp,
+                                  i64, i32, vp, ctypes.c_size_t, vp]
+    L.mxq_grad_norm_workspace_size.argtypes = [i32, vp]
+    L.mxq_grad_norm.argtypes = [vp, i32, vp, vp, ctypes.c_size_t, vp]
+    L.mxq_clip_grad_norm.argtypes = [vp, i32, f32, vp, vp, ctypes.c_size_t, vp]
     L.mxq_sf_to_mma.argtypes = [vp, i64, i64, vp, vp]
     L.mxq_last_device_status.argtypes = [vp]
     L.mxq_strerror.argtypes = [i32]
@@ -98,7 +114,10 @@ def load() -> ctypes.CDLL:
     L.mxq_test_stall_next_launch.argtypes = [i32]
     for name in ("mxq_quantize", "mxq_quantize_group", "mxq_dequantize", "fp8_quantize_pertensor", "fp8_ring_fold", "mxq_gemm",
                  "mxq_gemm_mixed", "mxq_gemm_workspace_size", "mxq_gemm_ws", "mxq_gemm_noalloc",
-                 "mxq_gemm_mx_out", "mxq_mm_fp8", "mxq_sf_to_mma",
+                 "mxq_gemm_mx_out", "mxq_mm_fp8", "mxq_layer_norm", "mxq_layer_norm_mx",
+                 "mxq_layer_norm_backward_workspace_size", "mxq_layer_norm_backward",
+                 "mxq_policy_loss_workspace_size", "mxq_policy_loss", "mxq_grad_norm_workspace_size",
+                 "mxq_grad_norm", "mxq_clip_grad_norm", "mxq_sf_to_mma",
                  "mxq_last_device_status", "mxq_version", "mxq_test_stall_next_launch"):
         getattr(L, name).restype = i32
     _lib = L
@@ -482,6 +501,303 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, trans_a: bool 
     _call("mxq_mm_fp8", a.device, _ptr(A), _ptr(B), batch, M, N, K, int(ba > 1), int(bb > 1), ta, tb, f,
           _ptr(scale), _ptr(bias), _ptr(c))
     return c
+
+
+# --------------------------------------------------------------------------- around the products of a training step
+# These calls are short, so their host path is too: pointers go to ctypes as
+# plain integers, outputs are one torch.empty each, and the device guard is
+# entered only when another device is current.
+_TYPE = {torch.bfloat16: BF16, torch.float32: F32}
+_PARAM = (torch.bfloat16, torch.float32)
+_F32_ONLY = (torch.float32,)
+_SCRATCH = {}
+_SIZES = {}
+
+
+def _launch(name: str, device: torch.device, *args) -> None:
+    """_call, with pointers as integers: entry point ``name`` with ``device``
+    current and torch's current stream of that device as the last argument."""
+    fn = getattr(_lib or load(), name)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise MXQError(rc, name)
+
+
+def _size(name: str, device: torch.device, *args) -> int:
+    """Workspace bytes that the library asks for (remembered per device and sizes)."""
+    key = (name, device.index, args)
+    n = _SIZES.get(key)
+    if n is None:
+        c = ctypes.c_size_t(0)
+        with torch.cuda.device(device):
+            _check(getattr(load(), name)(*args, ctypes.byref(c)), name)
+        if len(_SIZES) >= 4096:
+            _SIZES.clear()
+        n = _SIZES[key] = c.value
+    return n
+
+
+def _scratch(device: torch.device, nbytes: int) -> torch.Tensor:
+    """Zero-filled scratch of at least ``nbytes`` for torch's current stream
+    on ``device``, kept and grown as needed: one per stream, because calls
+    that share it must not overlap on the GPU."""
+    key = (device.index, torch._C._cuda_getCurrentRawStream(device.index))
+    w = _SCRATCH.get(key)
+    if w is None or w.numel() < nbytes:
+        w = _SCRATCH[key] = torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=device)
+    return w
+
+
+def _matrix(t: torch.Tensor, name: str):
+    """(type code, rows, cols, row stride) of a 2-D bf16 or float32 tensor
+    whose rows are contiguous (the row stride may exceed cols)."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPE:
+        raise ValueError(f"{name} must be a bf16 or float32 tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    rows, cols = t.shape
+    if cols < 1:
+        raise ValueError(f"{name} must have at least one column")
+    if t.is_contiguous():
+        return _TYPE[t.dtype], rows, cols, cols
+    ld, step = t.stride()
+    if rows < 2:
+        ld = cols
+    if (cols > 1 and step != 1) or ld < cols:
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    return _TYPE[t.dtype], rows, cols, ld
+
+
+def _vector(t: torch.Tensor, name: str, n: int, dtypes) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != 1 or not t.is_contiguous():
+        names = " or ".join(str(d).replace("torch.", "") for d in dtypes)
+        raise ValueError(f"{name} must be a contiguous {names} vector")
+    if t.numel() != n:
+        raise ValueError(f"{name} holds {t.numel()} elements, expected {n}")
+
+
+def _same_device(first: torch.Tensor, *others) -> torch.device:
+    """The CUDA device of ``first``, which every (tensor, name) must share."""
+    index = first.get_device()
+    for t, name in others:
+        if t is not None and (t.get_device() != index or index < 0):
+            _on_device(((t, name),), first.device)
+    return first.device
+
+
+def _param(t: Optional[torch.Tensor], name: str, n: int):
+    """(pointer, type code) of a weight or bias vector, or of none."""
+    if t is None:
+        return 0, 0
+    _vector(t, name, n, _PARAM)
+    return t.data_ptr(), _TYPE[t.dtype]
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, out_dtype: Optional[torch.dtype] = None):
+    """Layer norm of the rows of ``x`` [rows][cols] (bf16 or float32, any
+    sizes, row stride may exceed cols): (y, mean, rstd), y of ``out_dtype``
+    (x's type by default), mean and rstd float32 [rows] for
+    layer_norm_backward.  ``weight`` and ``bias`` are bf16 or float32 vectors
+    or None; the arithmetic is float32, y is rounded once."""
+    xt, rows, cols, ld = _matrix(x, "x")
+    w, wt = _param(weight, "weight", cols)
+    b, bt = _param(bias, "bias", cols)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _TYPE:
+        raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+    dev = _same_device(x, (x, "x"), (weight, "weight"), (bias, "bias"))
+    y = torch.empty(rows, cols, dtype=out_dtype, device=dev)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    _launch("mxq_layer_norm", dev, x.data_ptr(), rows, cols, ld, xt, w, wt, b, bt, eps, _TYPE[out_dtype], y.data_ptr(),
+            mean.data_ptr(), rstd.data_ptr())
+    return y, mean, rstd
+
+
+def mx_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  eps: float = 1e-5, fmt="e4m3", orientation="row", scale_mode="floor", sf_layout="canonical"):
+    """Layer norm of the rows of ``x`` straight to MX operands: (q_row, s_row,
+    q_col, s_col, mean, rstd), the first four as mx_quantize returns them for
+    the float32 y (no bf16 y is made).  Shapes and layouts as mx_quantize."""
+    f, o = _FMT[fmt], _ORIENT[orientation]
+    sm, sf = _SCALE[scale_mode], _SF[sf_layout]
+    xt, rows, cols, ld = _matrix(x, "x")
+    w, wt = _param(weight, "weight", cols)
+    b, bt = _param(bias, "bias", cols)
+    dev = _same_device(x, (x, "x"), (weight, "weight"), (bias, "bias"))
+    qb = 2 if f == E2M1 else 1
+    q_row = s_row = q_col = s_col = None
+    rp = rs = cp = cs = 0
+    if o & ROW:
+        q_row = torch.empty(rows, cols // qb, dtype=torch.uint8, device=dev)
+        s_row = torch.empty(rows, cols // 32, dtype=torch.uint8, device=dev)
+        rp, rs = q_row.data_ptr(), s_row.data_ptr()
+    if o & COL:
+        q_col = torch.empty(cols, rows // qb, dtype=torch.uint8, device=dev)
+        s_col = torch.empty(cols, rows // 32, dtype=torch.uint8, device=dev)
+        cp, cs = q_col.data_ptr(), s_col.data_ptr()
+    mean = torch.empty(rows, dtype=torch.float32, device=dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    _launch("mxq_layer_norm_mx", dev, x.data_ptr(), rows, cols, ld, xt, w, wt, b, bt, eps, f, o, sm, sf, rp, rs, cp, cs,
+            mean.data_ptr(), rstd.data_ptr())
+    return q_row, s_row, q_col, s_col, mean, rstd
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: Optional[torch.Tensor] = None, param_grads: bool = True):
+    """Backward pass of layer_norm (and of mx_layer_norm, for the gradient of
+    its y): (dx, dweight, dbias) from ``dy`` and the forward pass's ``x``,
+    ``mean``, ``rstd`` and ``weight``.  dx has x's type, dweight and dbias are
+    float32 [cols], or None without ``param_grads``."""
+    dt, _, _, ld_dy = _matrix(dy, "dy")
+    xt, rows, cols, ld = _matrix(x, "x")
+    if dy.shape != x.shape:
+        raise ValueError(f"dy is {tuple(dy.shape)}, x {tuple(x.shape)}")
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd are the forward pass's")
+    _vector(mean, "mean", rows, _F32_ONLY)
+    _vector(rstd, "rstd", rows, _F32_ONLY)
+    w, wt = _param(weight, "weight", cols)
+    dev = _same_device(x, (x, "x"), (dy, "dy"), (mean, "mean"), (rstd, "rstd"), (weight, "weight"))
+    dx = torch.empty(rows, cols, dtype=x.dtype, device=dev)
+    dw = db = None
+    wp = bp = 0
+    if param_grads:
+        dw = torch.empty(cols, dtype=torch.float32, device=dev)
+        db = torch.empty(cols, dtype=torch.float32, device=dev)
+        wp, bp = dw.data_ptr(), db.data_ptr()
+    need = _size("mxq_layer_norm_backward_workspace_size", dev, rows, cols)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _launch("mxq_layer_norm_backward", dev, dy.data_ptr(), ld_dy, dt, x.data_ptr(), ld, xt, rows, cols, mean.data_ptr(),
+            rstd.data_ptr(), w, wt, dx.data_ptr(), wp, bp, ws.data_ptr(), need)
+    return dx, dw, db
+
+
+def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
+                weights: torch.Tensor, ref_logp: Optional[torch.Tensor] = None, clip_low: float = 0.2,
+                clip_high: float = 0.2, beta: float = 0.0, grad_scale: float = 1.0,
+                grad_dtype: Optional[torch.dtype] = None, grad: bool = True):
+    """Clipped policy loss with a KL term over tokens, forward and backward
+    (mxq_policy_loss has the formula): (loss, logp, dlogits).
+
+    ``logits`` [tokens][vocab] bf16 or float32 (row stride may exceed vocab),
+    ``targets`` int64 or int32, the others float32, all [tokens].  The loss is
+    the sum of ``weights`` times the tokens' terms, so a mean over tokens or
+    over sequences is a choice of weights; a token of weight 0 is not read
+    (its target may be any padding value) and has logp 0 and gradient 0.
+    ``ref_logp`` is needed when ``beta`` is not 0.  dlogits, of ``grad_dtype``
+    (logits' type by default), is multiplied by ``grad_scale``; None without
+    ``grad``."""
+    zt, tokens, vocab, ld = _matrix(logits, "logits")
+    grad_dtype = logits.dtype if grad_dtype is None else grad_dtype
+    if grad_dtype not in _TYPE:
+        raise ValueError("grad_dtype must be torch.float32 or torch.bfloat16")
+    if not clip_low >= 0 or not clip_high >= 0:
+        raise ValueError("clip_low and clip_high must not be negative")
+    for t, name in ((targets, "targets"), (old_logp, "old_logp"), (advantages, "advantages"), (weights, "weights")):
+        if t is None:
+            raise ValueError(f"{name} is needed")
+    _vector(targets, "targets", tokens, (torch.int64, torch.int32))
+    _vector(old_logp, "old_logp", tokens, _F32_ONLY)
+    _vector(advantages, "advantages", tokens, _F32_ONLY)
+    _vector(weights, "weights", tokens, _F32_ONLY)
+    ref = 0
+    if ref_logp is not None:
+        _vector(ref_logp, "ref_logp", tokens, _F32_ONLY)
+        ref = ref_logp.data_ptr()
+    elif beta != 0:
+        raise ValueError("ref_logp is needed")
+    dev = _same_device(logits, (logits, "logits"), (targets, "targets"), (old_logp, "old_logp"),
+                       (advantages, "advantages"), (weights, "weights"), (ref_logp, "ref_logp"))
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    logp = torch.empty(tokens, dtype=torch.float32, device=dev)
+    dz = None
+    gp = 0
+    if grad:
+        dz = torch.empty(tokens, vocab, dtype=grad_dtype, device=dev)
+        gp = dz.data_ptr()
+    ws = _scratch(dev, _size("mxq_policy_loss_workspace_size", dev, tokens))
+    _launch("mxq_policy_loss", dev, logits.data_ptr(), tokens, vocab, ld, zt, targets.data_ptr(),
+            int(targets.dtype == torch.int64), old_logp.data_ptr(), advantages.data_ptr(), weights.data_ptr(), ref,
+            clip_low, clip_high, beta, grad_scale, loss.data_ptr(), logp.data_ptr(), gp, vocab, _TYPE[grad_dtype],
+            ws.data_ptr(), ws.numel())
+    return loss, logp, dz
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one stretch of memory, in some order of its axes."""
+    n = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
+        if stride != n:
+            return False
+        n *= size
+    return True
+
+
+def _grad_tensors(ts, what: str):
+    """Type codes of a list of gradient tensors, each filling its stretch of memory."""
+    types = []
+    for k, t in enumerate(ts):
+        code = _TYPE.get(t.dtype) if isinstance(t, torch.Tensor) else None
+        if code is None:
+            raise ValueError(f"{what}[{k}] must be a bf16 or float32 tensor")
+        if not t.is_contiguous() and not _dense(t):
+            raise ValueError(f"{what}[{k}] must fill its storage (contiguous, or a transpose of such)")
+        types.append(code)
+    return types
+
+
+def _grad_call(name: str, grads, out, *args) -> torch.Tensor:
+    """Check the lists and run entry point ``name`` on them: one mxq_grad per
+    tensor, written as four 64-bit words."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("at least one gradient tensor")
+    types = _grad_tensors(grads, "grads")
+    outs, out_types = grads, types
+    if out is not None:
+        outs = list(out)
+        if len(outs) != len(grads):
+            raise ValueError(f"{len(grads)} gradients, {len(outs)} outputs")
+        out_types = _grad_tensors(outs, "out")
+        for k, (g, o) in enumerate(zip(grads, outs)):
+            if o.shape != g.shape or not (g.is_contiguous() and o.is_contiguous() or g.stride() == o.stride()):
+                raise ValueError(f"out[{k}] must have the shape and strides of grads[{k}]")
+    dev, index = grads[0].device, grads[0].get_device()
+    for ts, what in ((grads, "grads"), (outs, "out")):
+        for k, t in enumerate(ts):
+            if t.get_device() != index or index < 0:
+                _on_device(((t, f"{what}[{k}]"),), dev)
+    words = array.array("q")
+    for g, o, gt, ot in zip(grads, outs, types, out_types):
+        words.extend((g.data_ptr(), o.data_ptr(), g.numel(), gt | ot << 32))
+    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    need = _size("mxq_grad_norm_workspace_size", dev, len(grads))
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _launch(name, dev, words.buffer_info()[0], len(grads), *args, norm.data_ptr(), ws.data_ptr(), need)
+    return norm
+
+
+def grad_norm(grads) -> torch.Tensor:
+    """The 2-norm of all elements of a list of bf16 and float32 tensors, as a
+    1-element float32 tensor."""
+    return _grad_call("mxq_grad_norm", grads, None)
+
+
+def clip_grad_norm(grads, max_norm: float, out=None) -> torch.Tensor:
+    """Scale ``grads`` by min(1, max_norm / (norm + 1e-6)), norm being their
+    global 2-norm, which is returned (1-element float32, nothing is read back
+    to the host).  In place, or into the tensors of ``out`` (same shapes,
+    bf16 or float32, e.g. an optimizer's float32 buffers)."""
+    if not max_norm >= 0:
+        raise ValueError("max_norm must not be negative")
+    return _grad_call("mxq_clip_grad_norm", grads, out, max_norm)
 
 
 def sf_to_mma(s: torch.Tensor) -> torch.Tensor:

@@ -1,0 +1,300 @@
+// Global 2-norm over a list of tensors, and clipping by it:
+//   n = sqrt(sum g^2),  c = min(1, max_norm / (n + 1e-6)),  out = c g.
+//
+// The tensors are cut into chunks that a persistent grid walks through; the
+// list travels in the kernel's parameters, so nothing is copied to the device
+// and nothing is kept between calls.  Both kernels are bound by HBM: the norm
+// reads every element once, the scaling reads and writes it once.
+#include <algorithm>
+
+#include "rowops.cuh"
+
+namespace mxq {
+namespace {
+
+constexpr int TPB = 256;
+constexpr int TABLE_SMALL = 64, TABLE_LARGE = 512;   // tensors of one launch (2 KiB, 16 KiB of parameters)
+
+struct Entry {
+  const void* g;
+  void* out;
+  int64_t n;
+  uint32_t first;          // its first chunk in the launch
+  int16_t g_f32, out_f32;
+};
+
+template <int N>
+struct Table {
+  Entry e[N];
+  int count;
+  uint32_t chunks;
+  int chunk;               // elements (a multiple of 8)
+};
+
+template <int N>
+__device__ __forceinline__ int entry_of(const Table<N>& t, uint32_t c) {
+  int lo = 0, hi = t.count - 1;                      // the last entry with first <= c
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.e[mid].first <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A thread's sum of squares.  Squares of ordinary values add up in float32
+// over a batch and in float64 across batches; a batch whose largest value
+// lies outside 2^-50 .. 2^50 (its square could overflow or vanish in float32)
+// or is not finite is squared in float64.
+template <int N>
+__device__ __forceinline__ void add_squares(const float (&v)[N], double& acc) {
+  float m = 0.f, q[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    m = fmax3_nan(m, fabsf(v[i]), 0.f);
+    q[i] = v[i] * v[i];
+  }
+  if ((m >= 0x1p-50f && m <= 0x1p50f) || m == 0.f) {
+    acc += static_cast<double>(tree_sum(q));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc += static_cast<double>(v[i]) * static_cast<double>(v[i]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void squares_of(const T* p, int len, double& acc) {
+  constexpr int VE = 16 / static_cast<int>(sizeof(T));
+  constexpr int U = 4;                               // vectors in flight
+  int done = 0;
+  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    const int nvec = len / VE;
+    for (int i = threadIdx.x; i < nvec; i += TPB * U) {
+      Vec<T, VE> r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        r[u].fill(0);
+        if (i + u * TPB < nvec) r[u].load(p + (i + u * TPB) * VE);
+      }
+      float v[U * VE];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[u * VE + j] = r[u].get(j);
+      add_squares(v, acc);
+    }
+    done = nvec * VE;
+  }
+  for (int i = done + threadIdx.x; i < len; i += TPB) {
+    Vec<T, 1> r;
+    r.load(p + i);
+    const float v[1] = {r.get(0)};
+    add_squares(v, acc);
+  }
+}
+
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double red[TPB / 32];
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = red[0];
+#pragma unroll
+  for (int i = 1; i < TPB / 32; ++i) s += red[i];
+  return s;
+}
+
+template <int N>
+__global__ void __launch_bounds__(TPB) square_sum_kernel(const __grid_constant__ Table<N> t, double* part) {
+  grid_dep_wait();
+  double acc = 0.0;
+  for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const Entry& e = t.e[entry_of(t, c)];
+    const int64_t off = static_cast<int64_t>(c - e.first) * t.chunk;
+    const int len = static_cast<int>(min(static_cast<int64_t>(t.chunk), e.n - off));
+    if (e.g_f32) squares_of(static_cast<const float*>(e.g) + off, len, acc);
+    else squares_of(static_cast<const __nv_bfloat16*>(e.g) + off, len, acc);
+  }
+  const double s = block_sum(acc);
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+// The sum of all parts in a fixed order, the same in every CTA.
+__device__ __forceinline__ float norm_of(const double* part, int parts) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < parts; i += TPB) s += part[i];
+  return static_cast<float>(sqrt(block_sum(s)));
+}
+
+__global__ void __launch_bounds__(TPB) norm_kernel(const double* part, int parts, float* norm) {
+  grid_dep_wait();
+  const float n = norm_of(part, parts);
+  if (threadIdx.x == 0) norm[0] = n;
+}
+
+template <typename TI, typename TO>
+__device__ __forceinline__ void scale_of(const TI* p, TO* o, int len, float c) {
+  constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
+  constexpr int U = 4;
+  int done = 0;
+  if ((reinterpret_cast<uintptr_t>(p) & (VE * sizeof(TI) - 1)) == 0 &&
+      (reinterpret_cast<uintptr_t>(o) & 15 & (VE * sizeof(TO) - 1)) == 0) {
+    const int nvec = len / VE;
+    for (int i = threadIdx.x; i < nvec; i += TPB * U) {
+      Vec<TI, VE> r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u * TPB < nvec) r[u].load(p + (i + u * TPB) * VE);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i + u * TPB >= nvec) continue;
+        float v[VE];
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[j] = r[u].get(j) * c;
+        store_vec<TO, VE>(o + (i + u * TPB) * VE, v);
+      }
+    }
+    done = nvec * VE;
+  }
+  for (int i = done + threadIdx.x; i < len; i += TPB) {
+    Vec<TI, 1> r;
+    r.load(p + i);
+    const float v[1] = {r.get(0) * c};
+    store_vec<TO, 1>(o + i, v);
+  }
+}
+
+// Every CTA derives the factor from the parts, then scales its chunks, last
+// first: the chunks that the norm kernel read last are still in L2.
+template <int N>
+__global__ void __launch_bounds__(TPB) scale_kernel(const __grid_constant__ Table<N> t, const double* part, int parts,
+                                                    float max_norm, float* norm) {
+  grid_dep_wait();
+  const float n = norm_of(part, parts);
+  if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = n;
+  float c = max_norm / (n + 1e-6f);
+  if (c > 1.f) c = 1.f;                              // a NaN norm stays NaN
+  for (uint32_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
+    const uint32_t ch = t.chunks - 1 - k;
+    const Entry& e = t.e[entry_of(t, ch)];
+    if (c == 1.f && e.g == e.out) continue;          // in place and nothing to change
+    const int64_t off = static_cast<int64_t>(ch - e.first) * t.chunk;
+    const int len = static_cast<int>(min(static_cast<int64_t>(t.chunk), e.n - off));
+    const float* gf = static_cast<const float*>(e.g) + off;
+    const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(e.g) + off;
+    float* of = static_cast<float*>(e.out) + off;
+    __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(e.out) + off;
+    if (e.g_f32) {
+      if (e.out_f32) scale_of(gf, of, len, c);
+      else scale_of(gf, ob, len, c);
+    } else {
+      if (e.out_f32) scale_of(gb, of, len, c);
+      else scale_of(gb, ob, len, c);
+    }
+  }
+}
+
+using namespace mxq_host;
+
+int grid_limit() { return 4 * sm_count(); }
+
+int check_grads(const mxq_grad* g, int n, bool clip) {
+  if (n < 0 || (n && !g)) return MXQ_ERR_BAD_ARG;
+  for (int i = 0; i < n; ++i) {
+    if (g[i].n < 0 || g[i].n > (1ll << 42)) return MXQ_ERR_BAD_SHAPE;
+    if (g[i].g_type != MXQ_BF16 && g[i].g_type != MXQ_F32) return MXQ_ERR_BAD_ARG;
+    if (clip && g[i].out_type != MXQ_BF16 && g[i].out_type != MXQ_F32) return MXQ_ERR_BAD_ARG;
+    if (!g[i].n) continue;
+    if (!g[i].g || (clip && !g[i].out)) return MXQ_ERR_BAD_ARG;
+    if (clip && g[i].g == g[i].out && g[i].g_type != g[i].out_type) return MXQ_ERR_BAD_ARG;
+    if (reinterpret_cast<uintptr_t>(g[i].g) & (g[i].g_type == MXQ_F32 ? 3 : 1)) return MXQ_ERR_MISALIGNED;
+    if (clip && (reinterpret_cast<uintptr_t>(g[i].out) & (g[i].out_type == MXQ_F32 ? 3 : 1))) return MXQ_ERR_MISALIGNED;
+  }
+  return MXQ_OK;
+}
+
+// Elements of a chunk: enough chunks for every CTA to have several, 2048 (one
+// round of a CTA's loads) to 16384.
+int chunk_size(int64_t total) {
+  const int64_t want = total / (4ll * grid_limit());
+  return want >= 16384 ? 16384 : want >= 8192 ? 8192 : want >= 4096 ? 4096 : 2048;
+}
+
+// Fills t with entries from *i on, as many as fit; false when none is left.
+template <int N>
+bool next_table(const mxq_grad* g, int n, int chunk, int* i, Table<N>& t) {
+  t.count = 0;
+  t.chunks = 0;
+  t.chunk = chunk;
+  for (; *i < n && t.count < N; ++*i) {
+    const mxq_grad& s = g[*i];
+    if (!s.n) continue;
+    const int64_t c = (s.n + chunk - 1) / chunk;
+    if (t.chunks + c > 0x7FFFFFFF) break;
+    t.e[t.count++] = Entry{s.g, s.out, s.n, t.chunks, static_cast<int16_t>(s.g_type == MXQ_F32),
+                           static_cast<int16_t>(s.out_type == MXQ_F32)};
+    t.chunks += static_cast<uint32_t>(c);
+  }
+  return t.count > 0;
+}
+
+template <int N>
+int run(const mxq_grad* g, int n, int64_t total, bool clip, float max_norm, float* norm, double* part, cudaStream_t st) {
+  const int chunk = chunk_size(total);
+  Table<N> t;
+  int parts = 0;
+  for (int i = 0; next_table(g, n, chunk, &i, t);) {
+    const int grid = static_cast<int>(std::min<int64_t>(t.chunks, grid_limit()));
+    const int rc = launch_pdl(square_sum_kernel<N>, dim3(grid), dim3(TPB), 0, st, t, part + parts);
+    if (rc) return rc;
+    parts += grid;
+  }
+  if (!clip || !parts)
+    return launch_pdl(norm_kernel, dim3(1), dim3(TPB), 0, st, static_cast<const double*>(part), parts, norm);
+  for (int i = 0; next_table(g, n, chunk, &i, t);) {
+    const int grid = static_cast<int>(std::min<int64_t>(t.chunks, grid_limit()));
+    const int rc = launch_pdl(scale_kernel<N>, dim3(grid), dim3(TPB), 0, st, t, static_cast<const double*>(part), parts,
+                              max_norm, norm);
+    if (rc) return rc;
+  }
+  return MXQ_OK;
+}
+
+int grad_call(const mxq_grad* g, int n, bool clip, float max_norm, float* norm, void* ws, size_t bytes, void* stream) {
+  if (!norm) return MXQ_ERR_BAD_ARG;
+  const int rc = check_grads(g, n, clip);
+  if (rc) return rc;
+  if (clip && !(max_norm >= 0.f)) return MXQ_ERR_BAD_ARG;
+  size_t need = 0;
+  mxq_grad_norm_workspace_size(n, &need);
+  if (!ws || bytes < need) return MXQ_ERR_BAD_ARG;
+  if ((reinterpret_cast<uintptr_t>(norm) & 3) || !aligned16(ws)) return MXQ_ERR_MISALIGNED;
+  if (!device_ok()) return MXQ_ERR_UNSUPPORTED;
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) total += g[i].n;
+  const auto st = static_cast<cudaStream_t>(stream);
+  double* part = static_cast<double*>(ws);
+  return n <= TABLE_SMALL ? run<TABLE_SMALL>(g, n, total, clip, max_norm, norm, part, st)
+                          : run<TABLE_LARGE>(g, n, total, clip, max_norm, norm, part, st);
+}
+
+}  // namespace
+}  // namespace mxq
+
+extern "C" int mxq_grad_norm_workspace_size(int ntensors, size_t* bytes) {
+  if (!bytes || ntensors < 0) return MXQ_ERR_BAD_ARG;
+  // every launch fills its table up, short of a list of more than 2^31 chunks
+  const size_t launches = static_cast<size_t>(ntensors) / mxq::TABLE_LARGE + 2;
+  *bytes = launches * mxq::grid_limit() * sizeof(double);
+  return MXQ_OK;
+}
+
+extern "C" int mxq_grad_norm(const mxq_grad* grads, int ntensors, float* norm, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  return mxq::grad_call(grads, ntensors, false, 0.f, norm, workspace, workspace_bytes, stream);
+}
+
+extern "C" int mxq_clip_grad_norm(const mxq_grad* grads, int ntensors, float max_norm, float* norm, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  return mxq::grad_call(grads, ntensors, true, max_norm, norm, workspace, workspace_bytes, stream);
+}

@@ -1,0 +1,353 @@
+// Clipped policy loss with a KL term, from logits: the loss, the tokens'
+// log-probabilities and the gradient of the logits in one pass over them.
+//
+//   lp = z_a - lse(z),  r = exp(lp - old),  u = min(r A, clip(r, 1-lo, 1+hi) A)
+//   k3 = exp(ref - lp) - (ref - lp) - 1,    l = -u + beta k3,  loss = sum w l
+//   dl/dlp = -A r [r A <= clip(r) A] + beta (1 - exp(ref - lp))
+//   dz_v = scale w dl/dlp ([v == a] - exp(z_v - lse))
+//
+// A row's exponentials stay in the registers of one CTA, or of a cluster of
+// up to eight CTAs, so the logits are read once and the gradient is written
+// once: HBM bounds it (one exponential per element).  A warp takes its own
+// maximum m_w and keeps e_v = exp(z_v - m_w); the pairs (m_w, sum e_v) of all
+// warps go to every CTA of the cluster, and p_v = e_v exp(m_w - lse) needs no
+// second exponential.
+#include <algorithm>
+
+#include "rowops.cuh"
+
+namespace mxq {
+namespace {
+
+constexpr int TPB = 512;                 // threads of a CTA
+constexpr int WPB = TPB / 32;
+constexpr int MAX_SLABS = 8;             // CTAs of a cluster (the portable limit)
+constexpr int MAX_E = 32;                // elements of a thread
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct LossArgs {
+  const void* z;
+  int64_t ld_z;
+  void* g;                               // NULL: no gradient
+  int64_t ld_g;
+  const void* targets;
+  int targets64;
+  const float *old_lp, *adv, *weights, *ref_lp;
+  float lo, hi, beta, scale;
+  int tokens, vocab;
+  float* logp;
+  float* terms;                          // [tokens] w * l, summed by the last CTA
+  float* loss;
+  unsigned* ticket;                      // 0 on entry, left 0
+};
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// exp(v - m) for m a maximum: the difference first, so that its rounding is
+// relative to the distance from the maximum and not to the logits' size.
+__device__ __forceinline__ float exp_rel(float v, float m) { return ex2((v - m) * kLog2e); }
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+
+// Elements [e0, e0 + VE) of a row of V, where only those in [0, V) exist; the
+// others are -inf.  Whole vectors go as one aligned load.
+template <typename T, int VE>
+__device__ __forceinline__ void load_edge(const T* row, int e0, int V, float (&v)[VE]) {
+  if (e0 >= 0 && e0 + VE <= V) {
+    Vec<T, VE> r;
+    r.load(row + e0);
+#pragma unroll
+    for (int j = 0; j < VE; ++j) v[j] = r.get(j);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      v[j] = -INFINITY;
+      if (e0 + j >= 0 && e0 + j < V) {
+        Vec<T, 1> r;
+        r.load(row + e0 + j);
+        v[j] = r.get(0);
+      }
+    }
+  }
+}
+
+template <typename T, int VE>
+__device__ __forceinline__ void store_edge(T* row, int e0, int V, const float (&v)[VE]) {
+  if (e0 >= 0 && e0 + VE <= V) store_vec<T, VE>(row + e0, v);
+  else
+#pragma unroll
+    for (int j = 0; j < VE; ++j)
+      if (e0 + j >= 0 && e0 + j < V) {
+        const float one[1] = {v[j]};
+        store_vec<T, 1>(row + e0 + j, one);
+      }
+}
+
+// Loss term and its slope dl/dlp of one token.
+__device__ __forceinline__ void token_loss(const LossArgs& a, int64_t row, float lp, float& l, float& slope) {
+  const float A = a.adv[row];
+  const float r = expf(lp - a.old_lp[row]);
+  const float ra = r * A, ca = fminf(fmaxf(r, 1.f - a.lo), 1.f + a.hi) * A;
+  const float nan = __int_as_float(0x7FFFFFFF);
+  l = ra <= ca ? -ra : (ca < ra ? -ca : nan);
+  slope = lp != lp ? nan : (ra <= ca ? -ra : 0.f);
+  if (a.beta != 0.f) {
+    const float d = a.ref_lp[row] - lp;
+    const float x = expm1f(d);
+    l += a.beta * (x - d);
+    slope -= a.beta * x;
+  }
+}
+
+// The last CTA to finish adds the tokens' terms in their order per thread and
+// the threads' sums in a fixed tree, in float64.
+__device__ __forceinline__ void finish_loss(const LossArgs& a, unsigned ctas) {
+  __shared__ unsigned last;
+  __shared__ double sums[WPB];
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) == ctas - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double s = 0.0;
+  for (int i = threadIdx.x; i < a.tokens; i += TPB) s += static_cast<double>(__ldcg(a.terms + i));
+  s = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < WPB; ++i) s += sums[i];
+    a.loss[0] = static_cast<float>(s);
+    *a.ticket = 0;
+  }
+}
+
+// `slabs` CTAs (one cluster) per token; a thread holds NV vectors of VE
+// elements.  Vectors start at the row's first 16-byte boundary at or before
+// its first element, `h` elements ahead of it, so rows of odd length still
+// move in whole words; only the first and the last vector are ragged.
+// LONG: rows beyond the registers of a cluster; two passes, the second from
+// L2.
+template <typename TZ, typename TG, int VE, int NV, bool LONG>
+__global__ void __launch_bounds__(TPB, 2) policy_kernel(const LossArgs a, int slabs) {
+  __shared__ float2 pairs[MAX_SLABS * WPB];
+  cluster_arrive();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = blockIdx.x % slabs;
+  const int64_t row = blockIdx.x / slabs;
+  const TZ* z = static_cast<const TZ*>(a.z) + row * a.ld_z;
+  TG* g = a.g ? static_cast<TG*>(a.g) + row * a.ld_g : nullptr;
+  const int V = a.vocab;
+  const int h = static_cast<int>((reinterpret_cast<uintptr_t>(z) / sizeof(TZ)) % VE);
+  const int nvec = (V + h + VE - 1) / VE;
+  const float wt = a.weights[row];
+
+  if (wt == 0.f) {                       // nothing of the row is read
+    const float zero[VE] = {};
+    if (g)
+      for (int i = rank * TPB + threadIdx.x; i < nvec; i += slabs * TPB) store_edge<TG, VE>(g, i * VE - h, V, zero);
+    if (rank == 0 && threadIdx.x == 0) {
+      a.logp[row] = 0.f;
+      a.terms[row] = 0.f;
+    }
+    cluster_wait();
+  } else {
+    const int64_t target = a.targets64 ? static_cast<const int64_t*>(a.targets)[row]
+                                       : static_cast<int64_t>(static_cast<const int*>(a.targets)[row]);
+    const bool inside = target >= 0 && target < V;
+    float za = __int_as_float(0x7FFFFFFF);
+    if (inside) {
+      Vec<TZ, 1> t;
+      t.load(z + target);
+      za = t.get(0);
+    }
+    const int first = LONG ? rank * TPB + threadIdx.x : rank * TPB * NV + threadIdx.x;
+    float e[NV][VE];
+    float m = -INFINITY, s = 0.f;
+    if constexpr (LONG) {
+      for (int i = first; i < nvec; i += slabs * TPB) {
+        float v[VE];
+        load_edge<TZ, VE>(z, i * VE - h, V, v);
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) top = fmaxf(top, v[j]);
+        const float ms = top == -INFINITY ? 0.f : top;
+        s *= exp_rel(m, ms);
+        m = top;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) s += exp_rel(v[j], ms);
+      }
+      const float top = warp_max(m);
+      s = warp_sum(s * exp_rel(m, top == -INFINITY ? 0.f : top));
+      m = top;
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (first + k * TPB < nvec) load_edge<TZ, VE>(z, (first + k * TPB) * VE - h, V, e[k]);
+        else
+#pragma unroll
+          for (int j = 0; j < VE; ++j) e[k][j] = -INFINITY;
+      }
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) m = fmaxf(m, e[k][j]);
+      m = warp_max(m);
+      const float ms = m == -INFINITY ? 0.f : m;
+      float part[NV];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) e[k][j] = exp_rel(e[k][j], ms);
+        part[k] = tree_sum(e[k]);
+      }
+      s = warp_sum(tree_sum(part));
+    }
+    cluster_wait();                      // every CTA of the cluster has started
+    if (lane < slabs) st_cluster_f2(smem_u32(&pairs[rank * WPB + warp]), lane, m, s);
+    cluster_sync();
+    float top = -INFINITY;
+    for (int i = lane; i < slabs * WPB; i += 32) top = fmaxf(top, pairs[i].x);
+    top = warp_max(top);
+    float total = 0.f;
+    for (int i = lane; i < slabs * WPB; i += 32) total += pairs[i].y * exp_rel(pairs[i].x, top);
+    total = warp_sum(total);
+    const float lp = (za - top) - logf(total);
+    float l, slope;
+    token_loss(a, row, lp, l, slope);
+    if (rank == 0 && threadIdx.x == 0) {
+      a.logp[row] = lp;
+      a.terms[row] = wt * l;
+    }
+    if (g) {
+      const float k = a.scale * wt * slope;
+      const int at = inside ? static_cast<int>(target) : -VE;
+      if constexpr (LONG) {
+        const float f = -k / total;
+        for (int i = first; i < nvec; i += slabs * TPB) {
+          const int e0 = i * VE - h;
+          float v[VE];
+          load_edge<TZ, VE>(z, e0, V, v);
+#pragma unroll
+          for (int j = 0; j < VE; ++j) v[j] = fmaf(exp_rel(v[j], top), f, e0 + j == at ? k : 0.f);
+          store_edge<TG, VE>(g, e0, V, v);
+        }
+      } else {
+        // this warp's exponentials are relative to m
+        const float f = -k * (exp_rel(m, top) / total);
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+          if (first + q * TPB >= nvec) continue;
+          const int e0 = (first + q * TPB) * VE - h;
+          float o[VE];
+#pragma unroll
+          for (int j = 0; j < VE; ++j) o[j] = fmaf(e[q][j], f, e0 + j == at ? k : 0.f);
+          store_edge<TG, VE>(g, e0, V, o);
+        }
+      }
+    }
+  }
+  if (rank == 0) finish_loss(a, a.tokens);
+}
+
+using namespace mxq_host;
+
+bool valid_type(int t) { return t == MXQ_BF16 || t == MXQ_F32; }
+int type_size(int t) { return t == MXQ_F32 ? 4 : 2; }
+bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+template <typename TZ, typename TG, int VE, int NV, bool LONG>
+int launch_policy(const LossArgs& a, int slabs, cudaStream_t st) {
+  const int64_t grid = static_cast<int64_t>(a.tokens) * slabs;
+  if (grid > 0x7FFFFFFF) return MXQ_ERR_BAD_SHAPE;
+  return launch_pdl_cluster(policy_kernel<TZ, TG, VE, NV, LONG>, dim3(static_cast<unsigned>(grid)), dim3(TPB), 0, st,
+                            slabs, a, slabs);
+}
+
+// The fewest CTAs whose registers hold a row; with few tokens more, until
+// there are two CTAs for every SM or eight to a row.
+template <typename TZ, typename TG, int VE>
+int dispatch_policy(const LossArgs& a, cudaStream_t st) {
+  constexpr int NMAX = MAX_E / VE;
+  // the words of a row, whatever its shift
+  const bool flush = a.ld_z % VE == 0 && reinterpret_cast<uintptr_t>(a.z) / sizeof(TZ) % VE == 0;
+  const int64_t nvec = (static_cast<int64_t>(a.vocab) + (flush ? 0 : VE - 1) + VE - 1) / VE;
+  int slabs = static_cast<int>(std::min<int64_t>((nvec + TPB * NMAX - 1) / (TPB * NMAX), MAX_SLABS + 1));
+  if (slabs > MAX_SLABS) return launch_policy<TZ, TG, VE, 1, true>(a, MAX_SLABS, st);
+  while (slabs < MAX_SLABS && static_cast<int64_t>(a.tokens) * slabs < 2 * sm_count() && nvec > TPB * slabs)
+    slabs = std::min(MAX_SLABS, 2 * slabs);
+  const int64_t nv = (nvec + static_cast<int64_t>(TPB) * slabs - 1) / (static_cast<int64_t>(TPB) * slabs);
+  if (nv <= NMAX / 4) return launch_policy<TZ, TG, VE, NMAX / 4, false>(a, slabs, st);
+  if (nv <= NMAX / 2) return launch_policy<TZ, TG, VE, NMAX / 2, false>(a, slabs, st);
+  return launch_policy<TZ, TG, VE, NMAX, false>(a, slabs, st);
+}
+
+template <typename TZ, typename TG>
+int policy(const LossArgs& a, cudaStream_t st) {
+  constexpr int VE = sizeof(TZ) == 2 && sizeof(TG) == 2 ? 8 : 4;
+  // whole words on both sides: every row of the gradient starts at the same
+  // element of its VE-element word as the row of logits
+  const bool same = !a.g || ((a.ld_z - a.ld_g) % VE == 0 &&
+                             (reinterpret_cast<uintptr_t>(a.z) / sizeof(TZ)) % VE ==
+                                 (reinterpret_cast<uintptr_t>(a.g) / sizeof(TG)) % VE);
+  return same ? dispatch_policy<TZ, TG, VE>(a, st) : dispatch_policy<TZ, TG, 1>(a, st);
+}
+
+}  // namespace
+}  // namespace mxq
+
+using namespace mxq;
+using namespace mxq_host;
+
+extern "C" int mxq_policy_loss_workspace_size(int64_t tokens, size_t* bytes) {
+  if (!bytes) return MXQ_ERR_BAD_ARG;
+  if (tokens < 0) return MXQ_ERR_BAD_SHAPE;
+  *bytes = 256 + static_cast<size_t>(tokens) * sizeof(float);
+  return MXQ_OK;
+}
+
+extern "C" int mxq_policy_loss(const void* logits, int64_t tokens, int64_t vocab, int64_t ld, int logits_type,
+                               const void* targets, int targets_64, const float* old_logp, const float* advantages,
+                               const float* weights, const float* ref_logp, float clip_low, float clip_high,
+                               float beta, float grad_scale, float* loss, float* logp, void* grad, int64_t ld_grad,
+                               int grad_type, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_type(logits_type) || (grad && !valid_type(grad_type))) return MXQ_ERR_BAD_ARG;
+  if ((targets_64 != 0 && targets_64 != 1) || !loss) return MXQ_ERR_BAD_ARG;
+  if (tokens < 0 || vocab < 1 || ld < vocab || (grad && ld_grad < vocab)) return MXQ_ERR_BAD_SHAPE;
+  if (tokens > 0x7FFFFFFFll / MAX_SLABS || vocab > 0x7FFFFF00ll) return MXQ_ERR_BAD_SHAPE;
+  if (tokens && (!logits || !targets || !old_logp || !advantages || !weights || !logp)) return MXQ_ERR_BAD_ARG;
+  if (tokens && beta != 0.f && !ref_logp) return MXQ_ERR_BAD_ARG;
+  if (!(clip_low >= 0.f) || !(clip_high >= 0.f)) return MXQ_ERR_BAD_ARG;
+  size_t need = 0;
+  mxq_policy_loss_workspace_size(tokens, &need);
+  if (!workspace || workspace_bytes < need) return MXQ_ERR_BAD_ARG;
+  if (!aligned_to(logits, type_size(logits_type)) || !aligned_to(targets, targets_64 ? 8 : 4) ||
+      !aligned_to(old_logp, 4) || !aligned_to(advantages, 4) || !aligned_to(weights, 4) || !aligned_to(ref_logp, 4) ||
+      !aligned_to(loss, 4) || !aligned_to(logp, 4) || (grad && !aligned_to(grad, type_size(grad_type))) ||
+      !aligned16(workspace))
+    return MXQ_ERR_MISALIGNED;
+  if (!device_ok()) return MXQ_ERR_UNSUPPORTED;
+  const auto st = static_cast<cudaStream_t>(stream);
+  if (!tokens) return cudaMemsetAsync(loss, 0, sizeof(float), st) == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+  LossArgs a{};
+  a.z = logits, a.ld_z = ld, a.g = grad, a.ld_g = ld_grad;
+  a.targets = targets, a.targets64 = targets_64;
+  a.old_lp = old_logp, a.adv = advantages, a.weights = weights, a.ref_lp = ref_logp;
+  a.lo = clip_low, a.hi = clip_high, a.beta = beta, a.scale = grad_scale;
+  a.tokens = static_cast<int>(tokens), a.vocab = static_cast<int>(vocab);
+  a.logp = logp, a.loss = loss;
+  a.ticket = static_cast<unsigned*>(workspace);
+  a.terms = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+  using bf16 = __nv_bfloat16;
+  if (logits_type == MXQ_BF16)
+    return grad && grad_type == MXQ_F32 ? policy<bf16, float>(a, st) : policy<bf16, bf16>(a, st);
+  return grad && grad_type == MXQ_BF16 ? policy<float, bf16>(a, st) : policy<float, float>(a, st);
+}

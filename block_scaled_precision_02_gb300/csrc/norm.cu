@@ -1,0 +1,896 @@
+// Layer norm over the rows of a matrix: y = (x - mean) * rstd * w + b, as
+// bf16 / float32 or straight to MX codes and scales, and its backward pass
+// with the reduction of the weight's and bias's gradients.
+//
+// Statistics are float32 and come from the data held in registers: partial
+// means and sums of squared deviations merge as
+//   M2(A+B) = M2(A) + M2(B) + n_A (mean_A - mean)^2 + n_B (mean_B - mean)^2,
+// which does not cancel when the mean is large against the spread.
+#include <algorithm>
+
+#include "rowops.cuh"
+
+namespace mxq {
+namespace {
+
+// What a row kernel writes: bf16 or float32 rows, or MX codes of a format.
+constexpr int OUT_BF16 = -2, OUT_F32 = -1;
+
+struct NormArgs {
+  const void* x;
+  int64_t ld;
+  int rows, cols;
+  const void* w;          // [cols] or NULL (1)
+  const void* b;          // [cols] or NULL (0)
+  int w_f32, b_f32;
+  float eps;
+  void* y;                // row outputs; NULL: statistics only
+  float* mean;
+  float* rstd;
+  uint8_t *q_row, *s_row, *q_col, *s_col;
+  int ceil_mode, mma, pack_row;   // pack_row: the scales of four blocks go as one word
+};
+
+__device__ __forceinline__ float norm_value(float x, float mean, float rstd, float w, float b) {
+  return __fmaf_rn(__fmul_rn(__fsub_rn(x, mean), rstd), w, b);
+}
+
+template <int VE>
+__device__ __forceinline__ void load_affine(const NormArgs& a, int at, float (&w)[VE], float (&b)[VE]) {
+  if (a.w) load_param<VE>(a.w, a.w_f32, at, w);
+  else
+#pragma unroll
+    for (int j = 0; j < VE; ++j) w[j] = 1.f;
+  if (a.b) load_param<VE>(a.b, a.b_f32, at, b);
+  else
+#pragma unroll
+    for (int j = 0; j < VE; ++j) b[j] = 0.f;
+}
+
+// Elements of a row of `cols` that warp w of a group of G threads holds, when
+// thread t holds the vectors k*G + t.
+template <int VE, int NV>
+__device__ __forceinline__ int warp_count(int cols, int G, int w) {
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) n += max(0, min(32 * VE, cols - (k * G + 32 * w) * VE));
+  return n;
+}
+
+// Sum of squared deviations of a thread's valid vectors from m.
+template <int VE, int NV>
+__device__ __forceinline__ float sq_dev(const float (&v)[NV][VE], float m, int t, int G, int nvec) {
+  float s[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    float d[VE];
+#pragma unroll
+    for (int j = 0; j < VE; ++j) d[j] = (v[k][j] - m) * (v[k][j] - m);
+    s[k] = k * G + t < nvec ? tree_sum(d) : 0.f;
+  }
+  return tree_sum(s);
+}
+
+// One row per warp (WARP: eight rows per CTA, no barrier) or per CTA (one
+// barrier); the row stays in registers, VE * NV elements per thread, so x is
+// read once and y written once: HBM bounds it.
+template <typename TX, int OUT, int VE, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 1024) norm_row_kernel(const NormArgs a) {
+  __shared__ float2 part[32];
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = WARP ? 32 : blockDim.x, t = WARP ? lane : threadIdx.x;
+  const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
+  if (WARP && row >= a.rows) return;
+  const int nvec = a.cols / VE;
+  const TX* x = static_cast<const TX*>(a.x) + row * a.ld;
+
+  float v[NV][VE];
+  {
+    Vec<TX, VE> raw[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      raw[k].fill(0);
+      if (k * G + t < nvec) raw[k].load(x + (k * G + t) * VE);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int j = 0; j < VE; ++j) v[k][j] = raw[k].get(j);
+  }
+
+  float s[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) s[k] = tree_sum(v[k]);
+  float sum = warp_sum(tree_sum(s));
+  const float inv_c = 1.f / static_cast<float>(a.cols);
+  float mean, m2;
+  if constexpr (WARP) {
+    mean = sum * inv_c;
+    m2 = warp_sum(sq_dev<VE, NV>(v, mean, t, G, nvec));
+  } else {
+    const int n = warp_count<VE, NV>(a.cols, G, warp);
+    m2 = warp_sum(sq_dev<VE, NV>(v, n ? sum / static_cast<float>(n) : 0.f, t, G, nvec));
+    if (lane == 0) part[warp] = make_float2(sum, m2);
+    __syncthreads();
+    const bool have = lane < (G >> 5);
+    const float2 pw = have ? part[lane] : make_float2(0.f, 0.f);
+    const int nw = have ? warp_count<VE, NV>(a.cols, G, lane) : 0;
+    mean = warp_sum(pw.x) * inv_c;
+    const float d = nw ? pw.x / static_cast<float>(nw) - mean : 0.f;
+    m2 = warp_sum(pw.y + static_cast<float>(nw) * d * d);
+  }
+  const float rstd = 1.f / sqrtf(m2 * inv_c + a.eps);
+  if (t == 0) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
+
+  if constexpr (OUT < 0) {
+    using TY = typename std::conditional<OUT == OUT_F32, float, __nv_bfloat16>::type;
+    if (!a.y) return;
+    TY* y = static_cast<TY*>(a.y) + row * a.cols;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int at = (k * G + t) * VE;
+      if (at >= nvec * VE) continue;
+      float w[VE], b[VE], o[VE];
+      load_affine<VE>(a, at, w, b);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) o[j] = norm_value(v[k][j], mean, rstd, w[j], b[j]);
+      store_vec<TY, VE>(y + at, o);
+    }
+  } else {
+    // 32 / VE neighbouring lanes hold a block; its amax by shuffles
+    constexpr int LPB = 32 / VE;
+    constexpr int QW = code_words<OUT, VE>();
+    const int kb = a.cols / 32;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int at = (k * G + t) * VE;
+      const bool valid = at < a.cols;
+      float o[VE];
+      float m = 0.f;
+      if (valid) {
+        float w[VE], b[VE];
+        load_affine<VE>(a, at, w, b);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          o[j] = norm_value(v[k][j], mean, rstd, w[j], b[j]);
+          m = fmax3_nan(m, fabsf(o[j]), 0.f);
+        }
+      }
+#pragma unroll
+      for (int i = 1; i < LPB; i <<= 1) m = fmax3_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, i), 0.f);
+      const uint32_t ab = __float_as_uint(m) & 0x7FFFFFFFu;
+      float mult;
+      const uint32_t code = mx_scale<OUT>(ab, a.ceil_mode, mult);
+      if (valid) {
+        uint32_t q[QW];
+        mx_codes<OUT, VE>(o, mult, code == 0xFFu, q);
+        uint8_t* dst = a.q_row + (OUT == MXQ_E2M1 ? (row * a.cols + at) / 2 : row * a.cols + at);
+        if constexpr (OUT == MXQ_E2M1 && VE == 4) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(q[0]);
+        else if constexpr (QW == 1) *reinterpret_cast<uint32_t*>(dst) = q[0];
+        else *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+      }
+      if (a.pack_row) {     // the scales of four neighbouring blocks as one word
+        uint32_t word = code << (8 * ((lane / LPB) & 3));
+        word |= __shfl_xor_sync(0xFFFFFFFFu, word, LPB);
+        word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * LPB);
+        if (valid && lane % (4 * LPB) == 0)
+          *reinterpret_cast<uint32_t*>(a.s_row + scale_at(row, at / 32, kb, a.mma)) = word;
+      } else if (valid && lane % LPB == 0) {
+        a.s_row[scale_at(row, at / 32, kb, a.mma)] = static_cast<uint8_t>(code);
+      }
+    }
+  }
+}
+
+// Block-wide sum over 1024 threads (all threads get it); `red` holds 32 floats.
+__device__ __forceinline__ float block_sum_1024(float v, float* red) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum(red[threadIdx.x & 31]);
+}
+
+// Rows too long for the registers of one CTA (more than 32768 elements): one
+// CTA per row and three passes over it (sum, deviations, output), the later
+// two from L2.
+template <typename TX, int OUT>
+__global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
+  __shared__ float red[32];
+  grid_dep_wait();
+  const int64_t row = blockIdx.x;
+  const TX* x = static_cast<const TX*>(a.x) + row * a.ld;
+  const float inv_c = 1.f / static_cast<float>(a.cols);
+  Vec<TX, 1> e;
+  float s = 0.f;
+  for (int i = threadIdx.x; i < a.cols; i += 1024) {
+    e.load(x + i);
+    s += e.get(0);
+  }
+  const float mean = block_sum_1024(s, red) * inv_c;
+  s = 0.f;
+  for (int i = threadIdx.x; i < a.cols; i += 1024) {
+    e.load(x + i);
+    s += (e.get(0) - mean) * (e.get(0) - mean);
+  }
+  const float rstd = 1.f / sqrtf(block_sum_1024(s, red) * inv_c + a.eps);
+  if (threadIdx.x == 0) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
+  if (!a.y) return;
+  using TY = typename std::conditional<OUT == OUT_F32, float, __nv_bfloat16>::type;
+  TY* y = static_cast<TY*>(a.y) + row * a.cols;
+  for (int i = threadIdx.x; i < a.cols; i += 1024) {
+    float w[1], b[1], o[1];
+    load_affine<1>(a, i, w, b);
+    e.load(x + i);
+    o[0] = norm_value(e.get(0), mean, rstd, w[0], b[0]);
+    store_vec<TY, 1>(y + i, o);
+  }
+}
+
+// Quantizing norm with column blocks: a CTA holds 32 rows of up to SLAB
+// columns, raw, in registers (the row pass) and in shared memory (the column
+// pass), so x is read from HBM once for both copies.  CLUSTER: the CTAs of a
+// cluster hold the slabs of the same 32 rows; each pushes its 32 partial
+// (sum, M2) pairs into every CTA's shared memory, and one cluster barrier
+// later each merges them.  Otherwise the statistics are given.
+template <typename TX> constexpr int slab_cols() { return sizeof(TX) == 2 ? 1024 : 512; }
+
+template <typename TX, int FMT, int ORIENT, bool CLUSTER>
+__global__ void __launch_bounds__(256, 2) norm_tile_kernel(const NormArgs a, int slabs) {
+  constexpr int SLAB = slab_cols<TX>();
+  constexpr int VE = 16 / static_cast<int>(sizeof(TX));
+  constexpr int NV = SLAB / (32 * VE);
+  constexpr int RW = 4;                                  // rows of a warp
+  constexpr int LPB = 32 / VE;
+  extern __shared__ __align__(16) uint8_t tile[];        // [32][SLAB] raw
+  __shared__ float2 parts[8][32];                        // [rank][row] (sum, M2)
+  __shared__ float2 stat[32];                            // [row] (mean, rstd)
+  if constexpr (CLUSTER) cluster_arrive();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = blockIdx.x % slabs;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / slabs) * 32;
+  const int c0 = rank * SLAB;
+  const int nc = min(SLAB, a.cols - c0);                 // columns of this slab (a multiple of 32)
+  const TX* x = static_cast<const TX*>(a.x) + row0 * a.ld + c0;
+
+  Vec<TX, VE> raw[RW][NV];
+#pragma unroll
+  for (int r = 0; r < RW; ++r)
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      raw[r][k].fill(0);
+      const int at = (k * 32 + lane) * VE;
+      if (at < nc) raw[r][k].load(x + (warp * RW + r) * a.ld + at);
+    }
+  if constexpr (ORIENT & MXQ_COL) {
+#pragma unroll
+    for (int r = 0; r < RW; ++r)
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        *reinterpret_cast<uint4*>(tile + ((warp * RW + r) * SLAB + (k * 32 + lane) * VE) * sizeof(TX)) =
+            make_uint4(raw[r][k].w[0], raw[r][k].w[1], raw[r][k].w[2], raw[r][k].w[3]);
+  }
+
+  if constexpr (CLUSTER) {
+    float2 mine = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      float s[NV], d[NV];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float v[VE];
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[j] = raw[r][k].get(j);
+        s[k] = tree_sum(v);
+      }
+      const float sum = warp_sum(tree_sum(s));
+      const float m = sum / static_cast<float>(nc);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float v[VE];
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[j] = (raw[r][k].get(j) - m) * (raw[r][k].get(j) - m);
+        d[k] = (k * 32 + lane) * VE < nc ? tree_sum(v) : 0.f;
+      }
+      const float m2 = warp_sum(tree_sum(d));
+      if (lane == r) mine = make_float2(sum, m2);
+    }
+    cluster_wait();                                      // every CTA of the cluster has started
+    if (lane < RW)
+      for (int k = 0; k < slabs; ++k)
+        st_cluster_f2(smem_u32(&parts[rank][warp * RW + lane]), k, mine.x, mine.y);
+    cluster_sync();
+    if (warp == 0) {
+      float sum = 0.f, m2 = 0.f;
+      for (int k = 0; k < slabs; ++k) sum += parts[k][lane].x;
+      const float mean = sum / static_cast<float>(a.cols);
+      for (int k = 0; k < slabs; ++k) {
+        const float n = static_cast<float>(min(SLAB, a.cols - k * SLAB));
+        const float d = parts[k][lane].x / n - mean;
+        m2 += parts[k][lane].y + n * d * d;
+      }
+      const float rstd = 1.f / sqrtf(m2 / static_cast<float>(a.cols) + a.eps);
+      stat[lane] = make_float2(mean, rstd);
+      if (rank == 0) {
+        a.mean[row0 + lane] = mean;
+        a.rstd[row0 + lane] = rstd;
+      }
+    }
+  } else {
+    if (warp == 0) stat[lane] = make_float2(a.mean[row0 + lane], a.rstd[row0 + lane]);
+  }
+  __syncthreads();
+
+  if constexpr (ORIENT & MXQ_ROW) {
+    constexpr int QW = code_words<FMT, VE>();
+    const int kb = a.cols / 32;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int at = (k * 32 + lane) * VE;
+      const bool valid = at < nc;
+      float w[VE], b[VE];
+      if (valid) load_affine<VE>(a, c0 + at, w, b);
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        const int64_t row = row0 + warp * RW + r;
+        const float2 st = stat[warp * RW + r];
+        float o[VE];
+        float m = 0.f;
+        if (valid) {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            o[j] = norm_value(raw[r][k].get(j), st.x, st.y, w[j], b[j]);
+            m = fmax3_nan(m, fabsf(o[j]), 0.f);
+          }
+        }
+#pragma unroll
+        for (int i = 1; i < LPB; i <<= 1) m = fmax3_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, i), 0.f);
+        float mult;
+        const uint32_t code = mx_scale<FMT>(__float_as_uint(m) & 0x7FFFFFFFu, a.ceil_mode, mult);
+        if (valid) {
+          uint32_t q[QW];
+          mx_codes<FMT, VE>(o, mult, code == 0xFFu, q);
+          const int64_t el = row * a.cols + c0 + at;
+          uint8_t* dst = a.q_row + (FMT == MXQ_E2M1 ? el / 2 : el);
+          if constexpr (FMT == MXQ_E2M1 && VE == 4) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(q[0]);
+          else if constexpr (QW == 1) *reinterpret_cast<uint32_t*>(dst) = q[0];
+          else *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+        }
+        if (a.pack_row) {
+          uint32_t word = code << (8 * ((lane / LPB) & 3));
+          word |= __shfl_xor_sync(0xFFFFFFFFu, word, LPB);
+          word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * LPB);
+          if (valid && lane % (4 * LPB) == 0)
+            *reinterpret_cast<uint32_t*>(a.s_row + scale_at(row, (c0 + at) / 32, kb, a.mma)) = word;
+        } else if (valid && lane % LPB == 0) {
+          a.s_row[scale_at(row, (c0 + at) / 32, kb, a.mma)] = static_cast<uint8_t>(code);
+        }
+      }
+    }
+  }
+
+  if constexpr (ORIENT & MXQ_COL) {
+    // one column per thread and turn: its 32 rows are one block
+    constexpr int QW = code_words<FMT, 32>();
+    const int kb = a.rows / 32;
+    for (int c = threadIdx.x; c < nc; c += 256) {
+      float w[1], b[1], o[32];
+      load_affine<1>(a, c0 + c, w, b);
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        const float2 st = stat[r];
+        float xv;
+        if constexpr (sizeof(TX) == 2)
+          xv = bf16lo(*reinterpret_cast<const uint16_t*>(tile + (r * SLAB + c) * 2));
+        else
+          xv = *reinterpret_cast<const float*>(tile + (r * SLAB + c) * 4);
+        o[r] = norm_value(xv, st.x, st.y, w[0], b[0]);
+      }
+      float mult;
+      const uint32_t code = mx_scale<FMT>(amax32_tree([&](int j) { return fabsf(o[j]); }), a.ceil_mode, mult);
+      uint32_t q[QW];
+      mx_codes<FMT, 32>(o, mult, code == 0xFFu, q);
+      const int64_t el = static_cast<int64_t>(c0 + c) * a.rows + row0;
+      uint8_t* dst = a.q_col + (FMT == MXQ_E2M1 ? el / 2 : el);
+#pragma unroll
+      for (int i = 0; i < QW; i += 4)
+        *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(q[i], q[i + 1], q[i + 2], q[i + 3]);
+      a.s_col[scale_at(c0 + c, row0 / 32, kb, a.mma)] = static_cast<uint8_t>(code);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+struct BwdArgs {
+  const void* dy;
+  int64_t ld_dy;
+  const void* x;
+  int64_t ld_x;
+  int rows, cols;
+  const float* mean;
+  const float* rstd;
+  const void* w;
+  int w_f32;
+  void* dx;               // [rows][cols], the type of x
+  float* part;            // [parts][2][cols] sums of dy*h and dy over a CTA's rows; NULL: not wanted
+  float* coef;            // [rows][2] (long rows only)
+};
+
+// A thread owns VE * NV columns and keeps their two column sums in registers
+// while its CTA walks over rows, RB per step (their loads are in flight
+// together and share one barrier); a group of G threads has a row.  x and dy
+// are read once and dx written once, so HBM bounds it; the column sums of a
+// CTA go out once at the end and a second kernel adds them up in a fixed
+// order.
+template <typename TX, typename TD, int VE, int NV, int RB>
+__global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) {
+  __shared__ float2 red[2][RB][32];
+  extern __shared__ __align__(16) float comb[];
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int P = blockDim.x / G, g = threadIdx.x / G, t = threadIdx.x - g * G;
+  const int wpg = G >> 5;
+  const int nvec = a.cols / VE;
+  const float inv_c = 1.f / static_cast<float>(a.cols);
+
+  float w[NV][VE], aw[NV][VE], ab[NV][VE];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      w[k][j] = 1.f;
+      aw[k][j] = ab[k][j] = 0.f;
+    }
+    if (a.w && k * G + t < nvec) load_param<VE>(a.w, a.w_f32, (k * G + t) * VE, w[k]);
+  }
+
+  int buf = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * P * RB;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * P * RB; base < a.rows; base += step) {
+    const int64_t row = base + g * RB;
+    Vec<TX, VE> xr[RB][NV];
+    Vec<TD, VE> dr[RB][NV];
+    float mean[RB], rstd[RB], c1[RB], c2[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const bool in = row + r < a.rows;
+      mean[r] = in ? a.mean[row + r] : 0.f;
+      rstd[r] = in ? a.rstd[row + r] : 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        xr[r][k].fill(0);
+        dr[r][k].fill(0);
+        if (in && k * G + t < nvec) {
+          xr[r][k].load(static_cast<const TX*>(a.x) + (row + r) * a.ld_x + (k * G + t) * VE);
+          dr[r][k].load(static_cast<const TD*>(a.dy) + (row + r) * a.ld_dy + (k * G + t) * VE);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      float s1[NV], s2[NV];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float u[VE], v[VE];
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const float h = (xr[r][k].get(j) - mean[r]) * rstd[r];
+          const float d = dr[r][k].get(j);
+          u[j] = d * w[k][j];
+          v[j] = u[j] * h;
+          aw[k][j] = fmaf(d, h, aw[k][j]);
+          ab[k][j] += d;
+        }
+        s1[k] = tree_sum(u);
+        s2[k] = tree_sum(v);
+      }
+      c1[r] = warp_sum(tree_sum(s1));
+      c2[r] = warp_sum(tree_sum(s2));
+    }
+    if (wpg > 1) {
+      if (lane == 0)
+#pragma unroll
+        for (int r = 0; r < RB; ++r) red[buf][r][warp] = make_float2(c1[r], c2[r]);
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        c1[r] = c2[r] = 0.f;
+        for (int i = 0; i < wpg; ++i) {
+          const float2 v = red[buf][r][g * wpg + i];
+          c1[r] += v.x;
+          c2[r] += v.y;
+        }
+      }
+      buf ^= 1;
+    }
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      if (row + r >= a.rows) continue;
+      const float m1 = c1[r] * inv_c, m2 = c2[r] * inv_c;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (k * G + t >= nvec) continue;
+        float o[VE];
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const float h = (xr[r][k].get(j) - mean[r]) * rstd[r];
+          o[j] = (fmaf(dr[r][k].get(j), w[k][j], -m1) - h * m2) * rstd[r];
+        }
+        store_vec<TX, VE>(static_cast<TX*>(a.dx) + (row + r) * a.cols + (k * G + t) * VE, o);
+      }
+    }
+  }
+  if (!a.part) return;
+  float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+  if (P > 1) {                      // the groups of the CTA first, in their order
+    for (int i = 1; i < P; ++i) {
+      __syncthreads();
+      if (g == i)
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            comb[(2 * (k * VE + j)) * G + t] = aw[k][j];
+            comb[(2 * (k * VE + j) + 1) * G + t] = ab[k][j];
+          }
+      __syncthreads();
+      if (g == 0)
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            aw[k][j] += comb[(2 * (k * VE + j)) * G + t];
+            ab[k][j] += comb[(2 * (k * VE + j) + 1) * G + t];
+          }
+    }
+    if (g) return;
+  }
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    if (k * G + t >= nvec) continue;
+    if constexpr (VE == 1) {
+      out[k * G + t] = aw[k][0];
+      out[a.cols + k * G + t] = ab[k][0];
+    } else {
+      store_vec<float, VE>(out + (k * G + t) * VE, aw[k]);
+      store_vec<float, VE>(out + a.cols + (k * G + t) * VE, ab[k]);
+    }
+  }
+}
+
+// Rows too long for the registers: their two sums first ...
+template <typename TX, typename TD>
+__global__ void __launch_bounds__(1024) norm_bwd_long_rows_kernel(const BwdArgs a) {
+  __shared__ float red[32];
+  grid_dep_wait();
+  const int64_t row = blockIdx.x;
+  const TX* x = static_cast<const TX*>(a.x) + row * a.ld_x;
+  const TD* dy = static_cast<const TD*>(a.dy) + row * a.ld_dy;
+  const float mean = a.mean[row], rstd = a.rstd[row];
+  float c1 = 0.f, c2 = 0.f;
+  for (int i = threadIdx.x; i < a.cols; i += 1024) {
+    Vec<TX, 1> xe;
+    Vec<TD, 1> de;
+    xe.load(x + i);
+    de.load(dy + i);
+    float w[1] = {1.f};
+    if (a.w) load_param<1>(a.w, a.w_f32, i, w);
+    const float u = de.get(0) * w[0];
+    c1 += u;
+    c2 += u * ((xe.get(0) - mean) * rstd);
+  }
+  c1 = block_sum_1024(c1, red);
+  c2 = block_sum_1024(c2, red);
+  if (threadIdx.x == 0) {
+    a.coef[2 * row] = c1 / static_cast<float>(a.cols);
+    a.coef[2 * row + 1] = c2 / static_cast<float>(a.cols);
+  }
+}
+
+// ... then a column per thread over a range of rows (blockIdx.y).
+template <typename TX, typename TD>
+__global__ void __launch_bounds__(256) norm_bwd_long_cols_kernel(const BwdArgs a) {
+  grid_dep_wait();
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (c >= a.cols) return;
+  float w[1] = {1.f};
+  if (a.w) load_param<1>(a.w, a.w_f32, c, w);
+  float aw = 0.f, ab = 0.f;
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    Vec<TX, 1> xe;
+    Vec<TD, 1> de;
+    xe.load(static_cast<const TX*>(a.x) + row * a.ld_x + c);
+    de.load(static_cast<const TD*>(a.dy) + row * a.ld_dy + c);
+    const float rstd = a.rstd[row], h = (xe.get(0) - a.mean[row]) * rstd, d = de.get(0);
+    aw = fmaf(d, h, aw);
+    ab += d;
+    float o[1] = {(fmaf(d, w[0], -a.coef[2 * row]) - h * a.coef[2 * row + 1]) * rstd};
+    store_vec<TX, 1>(static_cast<TX*>(a.dx) + row * a.cols + c, o);
+  }
+  if (a.part) {
+    a.part[static_cast<int64_t>(blockIdx.y) * 2 * a.cols + c] = aw;
+    a.part[static_cast<int64_t>(blockIdx.y) * 2 * a.cols + a.cols + c] = ab;
+  }
+}
+
+// dw[c], db[c] = sums over the parts, in their order: 32 columns per CTA,
+// eight threads per column.
+__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* part, int parts, int cols, float* dw, float* db) {
+  __shared__ float red[8][33];
+  grid_dep_wait();
+  const int cx = threadIdx.x & 31, sy = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + cx;      // over both sums
+  float s = 0.f;
+  if (c < 2ll * cols)
+    for (int i = sy; i < parts; i += 8) s += part[static_cast<int64_t>(i) * 2 * cols + c];
+  red[sy][cx] = s;
+  __syncthreads();
+  if (sy == 0 && c < 2ll * cols) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += red[i][cx];
+    if (c < cols) {
+      if (dw) dw[c] = s;
+    } else if (db) {
+      db[c - cols] = s;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+using namespace mxq_host;
+
+constexpr int kMaxRowElems = 32768;       // forward: one CTA's registers
+constexpr int kMaxBwdElems = 16384;       // backward: data and two column sums
+
+bool valid_type(int t) { return t == MXQ_BF16 || t == MXQ_F32; }
+int type_size(int t) { return t == MXQ_F32 ? 4 : 2; }
+bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+int round_up(int v, int m) { return (v + m - 1) / m * m; }
+
+template <typename TX, int OUT, int VE, int NV>
+int launch_row(const NormArgs& a, bool warp, int threads, cudaStream_t st) {
+  if (warp)
+    return launch_pdl(norm_row_kernel<TX, OUT, VE, NV, true>, dim3((a.rows + 7) / 8), dim3(256), 0, st, a);
+  return launch_pdl(norm_row_kernel<TX, OUT, VE, NV, false>, dim3(a.rows), dim3(threads), 0, st, a);
+}
+
+// One row per warp while a lane holds at most 32 elements, else one per CTA of
+// just enough warps that a thread holds at most 32 elements.
+template <typename TX, int OUT, int VE>
+int dispatch_row(const NormArgs& a, cudaStream_t st) {
+  constexpr int MAXV = 32 / VE;
+  const int nvec = a.cols / VE;
+  const bool warp = nvec <= 32 * MAXV;
+  const int threads = warp ? 32 : round_up((nvec + MAXV - 1) / MAXV, 32);
+  const int nv = (nvec + threads - 1) / threads;
+  if constexpr (VE > 1) {
+    if (nv <= 1) return launch_row<TX, OUT, VE, 1>(a, warp, threads, st);
+    if (nv <= 2) return launch_row<TX, OUT, VE, 2>(a, warp, threads, st);
+  }
+  if constexpr (MAXV >= 8)
+    if (nv <= MAXV / 2) return launch_row<TX, OUT, VE, MAXV / 2>(a, warp, threads, st);
+  return launch_row<TX, OUT, VE, MAXV>(a, warp, threads, st);
+}
+
+template <typename TX, int OUT>
+int norm_rows(const NormArgs& a, bool vec, cudaStream_t st) {
+  constexpr int VE = sizeof(TX) == 2 && OUT != OUT_F32 ? 8 : 4;
+  if constexpr (OUT < 0) {
+    if (a.cols > kMaxRowElems) return launch_pdl(norm_long_kernel<TX, OUT>, dim3(a.rows), dim3(1024), 0, st, a);
+    if (!vec) return dispatch_row<TX, OUT, 1>(a, st);
+  }
+  return dispatch_row<TX, OUT, VE>(a, st);
+}
+
+template <typename TX, int FMT, int ORIENT, bool CLUSTER>
+int launch_tile(const NormArgs& a, cudaStream_t st) {
+  constexpr int SLAB = slab_cols<TX>();
+  const int slabs = (a.cols + SLAB - 1) / SLAB;
+  const int smem = (ORIENT & MXQ_COL) ? 32 * SLAB * static_cast<int>(sizeof(TX)) : 0;
+  auto kern = norm_tile_kernel<TX, FMT, ORIENT, CLUSTER>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return MXQ_ERR_CUDA;
+  const int64_t grid = static_cast<int64_t>(slabs) * (a.rows / 32);
+  if (grid > 0x7FFFFFFF) return MXQ_ERR_BAD_SHAPE;
+  if (CLUSTER) return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(grid)), dim3(256), smem, st, slabs, a, slabs);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(256), smem, st, a, slabs);
+}
+
+// Rows only: the row kernel.  With column blocks: one cluster per 32 rows
+// while a portable cluster (8 CTAs) holds them, else the statistics first and
+// then the slabs on their own (x is read twice).
+template <typename TX, int FMT>
+int norm_mx(const NormArgs& a, int orient, cudaStream_t st) {
+  if (orient == MXQ_ROW && a.cols <= kMaxRowElems) return norm_rows<TX, FMT>(a, true, st);
+  if (a.cols <= 8 * slab_cols<TX>())
+    return orient == MXQ_DUAL ? launch_tile<TX, FMT, MXQ_DUAL, true>(a, st) : launch_tile<TX, FMT, MXQ_COL, true>(a, st);
+  NormArgs s = a;
+  s.y = nullptr;
+  if (const int rc = norm_rows<TX, OUT_BF16>(s, true, st)) return rc;
+  if (orient == MXQ_ROW) return launch_tile<TX, FMT, MXQ_ROW, false>(a, st);
+  return orient == MXQ_DUAL ? launch_tile<TX, FMT, MXQ_DUAL, false>(a, st) : launch_tile<TX, FMT, MXQ_COL, false>(a, st);
+}
+
+template <typename TX>
+int norm_mx_fmt(const NormArgs& a, int fmt, int orient, cudaStream_t st) {
+  if (fmt == MXQ_E4M3) return norm_mx<TX, MXQ_E4M3>(a, orient, st);
+  if (fmt == MXQ_E5M2) return norm_mx<TX, MXQ_E5M2>(a, orient, st);
+  return norm_mx<TX, MXQ_E2M1>(a, orient, st);
+}
+
+int check_norm(const void* x, int64_t rows, int64_t cols, int64_t ld, int x_type, const void* w, int w_type,
+               const void* b, int b_type, const float* mean, const float* rstd) {
+  if (!valid_type(x_type) || (w && !valid_type(w_type)) || (b && !valid_type(b_type))) return MXQ_ERR_BAD_ARG;
+  if (rows < 0 || cols < 1 || ld < cols) return MXQ_ERR_BAD_SHAPE;
+  if (rows > 0x7FFFFFF0ll || cols > 0x7FFFFFF0ll) return MXQ_ERR_BAD_SHAPE;
+  if (rows && (!x || !mean || !rstd)) return MXQ_ERR_BAD_ARG;
+  if (!aligned_to(x, type_size(x_type)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4)) return MXQ_ERR_MISALIGNED;
+  if ((w && !aligned_to(w, type_size(w_type))) || (b && !aligned_to(b, type_size(b_type)))) return MXQ_ERR_MISALIGNED;
+  return MXQ_OK;
+}
+
+NormArgs norm_args(const void* x, int64_t rows, int64_t cols, int64_t ld, const void* w, int w_type, const void* b,
+                   int b_type, float eps, float* mean, float* rstd) {
+  NormArgs a{};
+  a.x = x, a.ld = ld, a.rows = static_cast<int>(rows), a.cols = static_cast<int>(cols);
+  a.w = w, a.b = b, a.w_f32 = w_type == MXQ_F32, a.b_f32 = b_type == MXQ_F32;
+  a.eps = eps, a.mean = mean, a.rstd = rstd;
+  return a;
+}
+
+// Backward: CTAs (parts of the column sums) that a launch may use.
+int bwd_parts() { return 4 * sm_count(); }
+
+template <typename TX, typename TD, int VE, int NV>
+int launch_bwd(const BwdArgs& a, int G, int& parts, cudaStream_t st) {
+  const int P = std::max(1, 512 / G);
+  const int threads = P * G;
+  const size_t smem = P > 1 ? static_cast<size_t>(2) * VE * NV * G * sizeof(float) : 0;
+  const int64_t groups = (a.rows + P - 1) / P;
+  const int most = std::min(bwd_parts(), std::max(1, 2048 / threads) * sm_count());
+  // four rows a step once every CTA has four steps' worth of them
+  if constexpr (VE * NV <= 8) if (groups >= 4ll * most) {
+    parts = static_cast<int>(std::min<int64_t>(most, (groups + 3) / 4));
+    return launch_pdl(norm_bwd_kernel<TX, TD, VE, NV, 4>, dim3(parts), dim3(threads), smem, st, a, G);
+  }
+  parts = static_cast<int>(std::min<int64_t>(most, groups));
+  return launch_pdl(norm_bwd_kernel<TX, TD, VE, NV, 1>, dim3(parts), dim3(threads), smem, st, a, G);
+}
+
+template <typename TX, typename TD, int VE>
+int dispatch_bwd(const BwdArgs& a, int& parts, cudaStream_t st) {
+  const int nvec = a.cols / VE;
+  constexpr int N1 = VE == 1 ? 4 : 1;
+  constexpr int N2 = 16 / VE;
+  if (nvec <= N1 * 1024) return launch_bwd<TX, TD, VE, N1>(a, round_up((nvec + N1 - 1) / N1, 32), parts, st);
+  return launch_bwd<TX, TD, VE, N2>(a, round_up((nvec + N2 - 1) / N2, 32), parts, st);
+}
+
+template <typename TX, typename TD>
+int norm_bwd(const BwdArgs& a, bool vec, int& parts, cudaStream_t st) {
+  if (a.cols <= kMaxBwdElems) {
+    constexpr int VE = sizeof(TX) == 2 && sizeof(TD) == 2 ? 8 : 4;
+    return vec ? dispatch_bwd<TX, TD, VE>(a, parts, st) : dispatch_bwd<TX, TD, 1>(a, parts, st);
+  }
+  const int rc = launch_pdl(norm_bwd_long_rows_kernel<TX, TD>, dim3(a.rows), dim3(1024), 0, st, a);
+  if (rc) return rc;
+  const int strips = (a.cols + 255) / 256;
+  parts = std::max(1, std::min(std::min(a.rows, bwd_parts()), 8 * sm_count() / strips));
+  return launch_pdl(norm_bwd_long_cols_kernel<TX, TD>, dim3(strips, parts), dim3(256), 0, st, a);
+}
+
+}  // namespace
+}  // namespace mxq
+
+using namespace mxq;
+using namespace mxq_host;
+
+extern "C" int mxq_layer_norm(const void* x, int64_t rows, int64_t cols, int64_t ld, int x_type, const void* w,
+                              int w_type, const void* b, int b_type, float eps, int y_type, void* y, float* mean,
+                              float* rstd, void* stream) {
+  if (!valid_type(y_type)) return MXQ_ERR_BAD_ARG;
+  const int rc = check_norm(x, rows, cols, ld, x_type, w, w_type, b, b_type, mean, rstd);
+  if (rc) return rc;
+  if (rows && !y) return MXQ_ERR_BAD_ARG;
+  if (!aligned_to(y, type_size(y_type))) return MXQ_ERR_MISALIGNED;
+  if (!device_ok()) return MXQ_ERR_UNSUPPORTED;
+  if (!rows) return MXQ_OK;
+  NormArgs a = norm_args(x, rows, cols, ld, w, w_type, b, b_type, eps, mean, rstd);
+  a.y = y;
+  const int ve = x_type == MXQ_BF16 && y_type == MXQ_BF16 ? 8 : 4;
+  const bool vec = cols % ve == 0 && ld % ve == 0 && aligned16(x) && aligned16(y) && aligned16(w) && aligned16(b);
+  const auto st = static_cast<cudaStream_t>(stream);
+  if (x_type == MXQ_BF16)
+    return y_type == MXQ_BF16 ? norm_rows<__nv_bfloat16, OUT_BF16>(a, vec, st) : norm_rows<__nv_bfloat16, OUT_F32>(a, vec, st);
+  return y_type == MXQ_BF16 ? norm_rows<float, OUT_BF16>(a, vec, st) : norm_rows<float, OUT_F32>(a, vec, st);
+}
+
+extern "C" int mxq_layer_norm_mx(const void* x, int64_t rows, int64_t cols, int64_t ld, int x_type, const void* w,
+                                 int w_type, const void* b, int b_type, float eps, int fmt, int orient,
+                                 int scale_mode, int sf_layout, void* q_row, uint8_t* s_row, void* q_col,
+                                 uint8_t* s_col, float* mean, float* rstd, void* stream) {
+  if (fmt != MXQ_E4M3 && fmt != MXQ_E5M2 && fmt != MXQ_E2M1) return MXQ_ERR_BAD_ARG;
+  if (orient != MXQ_ROW && orient != MXQ_COL && orient != MXQ_DUAL) return MXQ_ERR_BAD_ARG;
+  if (scale_mode != MXQ_SCALE_FLOOR_OCP && scale_mode != MXQ_SCALE_CEIL) return MXQ_ERR_BAD_ARG;
+  if (sf_layout != MXQ_SF_CANONICAL && sf_layout != MXQ_SF_MMA) return MXQ_ERR_BAD_ARG;
+  if ((orient & MXQ_ROW) && (!q_row || !s_row)) return MXQ_ERR_BAD_ARG;
+  if ((orient & MXQ_COL) && (!q_col || !s_col)) return MXQ_ERR_BAD_ARG;
+  const int rc = check_norm(x, rows, cols, ld, x_type, w, w_type, b, b_type, mean, rstd);
+  if (rc) return rc;
+  const int unit = sf_layout == MXQ_SF_MMA ? 128 : 32;
+  if (rows < 1 || rows % unit || cols % unit) return MXQ_ERR_BAD_SHAPE;
+  if (!aligned16(x) || ld % (16 / type_size(x_type)) || !aligned16(w) || !aligned16(b)) return MXQ_ERR_MISALIGNED;
+  if ((orient & MXQ_ROW) && !aligned16(q_row)) return MXQ_ERR_MISALIGNED;
+  if ((orient & MXQ_COL) && !aligned16(q_col)) return MXQ_ERR_MISALIGNED;
+  if (sf_layout == MXQ_SF_MMA && (((orient & MXQ_ROW) && !aligned16(s_row)) || ((orient & MXQ_COL) && !aligned16(s_col))))
+    return MXQ_ERR_MISALIGNED;
+  if (!device_ok()) return MXQ_ERR_UNSUPPORTED;
+  NormArgs a = norm_args(x, rows, cols, ld, w, w_type, b, b_type, eps, mean, rstd);
+  a.q_row = static_cast<uint8_t*>(q_row), a.s_row = s_row;
+  a.q_col = static_cast<uint8_t*>(q_col), a.s_col = s_col;
+  a.ceil_mode = scale_mode == MXQ_SCALE_CEIL;
+  a.mma = sf_layout == MXQ_SF_MMA;
+  a.pack_row = cols % 128 == 0 && aligned_to(s_row, 4);
+  const auto st = static_cast<cudaStream_t>(stream);
+  return x_type == MXQ_BF16 ? norm_mx_fmt<__nv_bfloat16>(a, fmt, orient, st) : norm_mx_fmt<float>(a, fmt, orient, st);
+}
+
+extern "C" int mxq_layer_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes) return MXQ_ERR_BAD_ARG;
+  if (rows < 0 || cols < 1) return MXQ_ERR_BAD_SHAPE;
+  const size_t parts = static_cast<size_t>(std::min<int64_t>(rows, bwd_parts()));
+  *bytes = parts * 2 * static_cast<size_t>(cols) * sizeof(float) +
+           (cols > kMaxBwdElems ? static_cast<size_t>(rows) * 2 * sizeof(float) : 0);
+  return MXQ_OK;
+}
+
+extern "C" int mxq_layer_norm_backward(const void* dy, int64_t ld_dy, int dy_type, const void* x, int64_t ld_x,
+                                       int x_type, int64_t rows, int64_t cols, const float* mean, const float* rstd,
+                                       const void* w, int w_type, void* dx, float* dw, float* db, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  if (!valid_type(dy_type)) return MXQ_ERR_BAD_ARG;
+  const int rc = check_norm(x, rows, cols, ld_x, x_type, w, w_type, nullptr, 0, mean, rstd);
+  if (rc) return rc;
+  if (ld_dy < cols) return MXQ_ERR_BAD_SHAPE;
+  if (rows && (!dy || !dx)) return MXQ_ERR_BAD_ARG;
+  const bool sums = dw || db;
+  size_t need = 0;
+  mxq_layer_norm_backward_workspace_size(rows, cols, &need);
+  if (rows && (sums || cols > kMaxBwdElems) && (!workspace || workspace_bytes < need)) return MXQ_ERR_BAD_ARG;
+  if (!aligned_to(dy, type_size(dy_type)) || !aligned_to(dx, type_size(x_type)) || !aligned16(workspace) ||
+      !aligned_to(dw, 4) || !aligned_to(db, 4))
+    return MXQ_ERR_MISALIGNED;
+  if (!device_ok()) return MXQ_ERR_UNSUPPORTED;
+  const auto st = static_cast<cudaStream_t>(stream);
+  if (!rows) {
+    if (dw && cudaMemsetAsync(dw, 0, cols * sizeof(float), st) != cudaSuccess) return MXQ_ERR_CUDA;
+    if (db && cudaMemsetAsync(db, 0, cols * sizeof(float), st) != cudaSuccess) return MXQ_ERR_CUDA;
+    return MXQ_OK;
+  }
+  BwdArgs a{};
+  a.dy = dy, a.ld_dy = ld_dy, a.x = x, a.ld_x = ld_x;
+  a.rows = static_cast<int>(rows), a.cols = static_cast<int>(cols);
+  a.mean = mean, a.rstd = rstd, a.w = w, a.w_f32 = w_type == MXQ_F32, a.dx = dx;
+  a.part = sums ? static_cast<float*>(workspace) : nullptr;
+  a.coef = static_cast<float*>(workspace) + std::min<int64_t>(rows, bwd_parts()) * 2 * cols;
+  const int ve = x_type == MXQ_BF16 && dy_type == MXQ_BF16 ? 8 : 4;
+  const bool vec = cols % ve == 0 && ld_x % ve == 0 && ld_dy % ve == 0 && aligned16(x) && aligned16(dy) &&
+                   aligned16(dx) && aligned16(w);
+  int parts = 0, rc2;
+  if (x_type == MXQ_BF16)
+    rc2 = dy_type == MXQ_BF16 ? norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, vec, parts, st)
+                              : norm_bwd<__nv_bfloat16, float>(a, vec, parts, st);
+  else
+    rc2 = dy_type == MXQ_BF16 ? norm_bwd<float, __nv_bfloat16>(a, vec, parts, st) : norm_bwd<float, float>(a, vec, parts, st);
+  if (rc2 || !sums) return rc2;
+  const int grid = static_cast<int>((2 * cols + 31) / 32);
+  return launch_pdl(norm_bwd_sum_kernel, dim3(grid), dim3(256), 0, st, static_cast<const float*>(workspace), parts,
+                    a.cols, dw, db);
+}

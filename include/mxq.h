@@ -97,6 +97,10 @@ extern "C" {
  * (r%32)*16 + ((r/32)%4)*4 + (k%4).  Same bytes, permuted. */
 #define MXQ_SF_CANONICAL 0
 #define MXQ_SF_MMA       1
+/* Element types of the training-step operators (layer norm, policy loss,
+ * gradient clipping). */
+#define MXQ_BF16 0
+#define MXQ_F32  1
 
 /* ---- MX quantize ([MX] sections 1 and 4, gap sections 1-2; [FAF]) ----------
  * x        bf16 [rows][ld] (only the first cols of each row are read),
@@ -338,6 +342,116 @@ int mxq_mm_fp8(const void* a, const void* b, int64_t batch, int64_t M,
                int64_t N, int64_t K, int a_batched, int b_batched,
                int trans_a, int trans_b, int fmt, const float* scale,
                const void* bias, void* c, void* stream);
+
+/* ---- layer norm ---------------------------------------------------------------
+ * Per row: mean = sum x / cols, var = sum (x - mean)^2 / cols,
+ * rstd = 1 / sqrt(var + eps), y = (x - mean) * rstd * w + b, in float32,
+ * rounded once to y's type (RNE).  The products' operands come from such rows.
+ * x        [rows][ld] of x_type (MXQ_BF16 | MXQ_F32); only the first cols of a
+ *          row are read.  rows >= 0, cols >= 1, ld >= cols, any sizes.
+ * w, b     [cols] of w_type / b_type, or NULL (1 and 0).
+ * y        [rows][cols] of y_type.
+ * mean, rstd  float [rows], kept for the backward pass.
+ * Pointers aligned to their elements (16-byte aligned rows of a multiple of
+ * 16 bytes run faster).  y must not overlap x. */
+int mxq_layer_norm(const void* x, int64_t rows, int64_t cols, int64_t ld,
+                   int x_type, const void* w, int w_type, const void* b,
+                   int b_type, float eps, int y_type, void* y, float* mean,
+                   float* rstd, void* stream);
+
+/* ---- layer norm straight to MX ([FAF]: a producer writes its consumer's
+ * format and layout) -------------------------------------------------------------
+ * The y of mxq_layer_norm, not rounded to bf16 but quantized from float32 by
+ * the rules of mxq_quantize (RNE): row blocks, column blocks or both.
+ * fmt, orient, scale_mode, sf_layout, q_row, s_row, q_col, s_col as
+ *          mxq_quantize; rows, cols multiples of 32 (128 for MXQ_SF_MMA), rows >= 1.
+ * x, w, b 16-byte aligned, ld a multiple of 16 bytes. */
+int mxq_layer_norm_mx(const void* x, int64_t rows, int64_t cols, int64_t ld,
+                      int x_type, const void* w, int w_type, const void* b,
+                      int b_type, float eps, int fmt, int orient,
+                      int scale_mode, int sf_layout, void* q_row,
+                      uint8_t* s_row, void* q_col, uint8_t* s_col,
+                      float* mean, float* rstd, void* stream);
+
+/* ---- layer norm, backward -------------------------------------------------------
+ * With h = (x - mean) * rstd and g = dy * w (means over the row's cols):
+ *   dx = rstd * (g - mean(g) - h * mean(g * h))   [rows][cols], x's type
+ *   dw = sum over rows of dy * h, db = sum over rows of dy   float [cols]
+ * dw, db   NULL where not wanted.  Float32 sums in a fixed order: the same
+ *          inputs on the same GPU give the same bits.  rows == 0 gives zeros.
+ * workspace  at least mxq_layer_norm_backward_workspace_size bytes, 16-byte
+ *          aligned, any contents (may be NULL when dw and db are and cols is
+ *          at most 16384). */
+int mxq_layer_norm_backward_workspace_size(int64_t rows, int64_t cols,
+                                           size_t* bytes);
+int mxq_layer_norm_backward(const void* dy, int64_t ld_dy, int dy_type,
+                            const void* x, int64_t ld_x, int x_type,
+                            int64_t rows, int64_t cols, const float* mean,
+                            const float* rstd, const void* w, int w_type,
+                            void* dx, float* dw, float* db, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ---- clipped policy loss with a KL term, forward and backward -----------------
+ * Per token (row of logits z, target a, weight w, advantage A):
+ *   lp = z_a - log sum_v exp(z_v)                           -> logp
+ *   r  = exp(lp - old_logp)
+ *   l  = -min(r A, min(max(r, 1 - clip_low), 1 + clip_high) A)
+ *        + beta (exp(d) - d - 1),  d = ref_logp - lp
+ *   loss = sum over tokens of w l
+ *   grad_v = grad_scale w dl/dlp ([v == a] - exp(z_v - lse))
+ * where the first term's slope is -A r while r A <= the clipped product and 0
+ * beyond, and the second's beta (1 - exp(d)).
+ * logits   [tokens][ld] of logits_type, only the first vocab of a row read.
+ * targets  int64 (targets_64 == 1) or int32 (0) [tokens].
+ * weights  float [tokens].  A token of weight 0 (a prompt token, padding) is
+ *          not looked at: its logits, target, old_logp, advantage and
+ *          ref_logp may hold anything; its logp and gradient are 0.
+ *          A target outside [0, vocab) under a non-zero weight reads nothing
+ *          and gives NaN.
+ * ref_logp may be NULL when beta == 0 (the second term is then left out).
+ * clip_low, clip_high >= 0.
+ * loss     one float; logp float [tokens].
+ * grad     NULL, or [tokens][ld_grad] of grad_type; must not overlap logits.
+ * workspace  mxq_policy_loss_workspace_size bytes, 16-byte aligned,
+ *          zero-filled before its first use (its first 256 bytes are left
+ *          zero).  Calls that share a workspace must not run concurrently.
+ * Sums in a fixed order; tokens == 0 gives loss 0. */
+int mxq_policy_loss_workspace_size(int64_t tokens, size_t* bytes);
+int mxq_policy_loss(const void* logits, int64_t tokens, int64_t vocab,
+                    int64_t ld, int logits_type, const void* targets,
+                    int targets_64, const float* old_logp,
+                    const float* advantages, const float* weights,
+                    const float* ref_logp, float clip_low, float clip_high,
+                    float beta, float grad_scale, float* loss, float* logp,
+                    void* grad, int64_t ld_grad, int grad_type,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- global gradient norm and clipping -----------------------------------------
+ *   norm = sqrt(sum over all tensors of g^2)
+ *   out  = g * min(1, max_norm / (norm + 1e-6)), rounded to out's type
+ * grads    host array (read during the call only), one entry per tensor of n
+ *          elements in a row; n == 0 is allowed.  mxq_grad_norm reads g only;
+ *          for mxq_clip_grad_norm out may be g itself (the same type) or
+ *          another buffer that overlaps no tensor.
+ * norm     one float.  Values whose squares overflow or vanish in float32
+ *          are squared in float64; a NaN or infinite element shows in norm
+ *          (NaN or inf), and the factor is then NaN or 0 as the formula says.
+ * max_norm >= 0.
+ * workspace  mxq_grad_norm_workspace_size(ntensors) bytes, 16-byte aligned,
+ *          any contents. */
+typedef struct mxq_grad {
+  const void* g;
+  void* out;
+  int64_t n;
+  int32_t g_type;              /* MXQ_BF16 | MXQ_F32 */
+  int32_t out_type;
+} mxq_grad;
+int mxq_grad_norm_workspace_size(int ntensors, size_t* bytes);
+int mxq_grad_norm(const mxq_grad* grads, int ntensors, float* norm,
+                  void* workspace, size_t workspace_bytes, void* stream);
+int mxq_clip_grad_norm(const mxq_grad* grads, int ntensors, float max_norm,
+                       float* norm, void* workspace, size_t workspace_bytes,
+                       void* stream);
 
 /* ---- scale layout conversion ([FAF]) -----------------------------------------
  * Canonical scales s [rows][kb] -> MMA layout (rows % 128 == 0,
