@@ -13,16 +13,15 @@
 // warps go to every CTA of the cluster, and p_v = e_v exp(m_w - lse) needs no
 // second exponential.
 #include <algorithm>
+#include <atomic>
 
 #include "rowops.cuh"
 
 namespace mxq {
 namespace {
 
-constexpr int TPB = 512;                 // threads of a CTA
-constexpr int WPB = TPB / 32;
 constexpr int MAX_SLABS = 8;             // CTAs of a cluster (the portable limit)
-constexpr int MAX_E = 32;                // elements of a thread
+constexpr int MAX_E = 32;                // elements of a thread (register kernel)
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct LossArgs {
@@ -106,11 +105,11 @@ __device__ __forceinline__ void token_loss(const LossArgs& a, int64_t row, float
   }
 }
 
-// The last CTA to finish adds the tokens' terms in their order per thread and
-// the threads' sums in a fixed tree, in float64.
+// The last of `ctas` CTAs to finish adds the tokens' terms in their order per
+// thread and the threads' sums in a fixed tree, in float64.
 __device__ __forceinline__ void finish_loss(const LossArgs& a, unsigned ctas) {
   __shared__ unsigned last;
-  __shared__ double sums[WPB];
+  __shared__ double sums[32];
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) == ctas - 1;
@@ -118,12 +117,12 @@ __device__ __forceinline__ void finish_loss(const LossArgs& a, unsigned ctas) {
   if (!last) return;
   __threadfence();
   double s = 0.0;
-  for (int i = threadIdx.x; i < a.tokens; i += TPB) s += static_cast<double>(__ldcg(a.terms + i));
+  for (int i = threadIdx.x; i < a.tokens; i += blockDim.x) s += static_cast<double>(__ldcg(a.terms + i));
   s = warp_sum(s);
   if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < WPB; ++i) s += sums[i];
+    for (int i = 1; i < static_cast<int>(blockDim.x >> 5); ++i) s += sums[i];
     a.loss[0] = static_cast<float>(s);
     *a.ticket = 0;
   }
@@ -135,8 +134,9 @@ __device__ __forceinline__ void finish_loss(const LossArgs& a, unsigned ctas) {
 // move in whole words; only the first and the last vector are ragged.
 // LONG: rows beyond the registers of a cluster; two passes, the second from
 // L2.
-template <typename TZ, typename TG, int VE, int NV, bool LONG>
-__global__ void __launch_bounds__(TPB, 2) policy_kernel(const LossArgs a, int slabs) {
+template <typename TZ, typename TG, int VE, int NV, bool LONG, int TPB>
+__global__ void __launch_bounds__(TPB, 1024 / TPB) policy_kernel(const LossArgs a, int slabs) {
+  constexpr int WPB = TPB / 32;
   __shared__ float2 pairs[MAX_SLABS * WPB];
   cluster_arrive();
   grid_dep_wait();
@@ -258,47 +258,364 @@ __global__ void __launch_bounds__(TPB, 2) policy_kernel(const LossArgs a, int sl
   if (rank == 0) finish_loss(a, a.tokens);
 }
 
+// ---------------------------------------------------------------- long rows of many tokens
+// A persistent CTA (or cluster of `slabs`) takes token after token.  Its part
+// of a row streams through a ring of 16 KiB chunks in shared memory: one warp
+// issues the bulk copies, the others take the running maximum and sum as
+// chunks arrive (first pass), exchange them over the cluster, and read the
+// same chunks again to write the gradient (second pass), which frees them.
+// The ring holds a whole part and a share of the next token's, so loads run
+// ahead through the exchange and the stores, and two CTAs share an SM, so one
+// computes while the other waits.  Two exponentials per element instead of
+// one, but no data held in registers.
+constexpr int RING_CHUNK = 16384, RING_SLOTS = 6, RING_AHEAD = 2;
+constexpr int RING_TPB = 512, RING_WARPS = RING_TPB / 32;
+constexpr float kLowest = -3.402823466e38f;
+
+// exp(v - m) of a pair, m and log2(e) splat.
+__device__ __forceinline__ void exp_pair(float a, float b, uint64_t mm, uint64_t l2e, float& x, float& y) {
+  float p, q;
+  f32x2_unpack(f32x2_mul(f32x2_sub(f32x2_pack(a, b), mm), l2e), p, q);
+  x = ex2(p);
+  y = ex2(q);
+}
+
+// A thread's running maximum and sum over VE more elements.
+template <int VE>
+__device__ __forceinline__ void take_in(const float (&v)[VE], float& m, float& s) {
+  float top = m;
+#pragma unroll
+  for (int j = 0; j < VE; j += 2) top = fmax3_nan(top, v[j], v[j + 1]);
+  s *= ex2((m - top) * kLog2e);
+  m = top;
+  const uint64_t mm = f32x2_splat(m), l2e = f32x2_splat(kLog2e);
+  uint64_t acc = f32x2_pack(s, 0.f);
+#pragma unroll
+  for (int j = 0; j < VE; j += 2) {
+    float x, y;
+    exp_pair(v[j], v[j + 1], mm, l2e, x, y);
+    acc = f32x2_add(acc, f32x2_pack(x, y));
+  }
+  float x, y;
+  f32x2_unpack(acc, x, y);
+  s = x + y;
+}
+
+// The gradient's VE elements in place of the logits: exp(v - top) * f, and k
+// more at the target.
+template <int VE>
+__device__ __forceinline__ void to_gradient(float (&v)[VE], uint64_t top, uint64_t f, int target, float k) {
+  const uint64_t l2e = f32x2_splat(kLog2e);
+#pragma unroll
+  for (int j = 0; j < VE; j += 2) {
+    float x, y;
+    exp_pair(v[j], v[j + 1], top, l2e, x, y);
+    f32x2_unpack(f32x2_mul(f32x2_pack(x, y), f), v[j], v[j + 1]);
+  }
+  if (static_cast<unsigned>(target) < static_cast<unsigned>(VE)) {
+#pragma unroll
+    for (int j = 0; j < VE; ++j)
+      if (j == target) v[j] += k;
+  }
+}
+
+// What a token brings besides its logits, loaded one token ahead.
+struct TokenIn {
+  float w;
+  int64_t target;
+};
+
+__device__ __forceinline__ TokenIn token_in(const LossArgs& a, int64_t row) {
+  TokenIn t{0.f, -1};
+  if (row < a.tokens) {
+    t.w = a.weights[row];
+    t.target = a.targets64 ? static_cast<const int64_t*>(a.targets)[row]
+                           : static_cast<int64_t>(static_cast<const int*>(a.targets)[row]);
+  }
+  return t;
+}
+
+template <typename TZ, typename TG>
+__global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const LossArgs a, int slabs, int part, int* status) {
+  constexpr int VE = 16 / static_cast<int>(sizeof(TZ));      // elements of a 16-byte word of logits
+  constexpr int CV = RING_CHUNK / 16;                        // words of a chunk
+  constexpr int U = CV / RING_TPB;                           // words of a thread in it
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float2 pairs[2][MAX_SLABS * RING_WARPS];
+  __shared__ __align__(8) uint64_t full[RING_SLOTS], empty[RING_SLOTS], xbar[2];
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < RING_SLOTS; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), RING_WARPS);
+    }
+    mbar_init(smem_u32(&xbar[0]), slabs * RING_WARPS);
+    mbar_init(smem_u32(&xbar[1]), slabs * RING_WARPS);
+    fence_mbar_init();
+  }
+  cluster_sync();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = blockIdx.x % slabs;
+  const int64_t row0 = blockIdx.x / slabs, step = gridDim.x / slabs;
+  const int V = a.vocab;
+  const int w0 = rank * part;                                // first word of this CTA's part
+  bool alive = true;                                         // false once a wait has given up
+
+  // elements between a row's first word boundary and its first element; words
+  // [lo, hi) are whole, a ragged first or last one is read by its thread alone
+  const auto shift = [&](int64_t row) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(a.z) / sizeof(TZ) + row * a.ld_z) % VE);
+  };
+
+  if (warp == RING_WARPS) {
+    if (lane == 0) {
+      int slot = 0, phase = 1, n = 0;                        // phase: parity of the slot's last release
+      float next = row0 < a.tokens ? a.weights[row0] : 0.f;
+      for (int64_t row = row0; row < a.tokens && alive; row += step) {
+        const float wt = next;
+        if (row + step < a.tokens) next = a.weights[row + step];
+        if (wt == 0.f) continue;
+        const int h = shift(row);
+        const uint8_t* base = static_cast<const uint8_t*>(a.z) + (row * a.ld_z - h) * static_cast<int64_t>(sizeof(TZ));
+        const int lo = h ? 1 : 0, hi = (V + h) / VE, end = min(w0 + part, (V + h + VE - 1) / VE);
+        for (int w = w0; w < end; w += CV) {
+          if (n >= RING_SLOTS) {
+            alive = mbar_wait(smem_u32(&empty[slot]), phase, status);
+            if (!alive) break;
+          }
+          const int b = max(w, lo), e = min(min(w + CV, end), hi);
+          const uint32_t bytes = e > b ? static_cast<uint32_t>(e - b) * 16u : 0u;
+          mbar_arrive_expect_tx(smem_u32(&full[slot]), bytes);
+          if (bytes)
+            bulk_load_1d(smem_u32(ring + slot * RING_CHUNK + (b - w) * 16), base + static_cast<int64_t>(b) * 16, bytes,
+                         smem_u32(&full[slot]));
+          ++n;
+          if (++slot == RING_SLOTS) slot = 0, phase ^= 1;
+        }
+      }
+      // no exit with copies in flight
+      for (int i = max(0, n - RING_SLOTS); i < n; ++i)
+        mbar_wait(smem_u32(&full[i % RING_SLOTS]), (i / RING_SLOTS) & 1, status);
+    }
+    __syncwarp();
+  } else {
+    const int t = threadIdx.x;
+    int slot = 0, phase = 0;                                 // the next chunk's slot and parity
+    int live = 0;                                            // tokens taken
+    TokenIn next = token_in(a, row0);
+    for (int64_t row = row0; row < a.tokens; row += step) {
+      const TokenIn tok = next;
+      next = token_in(a, row + step);
+      const TZ* z = static_cast<const TZ*>(a.z) + row * a.ld_z;
+      TG* g = a.g ? static_cast<TG*>(a.g) + row * a.ld_g : nullptr;
+      const int h = shift(row);
+      const int lo = h ? 1 : 0, hi = (V + h) / VE, end = min(w0 + part, (V + h + VE - 1) / VE);
+      if (tok.w == 0.f) {
+        const float zero[VE] = {};
+        if (g)
+          for (int w = w0 + t; w < end; w += RING_TPB) store_edge<TG, VE>(g, w * VE - h, V, zero);
+        if (rank == 0 && t == 0) {
+          a.logp[row] = 0.f;
+          a.terms[row] = 0.f;
+        }
+        continue;
+      }
+      const bool inside = tok.target >= 0 && tok.target < V;
+      float za = __int_as_float(0x7FFFFFFF);
+      if (inside) {
+        Vec<TZ, 1> one;
+        one.load(z + tok.target);
+        za = one.get(0);
+      }
+      const int whole_lo = max(w0, lo), whole_hi = min(end, hi);   // this part's whole words
+
+      // word `at` of the chunk that starts at word w, as float32; false: not in the row
+      const auto fetch = [&](const uint8_t* chunk, int w, int at, float (&v)[VE]) {
+        if (w + at >= whole_lo && w + at < whole_hi) {
+          const uint4 q = *reinterpret_cast<const uint4*>(chunk + at * 16);
+          Vec<TZ, VE> r;
+          r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
+#pragma unroll
+          for (int j = 0; j < VE; ++j) v[j] = r.get(j);
+          return true;
+        }
+        if (w + at >= end) return false;
+        load_edge<TZ, VE>(z, (w + at) * VE - h, V, v);
+        return true;
+      };
+
+      // first pass: running maximum and sum; the lowest float32 stands for
+      // "none yet", so no difference is inf - inf
+      float m = kLowest, s = 0.f;
+      const int slot0 = slot;
+      for (int w = w0; w < end; w += CV) {
+        if (alive) alive = mbar_wait(smem_u32(&full[slot]), phase, status);
+        const uint8_t* chunk = ring + slot * RING_CHUNK;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float v[VE];
+          if (fetch(chunk, w, t + u * RING_TPB, v)) take_in(v, m, s);
+        }
+        if (++slot == RING_SLOTS) slot = 0, phase ^= 1;
+      }
+      const float wm = warp_max(m);
+      s = warp_sum(s * ex2((m - wm) * kLog2e));
+      const int par = live & 1;
+      if (lane < slabs) {
+        st_cluster_f2(smem_u32(&pairs[par][rank * RING_WARPS + warp]), lane, wm, s);
+        mbar_arrive_remote(cluster_map(smem_u32(&xbar[par]), lane));
+      }
+      if (alive) alive = mbar_wait_suspend(smem_u32(&xbar[par]), (live >> 1) & 1, status);
+      ++live;
+      float top = kLowest;
+      for (int i = lane; i < slabs * RING_WARPS; i += 32) top = fmaxf(top, pairs[par][i].x);
+      top = warp_max(top);
+      float total = 0.f;
+      for (int i = lane; i < slabs * RING_WARPS; i += 32) total += pairs[par][i].y * ex2((pairs[par][i].x - top) * kLog2e);
+      total = warp_sum(total);
+      const float lp = (za - top) - logf(total);
+      float l, slope;
+      token_loss(a, row, lp, l, slope);
+      if (rank == 0 && t == 0) {
+        a.logp[row] = lp;
+        a.terms[row] = tok.w * l;
+      }
+
+      // second pass: the gradient, and the chunks are free
+      const float k = a.scale * tok.w * slope;
+      const int at = inside ? static_cast<int>(tok.target) : -VE;
+      const uint64_t tt = f32x2_splat(top), ff = f32x2_splat(-k / total);
+      int sl = slot0;
+      for (int w = w0; w < end; w += CV) {
+        const uint8_t* chunk = ring + sl * RING_CHUNK;
+        if (g) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float v[VE];
+            const int e0 = (w + t + u * RING_TPB) * VE - h;
+            if (fetch(chunk, w, t + u * RING_TPB, v)) {
+              to_gradient(v, tt, ff, at - e0, k);
+              store_edge<TG, VE>(g, e0, V, v);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&empty[sl]));
+        if (++sl == RING_SLOTS) sl = 0;
+      }
+    }
+  }
+  cluster_sync();                                            // no peer writes here any more
+  if (rank == 0) finish_loss(a, static_cast<unsigned>(step));
+}
+
 using namespace mxq_host;
 
 bool valid_type(int t) { return t == MXQ_BF16 || t == MXQ_F32; }
 int type_size(int t) { return t == MXQ_F32 ? 4 : 2; }
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-template <typename TZ, typename TG, int VE, int NV, bool LONG>
+template <typename TZ, typename TG, int VE, int NV, bool LONG, int TPB>
 int launch_policy(const LossArgs& a, int slabs, cudaStream_t st) {
   const int64_t grid = static_cast<int64_t>(a.tokens) * slabs;
   if (grid > 0x7FFFFFFF) return MXQ_ERR_BAD_SHAPE;
-  return launch_pdl_cluster(policy_kernel<TZ, TG, VE, NV, LONG>, dim3(static_cast<unsigned>(grid)), dim3(TPB), 0, st,
+  return launch_pdl_cluster(policy_kernel<TZ, TG, VE, NV, LONG, TPB>, dim3(static_cast<unsigned>(grid)), dim3(TPB), 0, st,
                             slabs, a, slabs);
 }
 
-// The fewest CTAs whose registers hold a row; with few tokens more, until
-// there are two CTAs for every SM or eight to a row.
+// Clusters of `slabs` CTAs that run at once (asked once per device and size).
+template <typename TZ, typename TG>
+int ring_clusters(int slabs) {
+  static std::atomic<int> known[64][MAX_SLABS + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][slabs].load(std::memory_order_relaxed);
+  if (n) return n;
+  auto kern = policy_ring_kernel<TZ, TG>;
+  const int smem = RING_CHUNK * RING_SLOTS;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(slabs * 2 * sm_count());
+  cfg.blockDim = dim3(RING_TPB + 32);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = slabs;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) return 0;
+  known[dev][slabs].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Words of a row of logits, whatever its shift.
+template <typename TZ>
+int64_t row_words(const LossArgs& a) {
+  constexpr int VE = 16 / static_cast<int>(sizeof(TZ));
+  const bool flush = a.ld_z % VE == 0 && reinterpret_cast<uintptr_t>(a.z) % 16 == 0;
+  return (static_cast<int64_t>(a.vocab) + (flush ? 0 : VE - 1) + VE - 1) / VE;
+}
+
+// The ring kernel takes rows of at least a chunk when every CTA gets two
+// tokens or more, in the smallest cluster whose CTAs keep RING_AHEAD chunks
+// of the ring for the next token.  0: not for it.
+template <typename TZ>
+int ring_slabs(const LossArgs& a) {
+  if (static_cast<int64_t>(a.vocab) * sizeof(TZ) < RING_CHUNK) return 0;
+  for (int slabs = 1; slabs <= MAX_SLABS; slabs *= 2)
+    if ((row_words<TZ>(a) + slabs - 1) / slabs <= (RING_SLOTS - RING_AHEAD) * (RING_CHUNK / 16))
+      return static_cast<int64_t>(a.tokens) * slabs >= 4 * sm_count() ? slabs : 0;
+  return 0;
+}
+
+template <typename TZ, typename TG>
+int launch_ring(const LossArgs& a, int slabs, cudaStream_t st) {
+  const int part = static_cast<int>((row_words<TZ>(a) + slabs - 1) / slabs);
+  const int clusters = std::min(a.tokens, ring_clusters<TZ, TG>(slabs));
+  int* status = status_ptr();
+  if (!clusters || !status) return MXQ_ERR_CUDA;
+  return launch_pdl_cluster(policy_ring_kernel<TZ, TG>, dim3(clusters * slabs), dim3(RING_TPB + 32),
+                            RING_CHUNK * RING_SLOTS, st, slabs, a, slabs, part, status);
+}
+
+// Rows of up to 4096 elements in a CTA of four warps; longer ones in the
+// fewest CTAs of sixteen whose registers hold them, and with few tokens in
+// more, until there are two CTAs for every SM or eight to a row.
 template <typename TZ, typename TG, int VE>
 int dispatch_policy(const LossArgs& a, cudaStream_t st) {
   constexpr int NMAX = MAX_E / VE;
   // the words of a row, whatever its shift
   const bool flush = a.ld_z % VE == 0 && reinterpret_cast<uintptr_t>(a.z) / sizeof(TZ) % VE == 0;
   const int64_t nvec = (static_cast<int64_t>(a.vocab) + (flush ? 0 : VE - 1) + VE - 1) / VE;
+  if (nvec <= 128 * NMAX && (nvec <= 512 || a.tokens >= sm_count())) {
+    if (nvec <= 128 * NMAX / 4) return launch_policy<TZ, TG, VE, NMAX / 4, false, 128>(a, 1, st);
+    return launch_policy<TZ, TG, VE, NMAX, false, 128>(a, 1, st);
+  }
+  constexpr int TPB = 512;
   int slabs = static_cast<int>(std::min<int64_t>((nvec + TPB * NMAX - 1) / (TPB * NMAX), MAX_SLABS + 1));
-  if (slabs > MAX_SLABS) return launch_policy<TZ, TG, VE, 1, true>(a, MAX_SLABS, st);
+  if (slabs > MAX_SLABS) return launch_policy<TZ, TG, VE, 1, true, TPB>(a, MAX_SLABS, st);
   while (slabs < MAX_SLABS && static_cast<int64_t>(a.tokens) * slabs < 2 * sm_count() && nvec > TPB * slabs)
     slabs = std::min(MAX_SLABS, 2 * slabs);
   const int64_t nv = (nvec + static_cast<int64_t>(TPB) * slabs - 1) / (static_cast<int64_t>(TPB) * slabs);
-  if (nv <= NMAX / 4) return launch_policy<TZ, TG, VE, NMAX / 4, false>(a, slabs, st);
-  if (nv <= NMAX / 2) return launch_policy<TZ, TG, VE, NMAX / 2, false>(a, slabs, st);
-  return launch_policy<TZ, TG, VE, NMAX, false>(a, slabs, st);
+  if (nv <= NMAX / 4) return launch_policy<TZ, TG, VE, NMAX / 4, false, TPB>(a, slabs, st);
+  if (nv <= NMAX / 2) return launch_policy<TZ, TG, VE, NMAX / 2, false, TPB>(a, slabs, st);
+  return launch_policy<TZ, TG, VE, NMAX, false, TPB>(a, slabs, st);
 }
 
 template <typename TZ, typename TG>
 int policy(const LossArgs& a, cudaStream_t st) {
   constexpr int VE = sizeof(TZ) == 2 && sizeof(TG) == 2 ? 8 : 4;
+  constexpr int RVE = 16 / static_cast<int>(sizeof(TZ));
   // whole words on both sides: every row of the gradient starts at the same
-  // element of its VE-element word as the row of logits
-  const bool same = !a.g || ((a.ld_z - a.ld_g) % VE == 0 &&
-                             (reinterpret_cast<uintptr_t>(a.z) / sizeof(TZ)) % VE ==
-                                 (reinterpret_cast<uintptr_t>(a.g) / sizeof(TG)) % VE);
-  return same ? dispatch_policy<TZ, TG, VE>(a, st) : dispatch_policy<TZ, TG, 1>(a, st);
+  // element of its word as the row of logits
+  const auto same = [&](int ve) {
+    return !a.g || ((a.ld_z - a.ld_g) % ve == 0 && (reinterpret_cast<uintptr_t>(a.z) / sizeof(TZ)) % ve ==
+                                                       (reinterpret_cast<uintptr_t>(a.g) / sizeof(TG)) % ve);
+  };
+  if (same(RVE))
+    if (const int slabs = ring_slabs<TZ>(a)) return launch_ring<TZ, TG>(a, slabs, st);
+  return same(VE) ? dispatch_policy<TZ, TG, VE>(a, st) : dispatch_policy<TZ, TG, 1>(a, st);
 }
 
 }  // namespace

@@ -111,6 +111,13 @@ __device__ __forceinline__ float tree_sum(const float (&v)[N]) {
   return t[0];
 }
 
+// a * b + c on packed pairs, one rounding each.
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // One cluster barrier, in two halves: what a thread did before the arrive is
 // visible to every thread of the cluster after the wait.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
