@@ -289,28 +289,23 @@ __device__ __forceinline__ void take_in(const float (&v)[VE], float& m, float& s
   s *= ex2((m - top) * kLog2e);
   m = top;
   const uint64_t mm = f32x2_splat(m), l2e = f32x2_splat(kLog2e);
-  uint64_t acc = f32x2_pack(s, 0.f);
+  float e[VE];
 #pragma unroll
-  for (int j = 0; j < VE; j += 2) {
-    float x, y;
-    exp_pair(v[j], v[j + 1], mm, l2e, x, y);
-    acc = f32x2_add(acc, f32x2_pack(x, y));
-  }
-  float x, y;
-  f32x2_unpack(acc, x, y);
-  s = x + y;
+  for (int j = 0; j < VE; j += 2) exp_pair(v[j], v[j + 1], mm, l2e, e[j], e[j + 1]);
+  s += tree_sum(e);
 }
 
 // The gradient's VE elements in place of the logits: exp(v - top) * f, and k
 // more at the target.
 template <int VE>
-__device__ __forceinline__ void to_gradient(float (&v)[VE], uint64_t top, uint64_t f, int target, float k) {
+__device__ __forceinline__ void to_gradient(float (&v)[VE], uint64_t top, float f, int target, float k) {
   const uint64_t l2e = f32x2_splat(kLog2e);
 #pragma unroll
   for (int j = 0; j < VE; j += 2) {
     float x, y;
     exp_pair(v[j], v[j + 1], top, l2e, x, y);
-    f32x2_unpack(f32x2_mul(f32x2_pack(x, y), f), v[j], v[j + 1]);
+    v[j] = x * f;
+    v[j + 1] = y * f;
   }
   if (static_cast<unsigned>(target) < static_cast<unsigned>(VE)) {
 #pragma unroll
@@ -348,8 +343,8 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
       mbar_init(smem_u32(&full[i]), 1);
       mbar_init(smem_u32(&empty[i]), RING_WARPS);
     }
-    mbar_init(smem_u32(&xbar[0]), slabs * RING_WARPS);
-    mbar_init(smem_u32(&xbar[1]), slabs * RING_WARPS);
+    mbar_init(smem_u32(&xbar[0]), 1);
+    mbar_init(smem_u32(&xbar[1]), 1);
     fence_mbar_init();
   }
   cluster_sync();
@@ -380,7 +375,7 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
         const int lo = h ? 1 : 0, hi = (V + h) / VE, end = min(w0 + part, (V + h + VE - 1) / VE);
         for (int w = w0; w < end; w += CV) {
           if (n >= RING_SLOTS) {
-            alive = mbar_wait(smem_u32(&empty[slot]), phase, status);
+            alive = mbar_wait_sleep(smem_u32(&empty[slot]), phase, status);
             if (!alive) break;
           }
           const int b = max(w, lo), e = min(min(w + CV, end), hi);
@@ -429,18 +424,18 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
       }
       const int whole_lo = max(w0, lo), whole_hi = min(end, hi);   // this part's whole words
 
-      // word `at` of the chunk that starts at word w, as float32; false: not in the row
-      const auto fetch = [&](const uint8_t* chunk, int w, int at, float (&v)[VE]) {
-        if (w + at >= whole_lo && w + at < whole_hi) {
-          const uint4 q = *reinterpret_cast<const uint4*>(chunk + at * 16);
-          Vec<TZ, VE> r;
-          r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
+      const auto whole = [&](const uint8_t* chunk, int at, float (&v)[VE]) {
+        const uint4 q = *reinterpret_cast<const uint4*>(chunk + at * 16);
+        Vec<TZ, VE> r;
+        r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
 #pragma unroll
-          for (int j = 0; j < VE; ++j) v[j] = r.get(j);
-          return true;
-        }
+        for (int j = 0; j < VE; ++j) v[j] = r.get(j);
+      };
+      // word `at` of the chunk that starts at word w; false: not in the row
+      const auto fetch = [&](const uint8_t* chunk, int w, int at, float (&v)[VE]) {
         if (w + at >= end) return false;
-        load_edge<TZ, VE>(z, (w + at) * VE - h, V, v);
+        if (w + at >= whole_lo && w + at < whole_hi) whole(chunk, at, v);
+        else load_edge<TZ, VE>(z, (w + at) * VE - h, V, v);
         return true;
       };
 
@@ -449,23 +444,30 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
       float m = kLowest, s = 0.f;
       const int slot0 = slot;
       for (int w = w0; w < end; w += CV) {
-        if (alive) alive = mbar_wait(smem_u32(&full[slot]), phase, status);
+        if (alive) alive = mbar_wait_sleep(smem_u32(&full[slot]), phase, status);
         const uint8_t* chunk = ring + slot * RING_CHUNK;
+        if (w >= whole_lo && w + CV <= whole_hi) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float v[VE];
-          if (fetch(chunk, w, t + u * RING_TPB, v)) take_in(v, m, s);
+          for (int u = 0; u < U; ++u) {
+            float v[VE];
+            whole(chunk, t + u * RING_TPB, v);
+            take_in(v, m, s);
+          }
+        } else {
+          for (int u = 0; u < U; ++u) {
+            float v[VE];
+            if (fetch(chunk, w, t + u * RING_TPB, v)) take_in(v, m, s);
+          }
         }
         if (++slot == RING_SLOTS) slot = 0, phase ^= 1;
       }
       const float wm = warp_max(m);
       s = warp_sum(s * ex2((m - wm) * kLog2e));
       const int par = live & 1;
-      if (lane < slabs) {
-        st_cluster_f2(smem_u32(&pairs[par][rank * RING_WARPS + warp]), lane, wm, s);
-        mbar_arrive_remote(cluster_map(smem_u32(&xbar[par]), lane));
-      }
-      if (alive) alive = mbar_wait_suspend(smem_u32(&xbar[par]), (live >> 1) & 1, status);
+      if (t == 0) mbar_arrive_expect_tx(smem_u32(&xbar[par]), slabs * RING_WARPS * 8);
+      if (lane < slabs)
+        st_async_f2(smem_u32(&pairs[par][rank * RING_WARPS + warp]), smem_u32(&xbar[par]), lane, wm, s);
+      if (alive) alive = mbar_wait_sleep(smem_u32(&xbar[par]), (live >> 1) & 1, status);
       ++live;
       float top = kLowest;
       for (int i = lane; i < slabs * RING_WARPS; i += 32) top = fmaxf(top, pairs[par][i].x);
@@ -484,17 +486,26 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
       // second pass: the gradient, and the chunks are free
       const float k = a.scale * tok.w * slope;
       const int at = inside ? static_cast<int>(tok.target) : -VE;
-      const uint64_t tt = f32x2_splat(top), ff = f32x2_splat(-k / total);
+      const uint64_t tt = f32x2_splat(top);
+      const float f = -k / total;
       int sl = slot0;
       for (int w = w0; w < end; w += CV) {
         const uint8_t* chunk = ring + sl * RING_CHUNK;
-        if (g) {
+        if (g && w >= whole_lo && w + CV <= whole_hi) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             float v[VE];
             const int e0 = (w + t + u * RING_TPB) * VE - h;
+            whole(chunk, t + u * RING_TPB, v);
+            to_gradient(v, tt, f, at - e0, k);
+            store_vec<TG, VE>(g + e0, v);
+          }
+        } else if (g) {
+          for (int u = 0; u < U; ++u) {
+            float v[VE];
+            const int e0 = (w + t + u * RING_TPB) * VE - h;
             if (fetch(chunk, w, t + u * RING_TPB, v)) {
-              to_gradient(v, tt, ff, at - e0, k);
+              to_gradient(v, tt, f, at - e0, k);
               store_edge<TG, VE>(g, e0, V, v);
             }
           }

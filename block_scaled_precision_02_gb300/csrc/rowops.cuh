@@ -129,6 +129,29 @@ __device__ __forceinline__ void st_cluster_f2(uint32_t addr, uint32_t rank, floa
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_map(addr, rank)), "f"(a), "f"(b) : "memory");
 }
 
+// The same as an asynchronous store that counts its 8 bytes on the target
+// CTA's mbarrier at `bar`: no fence, so the sender's earlier global stores
+// need not have landed.
+__device__ __forceinline__ void st_async_f2(uint32_t addr, uint32_t bar, uint32_t rank, float a, float b) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                   cluster_map(addr, rank)),
+               "f"(a), "f"(b), "r"(cluster_map(bar, rank))
+               : "memory");
+}
+
+// Bounded wait for phases that take microseconds: the thread sleeps in the
+// barrier unit instead of polling.
+__device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, int* status) {
+  if (mbar_try_wait_sleep(bar, parity, 2000u)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 20000u))
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      record_timeout(status);
+      return false;
+    }
+  return true;
+}
+
 // Scale byte of an MX block whose largest magnitude has the bits `ab`, and the
 // multiplier 2^-e of its elements; a block that holds NaN or an infinity gets
 // 0xFF (and zero codes: `bad` of mx_codes).
