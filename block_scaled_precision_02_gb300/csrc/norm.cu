@@ -186,6 +186,123 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_row_kernel(const NormA
   }
 }
 
+// ---------------------------------------------------------------- many rows
+// Groups of threads in a persistent CTA, each with a ring of whole rows in
+// shared memory that one of its threads fills by bulk copies ahead of use.
+// A row moves from its slot to registers; the barrier of the group's
+// reduction says that all have read it, and the slot takes the group's next
+// row but RING - 1.  Loads stay in flight through reductions and stores,
+// which registers alone do not allow (the row kernel's CTAs load, reduce and
+// store in turn).
+constexpr int MAX_GROUPS = 32, MAX_STAGES = 8;
+constexpr int kRingBytes = 160 * 1024;     // leaves L1 room for weight and bias
+
+__device__ __forceinline__ void group_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+}
+
+// After a wait has given up: no exit while copies may be in flight.  `slot`
+// and `phase` are the next slot to be used and its parity.
+__device__ __forceinline__ void await_ring(const uint64_t* full, int stages, int slot, int phase, int* status) {
+  for (int i = 0; i < stages; ++i) mbar_wait(smem_u32(full + i), i >= slot ? phase : phase ^ 1, status);
+}
+
+// One row into a slot.
+template <typename T>
+__device__ __forceinline__ void issue_row(uint8_t* slot, uint32_t bar, const void* x, int64_t ld, int64_t row, int cols) {
+  bulk_load_1d(smem_u32(slot), static_cast<const T*>(x) + row * ld, static_cast<uint32_t>(cols * sizeof(T)), bar);
+}
+
+template <typename TX, typename TY, int VE, int NV>
+__global__ void __launch_bounds__(1024, 1) norm_ring_kernel(const NormArgs a, int G, int stages, int* status) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float2 part[MAX_GROUPS][2][32];
+  __shared__ __align__(8) uint64_t full[MAX_GROUPS][MAX_STAGES];
+  const int lane = threadIdx.x & 31;
+  const int P = blockDim.x / G, g = threadIdx.x / G, t = threadIdx.x - g * G;
+  const int gw = t >> 5, wpg = G >> 5;
+  if (t == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[g][i]), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dep_wait();
+  const int nvec = a.cols / VE;
+  const int row_bytes = a.cols * static_cast<int>(sizeof(TX));
+  uint8_t* slots = ring + static_cast<size_t>(g) * stages * row_bytes;
+  const int64_t gi = static_cast<int64_t>(blockIdx.x) * P + g, step = static_cast<int64_t>(gridDim.x) * P;
+  const float inv_c = 1.f / static_cast<float>(a.cols);
+  const int n_mine = warp_count<VE, NV>(a.cols, G, gw), n_lane = lane < wpg ? warp_count<VE, NV>(a.cols, G, lane) : 0;
+  const float inv_mine = n_mine ? 1.f / static_cast<float>(n_mine) : 0.f;
+  const float inv_lane = n_lane ? 1.f / static_cast<float>(n_lane) : 0.f;
+  bool alive = true;
+
+  if (t == 0)
+    for (int i = 0; i < stages; ++i)
+      if (gi + i * step < a.rows) {
+        mbar_arrive_expect_tx(smem_u32(&full[g][i]), row_bytes);
+        issue_row<TX>(slots + i * row_bytes, smem_u32(&full[g][i]), a.x, a.ld, gi + i * step, a.cols);
+      }
+
+  int slot = 0, phase = 0, buf = 0;
+  for (int64_t row = gi; row < a.rows; row += step) {
+    if (alive) alive = mbar_wait(smem_u32(&full[g][slot]), phase, status);
+    float v[NV][VE], s[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      Vec<TX, VE> r;
+      r.fill(0);
+      if (k * G + t < nvec) r.load(reinterpret_cast<const TX*>(slots + slot * row_bytes) + (k * G + t) * VE);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) v[k][j] = r.get(j);
+      s[k] = tree_sum(v[k]);
+    }
+    float sum = warp_sum(tree_sum(s));
+    float mean, m2;
+    if (wpg == 1) {
+      __syncwarp();
+      mean = sum * inv_c;
+      m2 = warp_sum(sq_dev<VE, NV>(v, mean, t, G, nvec));
+    } else {
+      m2 = warp_sum(sq_dev<VE, NV>(v, sum * inv_mine, t, G, nvec));
+      if (lane == 0) part[g][buf][gw] = make_float2(sum, m2);
+      group_barrier(g, G);
+    }
+    if (t == 0) {                                        // the slot has been read by all
+      const int64_t next = row + stages * step;
+      if (next < a.rows) {
+        mbar_arrive_expect_tx(smem_u32(&full[g][slot]), row_bytes);
+        issue_row<TX>(slots + slot * row_bytes, smem_u32(&full[g][slot]), a.x, a.ld, next, a.cols);
+      }
+    }
+    if (++slot == stages) slot = 0, phase ^= 1;
+    if (wpg > 1) {
+      const float2 pw = lane < wpg ? part[g][buf][lane] : make_float2(0.f, 0.f);
+      buf ^= 1;
+      mean = warp_sum(pw.x) * inv_c;
+      const float d = n_lane ? pw.x * inv_lane - mean : 0.f;
+      m2 = warp_sum(pw.y + static_cast<float>(n_lane) * d * d);
+    }
+    const float rstd = 1.f / sqrtf(m2 * inv_c + a.eps);
+    if (t == 0) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+    TY* y = static_cast<TY*>(a.y) + row * a.cols;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int at = (k * G + t) * VE;
+      if (at >= a.cols) continue;
+      float w[VE], b[VE], o[VE];
+      load_affine<VE>(a, at, w, b);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) o[j] = norm_value(v[k][j], mean, rstd, w[j], b[j]);
+      store_vec<TY, VE>(y + at, o);
+    }
+  }
+  if (!alive && t == 0) await_ring(full[g], stages, slot, phase, status);
+}
+
 // Block-wide sum over 1024 threads (all threads get it); `red` holds 32 floats.
 __device__ __forceinline__ float block_sum_1024(float v, float* red) {
   v = warp_sum(v);
@@ -566,6 +683,179 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) 
   }
 }
 
+// The same for many rows, through rings of rows (x and dy side by side in a
+// slot).  Each thread keeps NV * VE columns' sums; with 32 of them the
+// weights stay in shared memory.
+template <typename TX, typename TD, int VE, int NV>
+__global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const BwdArgs a, int G, int stages, int* status) {
+  constexpr int E = VE * NV;
+  constexpr bool KEEP = E <= 16;             // h and g live in registers between the passes, else x and dy do
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float red[16][2][2][16];        // [group][buffer][sum][warp]
+  __shared__ __align__(8) uint64_t full[16][MAX_STAGES];
+  const int lane = threadIdx.x & 31;
+  const int P = blockDim.x / G, g = threadIdx.x / G, t = threadIdx.x - g * G;
+  const int gw = t >> 5, wpg = G >> 5;
+  if (t == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[g][i]), 1);
+    fence_mbar_init();
+  }
+  const int nvec = a.cols / VE;
+  const int xb = a.cols * static_cast<int>(sizeof(TX)), db = a.cols * static_cast<int>(sizeof(TD));
+  float* ws = reinterpret_cast<float*>(ring);                       // !KEEP: the weights
+  uint8_t* slots = ring + (KEEP ? 0 : a.cols * 4) + static_cast<size_t>(g) * stages * (xb + db);
+  grid_dep_wait();
+  float w[KEEP ? NV : 1][VE], aw[NV][VE], ab[NV][VE];
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int j = 0; j < VE; ++j) aw[k][j] = ab[k][j] = 0.f;
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (int j = 0; j < VE; ++j) w[k][j] = 1.f;
+      if (a.w && k * G + t < nvec) load_param<VE>(a.w, a.w_f32, (k * G + t) * VE, w[k]);
+    }
+  } else {
+    for (int i = threadIdx.x; i < a.cols; i += blockDim.x) {
+      float one[1] = {1.f};
+      if (a.w) load_param<1>(a.w, a.w_f32, i, one);
+      ws[i] = one[0];
+    }
+  }
+  __syncthreads();
+  const float inv_c = 1.f / static_cast<float>(a.cols);
+  const int64_t gi = static_cast<int64_t>(blockIdx.x) * P + g, step = static_cast<int64_t>(gridDim.x) * P;
+  bool alive = true;
+  const auto issue = [&](int slot, int64_t row) {
+    const uint32_t bar = smem_u32(&full[g][slot]);
+    mbar_arrive_expect_tx(bar, xb + db);
+    issue_row<TX>(slots + slot * (xb + db), bar, a.x, a.ld_x, row, a.cols);
+    issue_row<TD>(slots + slot * (xb + db) + xb, bar, a.dy, a.ld_dy, row, a.cols);
+  };
+  if (t == 0)
+    for (int i = 0; i < stages; ++i)
+      if (gi + i * step < a.rows) issue(i, gi + i * step);
+
+  int slot = 0, phase = 0, buf = 0;
+  float mean_n = gi < a.rows ? a.mean[gi] : 0.f, rstd_n = gi < a.rows ? a.rstd[gi] : 0.f;
+  for (int64_t row = gi; row < a.rows; row += step) {
+    const float mean = mean_n, rstd = rstd_n;
+    if (row + step < a.rows) mean_n = a.mean[row + step], rstd_n = a.rstd[row + step];
+    if (alive) alive = mbar_wait(smem_u32(&full[g][slot]), phase, status);
+    const uint8_t* sx = slots + slot * (xb + db);
+    Vec<TX, VE> xr[NV];
+    Vec<TD, VE> dr[NV];
+    float h[KEEP ? NV : 1][VE], u[KEEP ? NV : 1][VE];
+    float s1[NV], s2[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      xr[k].fill(0);
+      dr[k].fill(0);
+      if (k * G + t < nvec) {
+        xr[k].load(reinterpret_cast<const TX*>(sx) + (k * G + t) * VE);
+        dr[k].load(reinterpret_cast<const TD*>(sx + xb) + (k * G + t) * VE);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float wk[VE], p[VE], q[VE];
+      if constexpr (KEEP) {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) wk[j] = w[k][j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) wk[j] = 0.f;
+        if (k * G + t < nvec) load_param<VE>(ws, 1, (k * G + t) * VE, wk);
+      }
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const float hj = (xr[k].get(j) - mean) * rstd, d = dr[k].get(j);
+        p[j] = d * wk[j];
+        q[j] = p[j] * hj;
+        aw[k][j] = fmaf(d, hj, aw[k][j]);
+        ab[k][j] += d;
+        if constexpr (KEEP) h[k][j] = hj, u[k][j] = p[j];
+      }
+      s1[k] = tree_sum(p);
+      s2[k] = tree_sum(q);
+    }
+    // both sums in one butterfly: the lower half of the warp takes the first,
+    // the upper half the second
+    const float c1 = tree_sum(s1), c2 = tree_sum(s2);
+    const bool up = lane & 16;
+    float v = (up ? c2 : c1) + __shfl_xor_sync(0xFFFFFFFFu, up ? c1 : c2, 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (wpg > 1) {
+      if ((lane & 15) == 0) red[g][buf][lane >> 4][gw] = v;
+      group_barrier(g, G);
+    } else {
+      __syncwarp();
+    }
+    if (t == 0 && row + stages * step < a.rows) issue(slot, row + stages * step);   // read by all
+    if (++slot == stages) slot = 0, phase ^= 1;
+    if (wpg > 1) {
+      v = (lane & 15) < wpg ? red[g][buf][lane >> 4][lane & 15] : 0.f;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      buf ^= 1;
+    }
+    const float m1 = __shfl_sync(0xFFFFFFFFu, v, 0) * inv_c, m2 = __shfl_sync(0xFFFFFFFFu, v, 16) * inv_c;
+    TX* dx = static_cast<TX*>(a.dx) + row * a.cols;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (k * G + t >= nvec) continue;
+      float o[VE];
+      if constexpr (KEEP) {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) o[j] = fmaf(h[k][j], -m2, u[k][j] - m1) * rstd;
+      } else {
+        float wk[VE];
+        load_param<VE>(ws, 1, (k * G + t) * VE, wk);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const float hj = (xr[k].get(j) - mean) * rstd;
+          o[j] = fmaf(hj, -m2, dr[k].get(j) * wk[j] - m1) * rstd;
+        }
+      }
+      store_vec<TX, VE>(dx + (k * G + t) * VE, o);
+    }
+  }
+  if (!alive && t == 0) await_ring(full[g], stages, slot, phase, status);
+  if (!a.part) return;
+  float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+  float* comb = reinterpret_cast<float*>(ring);
+  for (int i = 1; i < P; ++i) {              // the groups of the CTA, in their order
+    __syncthreads();                         // (every copy has been waited for: the ring is free)
+    if (g == i)
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          comb[(2 * (k * VE + j)) * G + t] = aw[k][j];
+          comb[(2 * (k * VE + j) + 1) * G + t] = ab[k][j];
+        }
+    __syncthreads();
+    if (g == 0)
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          aw[k][j] += comb[(2 * (k * VE + j)) * G + t];
+          ab[k][j] += comb[(2 * (k * VE + j) + 1) * G + t];
+        }
+  }
+  if (g) return;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    if (k * G + t >= nvec) continue;
+    store_vec<float, VE>(out + (k * G + t) * VE, aw[k]);
+    store_vec<float, VE>(out + a.cols + (k * G + t) * VE, ab[k]);
+  }
+}
+
 // Rows too long for the registers: their two sums first ...
 template <typename TX, typename TD>
 __global__ void __launch_bounds__(1024) norm_bwd_long_rows_kernel(const BwdArgs a) {
@@ -649,6 +939,7 @@ using namespace mxq_host;
 
 constexpr int kMaxRowElems = 32768;       // forward: one CTA's registers
 constexpr int kMaxBwdElems = 16384;       // backward: data and two column sums
+constexpr int kBwdRingBytes = 208 * 1024;
 
 bool valid_type(int t) { return t == MXQ_BF16 || t == MXQ_F32; }
 int type_size(int t) { return t == MXQ_F32 ? 4 : 2; }
@@ -680,12 +971,37 @@ int dispatch_row(const NormArgs& a, cudaStream_t st) {
   return launch_row<TX, OUT, VE, MAXV>(a, warp, threads, st);
 }
 
+// Rings for rows of whole 16-byte words, 1 KiB to 64 KiB each, when every
+// group gets four or more.  0: not taken.
+template <typename TX, typename TY>
+bool try_norm_ring(const NormArgs& a, int* rc, cudaStream_t st) {
+  constexpr int VE = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
+  constexpr int NV = 16 / VE;
+  const int nvec = a.cols / VE;
+  const int row_bytes = a.cols * static_cast<int>(sizeof(TX));
+  if (!a.y || row_bytes < 1024 || nvec > 1024 * NV || a.ld * sizeof(TX) % 16 || row_bytes % 16) return false;
+  const int G = round_up((nvec + NV - 1) / NV, 32), P = 1024 / G;
+  const int stages = std::min(MAX_STAGES, kRingBytes / (P * row_bytes));
+  if (stages < 2 || a.rows < 4ll * P * sm_count()) return false;
+  int* status = status_ptr();
+  auto kern = norm_ring_kernel<TX, TY, VE, NV>;
+  const int smem = P * stages * row_bytes;
+  if (!status || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
+    *rc = MXQ_ERR_CUDA;
+  else
+    *rc = launch_pdl(kern, dim3(sm_count()), dim3(P * G), smem, st, a, G, stages, status);
+  return true;
+}
+
 template <typename TX, int OUT>
 int norm_rows(const NormArgs& a, bool vec, cudaStream_t st) {
   constexpr int VE = sizeof(TX) == 2 && OUT != OUT_F32 ? 8 : 4;
   if constexpr (OUT < 0) {
     if (a.cols > kMaxRowElems) return launch_pdl(norm_long_kernel<TX, OUT>, dim3(a.rows), dim3(1024), 0, st, a);
     if (!vec) return dispatch_row<TX, OUT, 1>(a, st);
+    using TY = typename std::conditional<OUT == OUT_F32, float, __nv_bfloat16>::type;
+    int rc;
+    if (try_norm_ring<TX, TY>(a, &rc, st)) return rc;
   }
   return dispatch_row<TX, OUT, VE>(a, st);
 }
@@ -755,13 +1071,41 @@ int launch_bwd(const BwdArgs& a, int G, int& parts, cudaStream_t st) {
   const size_t smem = P > 1 ? static_cast<size_t>(2) * VE * NV * G * sizeof(float) : 0;
   const int64_t groups = (a.rows + P - 1) / P;
   const int most = std::min(bwd_parts(), std::max(1, 2048 / threads) * sm_count());
-  // four rows a step once every CTA has four steps' worth of them
-  if constexpr (VE * NV <= 8) if (groups >= 4ll * most) {
-    parts = static_cast<int>(std::min<int64_t>(most, (groups + 3) / 4));
-    return launch_pdl(norm_bwd_kernel<TX, TD, VE, NV, 4>, dim3(parts), dim3(threads), smem, st, a, G);
-  }
   parts = static_cast<int>(std::min<int64_t>(most, groups));
   return launch_pdl(norm_bwd_kernel<TX, TD, VE, NV, 1>, dim3(parts), dim3(threads), smem, st, a, G);
+}
+
+// Rings while a slot (x and dy) is whole 16-byte words and every group gets
+// two rows or more.
+template <typename TX, typename TD, int VE, int NV>
+bool launch_bwd_ring(const BwdArgs& a, int G, int P, int* rc, int& parts, cudaStream_t st) {
+  const int slot = a.cols * static_cast<int>(sizeof(TX) + sizeof(TD));
+  const int fixed = VE * NV <= 16 ? 0 : a.cols * 4;
+  const int stages = std::min(MAX_STAGES, (kBwdRingBytes - fixed) / (P * slot));
+  if (stages < 2) return false;
+  int* status = status_ptr();
+  auto kern = norm_bwd_ring_kernel<TX, TD, VE, NV>;
+  const int smem = std::max(fixed + P * stages * slot, P > 1 ? 2 * VE * NV * G * 4 : 0);
+  parts = sm_count();
+  if (!status || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdRingBytes) != cudaSuccess)
+    *rc = MXQ_ERR_CUDA;
+  else
+    *rc = launch_pdl(kern, dim3(parts), dim3(P * G), smem, st, a, G, stages, status);
+  return true;
+}
+
+template <typename TX, typename TD, int VE>
+bool try_bwd_ring(const BwdArgs& a, int* rc, int& parts, cudaStream_t st) {
+  constexpr int N1 = 16 / VE, N2 = 32 / VE;
+  const int nvec = a.cols / VE;
+  if (a.cols * sizeof(TX) % 16 || a.cols * sizeof(TD) % 16 || a.ld_x * sizeof(TX) % 16 || a.ld_dy * sizeof(TD) % 16)
+    return false;
+  const int nv = nvec <= 512 * N1 ? N1 : N2;
+  if (nvec > 512 * N2) return false;
+  const int G = round_up((nvec + nv - 1) / nv, 32), P = 512 / G;
+  if (a.rows < 2ll * P * sm_count()) return false;
+  return nv == N1 ? launch_bwd_ring<TX, TD, VE, N1>(a, G, P, rc, parts, st)
+                  : launch_bwd_ring<TX, TD, VE, N2>(a, G, P, rc, parts, st);
 }
 
 template <typename TX, typename TD, int VE>
@@ -777,6 +1121,8 @@ template <typename TX, typename TD>
 int norm_bwd(const BwdArgs& a, bool vec, int& parts, cudaStream_t st) {
   if (a.cols <= kMaxBwdElems) {
     constexpr int VE = sizeof(TX) == 2 && sizeof(TD) == 2 ? 8 : 4;
+    int rc;
+    if (vec && try_bwd_ring<TX, TD, VE>(a, &rc, parts, st)) return rc;
     return vec ? dispatch_bwd<TX, TD, VE>(a, parts, st) : dispatch_bwd<TX, TD, 1>(a, parts, st);
   }
   const int rc = launch_pdl(norm_bwd_long_rows_kernel<TX, TD>, dim3(a.rows), dim3(1024), 0, st, a);
