@@ -190,12 +190,14 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_row_kernel(const NormA
 // Groups of threads in a persistent CTA, each with a ring of whole rows in
 // shared memory that one of its threads fills by bulk copies ahead of use.
 // A row moves from its slot to registers; the barrier of the group's
-// reduction says that all have read it, and the slot takes the group's next
-// row but RING - 1.  Loads stay in flight through reductions and stores,
-// which registers alone do not allow (the row kernel's CTAs load, reduce and
-// store in turn).
-constexpr int MAX_GROUPS = 32, MAX_STAGES = 8;
-constexpr int kRingBytes = 160 * 1024;     // leaves L1 room for weight and bias
+// reduction says that all have read it, and the slot takes a later row of the
+// group.  Loads stay in flight through reductions and stores, which registers
+// alone do not allow (the row kernel's CTAs load, reduce and store in turn).
+// A thread holds up to 32 elements, so the reductions' shuffles cost little
+// against the elements' own arithmetic, which runs on packed pairs.
+constexpr int MAX_GROUPS = 16, MAX_STAGES = 8;
+constexpr int RING_THREADS = 512;
+constexpr int kRingBytes = 216 * 1024;
 
 __device__ __forceinline__ void group_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
@@ -207,16 +209,99 @@ __device__ __forceinline__ void await_ring(const uint64_t* full, int stages, int
   for (int i = 0; i < stages; ++i) mbar_wait(smem_u32(full + i), i >= slot ? phase : phase ^ 1, status);
 }
 
-// One row into a slot.
+// A matrix whose rows go through slots.  Bulk copies move whole 16-byte words,
+// so a row that starts or ends inside one is copied with its neighbours'
+// bytes in those words; only where such a word would leave the matrix (its
+// first and last row) nothing is copied and the row is read in place.
 template <typename T>
-__device__ __forceinline__ void issue_row(uint8_t* slot, uint32_t bar, const void* x, int64_t ld, int64_t row, int cols) {
-  bulk_load_1d(smem_u32(slot), static_cast<const T*>(x) + row * ld, static_cast<uint32_t>(cols * sizeof(T)), bar);
+struct RowSource {
+  const T* base;
+  int64_t ld;
+  int cols, rows;
+
+  __device__ __forceinline__ const T* row(int64_t r) const { return base + r * ld; }
+  __device__ __forceinline__ int head(int64_t r) const { return static_cast<int>(reinterpret_cast<uintptr_t>(row(r)) & 15); }
+  __device__ __forceinline__ uint32_t bytes(int64_t r) const {
+    return static_cast<uint32_t>((head(r) + cols * static_cast<int>(sizeof(T)) + 15) & ~15);
+  }
+  __device__ __forceinline__ bool copied(int64_t r) const {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(row(r)) - head(r);
+    return lo >= reinterpret_cast<uintptr_t>(base) && lo + bytes(r) <= reinterpret_cast<uintptr_t>(row(rows - 1) + cols);
+  }
+  __device__ __forceinline__ void issue(uint8_t* slot, uint32_t bar, int64_t r) const {
+    bulk_load_1d(smem_u32(slot), reinterpret_cast<const uint8_t*>(row(r)) - head(r), bytes(r), bar);
+  }
+};
+
+// Bytes of a slot for rows of `row_bytes`.
+__host__ __device__ constexpr int slot_bytes(int row_bytes, bool whole) { return (row_bytes + 15) / 16 * 16 + (whole ? 0 : 16); }
+
+// Weight and bias as float32 in shared memory.  Vectors of four or eight
+// elements read them as 16-byte words without bank conflicts: the second
+// halves of eight-element vectors have a plane of their own.  Single elements
+// read (w, b) pairs.
+template <int VE>
+__device__ __forceinline__ int plane_at(int e, int cols) {
+  if constexpr (VE == 8) return ((e >> 2) & 1) * (cols / 2) + (e >> 3) * 4 + (e & 3);
+  return e;
+}
+template <int VE>
+__device__ __forceinline__ void stage_affine(const NormArgs& a, float* ws) {
+  for (int i = threadIdx.x; i < a.cols; i += blockDim.x) {
+    float w[1], b[1];
+    load_affine<1>(a, i, w, b);
+    if constexpr (VE == 1) {
+      ws[2 * i] = w[0];
+      ws[2 * i + 1] = b[0];
+    } else {
+      ws[plane_at<VE>(i, a.cols)] = w[0];
+      ws[a.cols + plane_at<VE>(i, a.cols)] = b[0];
+    }
+  }
+}
+template <int VE>
+__device__ __forceinline__ void staged(const float* ws, int at, int cols, float (&w)[VE]) {
+#pragma unroll
+  for (int i = 0; i < VE; i += 4) {
+    const float4 t = *reinterpret_cast<const float4*>(ws + plane_at<VE>(at + i, cols));
+    w[i] = t.x, w[i + 1] = t.y, w[i + 2] = t.z, w[i + 3] = t.w;
+  }
+}
+
+// Sum of VE elements, and of their squared distances from m.
+template <int VE>
+__device__ __forceinline__ float vec_sum(const float (&v)[VE]) {
+  if constexpr (VE == 1) return v[0];
+  else {
+    uint64_t p = f32x2_pack(v[0], v[1]);
+#pragma unroll
+    for (int j = 2; j < VE; j += 2) p = f32x2_add(p, f32x2_pack(v[j], v[j + 1]));
+    float x, y;
+    f32x2_unpack(p, x, y);
+    return x + y;
+  }
+}
+template <int VE>
+__device__ __forceinline__ float vec_sq_dev(const float (&v)[VE], float m) {
+  if constexpr (VE == 1) return (v[0] - m) * (v[0] - m);
+  else {
+    const uint64_t mm = f32x2_splat(m);
+    uint64_t d = f32x2_sub(f32x2_pack(v[0], v[1]), mm), p = f32x2_mul(d, d);
+#pragma unroll
+    for (int j = 2; j < VE; j += 2) {
+      d = f32x2_sub(f32x2_pack(v[j], v[j + 1]), mm);
+      p = f32x2_fma(d, d, p);
+    }
+    float x, y;
+    f32x2_unpack(p, x, y);
+    return x + y;
+  }
 }
 
 template <typename TX, typename TY, int VE, int NV>
-__global__ void __launch_bounds__(1024, 1) norm_ring_kernel(const NormArgs a, int G, int stages, int* status) {
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormArgs a, int G, int stages, int* status) {
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ float2 part[MAX_GROUPS][2][32];
+  __shared__ float2 part[MAX_GROUPS][2][16];
   __shared__ __align__(8) uint64_t full[MAX_GROUPS][MAX_STAGES];
   const int lane = threadIdx.x & 31;
   const int P = blockDim.x / G, g = threadIdx.x / G, t = threadIdx.x - g * G;
@@ -225,63 +310,73 @@ __global__ void __launch_bounds__(1024, 1) norm_ring_kernel(const NormArgs a, in
     for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[g][i]), 1);
     fence_mbar_init();
   }
-  __syncthreads();
   grid_dep_wait();
+  float* ws = reinterpret_cast<float*>(ring);
+  stage_affine<VE>(a, ws);
+  __syncthreads();
+  const RowSource<TX> src{static_cast<const TX*>(a.x), a.ld, a.cols, a.rows};
   const int nvec = a.cols / VE;
-  const int row_bytes = a.cols * static_cast<int>(sizeof(TX));
-  uint8_t* slots = ring + static_cast<size_t>(g) * stages * row_bytes;
+  const int sb = slot_bytes(a.cols * static_cast<int>(sizeof(TX)), VE > 1);
+  uint8_t* slots = ring + slot_bytes(8 * a.cols, true) + static_cast<size_t>(g) * stages * sb;
   const int64_t gi = static_cast<int64_t>(blockIdx.x) * P + g, step = static_cast<int64_t>(gridDim.x) * P;
   const float inv_c = 1.f / static_cast<float>(a.cols);
   const int n_mine = warp_count<VE, NV>(a.cols, G, gw), n_lane = lane < wpg ? warp_count<VE, NV>(a.cols, G, lane) : 0;
   const float inv_mine = n_mine ? 1.f / static_cast<float>(n_mine) : 0.f;
   const float inv_lane = n_lane ? 1.f / static_cast<float>(n_lane) : 0.f;
   bool alive = true;
-
+  const auto issue = [&](int slot, int64_t row) {
+    const uint32_t bar = smem_u32(&full[g][slot]);
+    const bool copy = VE > 1 || src.copied(row);
+    mbar_arrive_expect_tx(bar, copy ? src.bytes(row) : 0u);
+    if (copy) src.issue(slots + slot * sb, bar, row);
+  };
   if (t == 0)
     for (int i = 0; i < stages; ++i)
-      if (gi + i * step < a.rows) {
-        mbar_arrive_expect_tx(smem_u32(&full[g][i]), row_bytes);
-        issue_row<TX>(slots + i * row_bytes, smem_u32(&full[g][i]), a.x, a.ld, gi + i * step, a.cols);
-      }
+      if (gi + i * step < a.rows) issue(i, gi + i * step);
 
   int slot = 0, phase = 0, buf = 0;
   for (int64_t row = gi; row < a.rows; row += step) {
     if (alive) alive = mbar_wait(smem_u32(&full[g][slot]), phase, status);
     float v[NV][VE], s[NV];
+    const auto take = [&](const TX* from) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      Vec<TX, VE> r;
-      r.fill(0);
-      if (k * G + t < nvec) r.load(reinterpret_cast<const TX*>(slots + slot * row_bytes) + (k * G + t) * VE);
+      for (int k = 0; k < NV; ++k) {
+        Vec<TX, VE> r;
+        r.fill(0);
+        if (k * G + t < nvec) r.load(from + (k * G + t) * VE);
 #pragma unroll
-      for (int j = 0; j < VE; ++j) v[k][j] = r.get(j);
-      s[k] = tree_sum(v[k]);
-    }
+        for (int j = 0; j < VE; ++j) v[k][j] = r.get(j);
+        s[k] = vec_sum(v[k]);
+      }
+    };
+    if (VE > 1 || src.copied(row)) take(reinterpret_cast<const TX*>(slots + slot * sb + (VE > 1 ? 0 : src.head(row))));
+    else take(src.row(row));
     float sum = warp_sum(tree_sum(s));
-    float mean, m2;
-    if (wpg == 1) {
-      __syncwarp();
-      mean = sum * inv_c;
-      m2 = warp_sum(sq_dev<VE, NV>(v, mean, t, G, nvec));
-    } else {
-      m2 = warp_sum(sq_dev<VE, NV>(v, sum * inv_mine, t, G, nvec));
+    const float near = wpg == 1 ? sum * inv_c : sum * inv_mine;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) s[k] = k * G + t < nvec ? vec_sq_dev(v[k], near) : 0.f;
+    float mean = near, m2 = warp_sum(tree_sum(s));
+    if (wpg > 1) {
       if (lane == 0) part[g][buf][gw] = make_float2(sum, m2);
       group_barrier(g, G);
+    } else {
+      __syncwarp();
     }
-    if (t == 0) {                                        // the slot has been read by all
-      const int64_t next = row + stages * step;
-      if (next < a.rows) {
-        mbar_arrive_expect_tx(smem_u32(&full[g][slot]), row_bytes);
-        issue_row<TX>(slots + slot * row_bytes, smem_u32(&full[g][slot]), a.x, a.ld, next, a.cols);
-      }
-    }
+    if (t == 0 && row + stages * step < a.rows) issue(slot, row + stages * step);     // all have read the slot
     if (++slot == stages) slot = 0, phase ^= 1;
     if (wpg > 1) {
       const float2 pw = lane < wpg ? part[g][buf][lane] : make_float2(0.f, 0.f);
       buf ^= 1;
-      mean = warp_sum(pw.x) * inv_c;
+      // at most sixteen warps: the lower half of the lanes has all of them
+      sum = pw.x;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      mean = __shfl_sync(0xFFFFFFFFu, sum, 0) * inv_c;
       const float d = n_lane ? pw.x * inv_lane - mean : 0.f;
-      m2 = warp_sum(pw.y + static_cast<float>(n_lane) * d * d);
+      m2 = pw.y + static_cast<float>(n_lane) * d * d;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) m2 += __shfl_xor_sync(0xFFFFFFFFu, m2, o);
+      m2 = __shfl_sync(0xFFFFFFFFu, m2, 0);
     }
     const float rstd = 1.f / sqrtf(m2 * inv_c + a.eps);
     if (t == 0) {
@@ -289,14 +384,25 @@ __global__ void __launch_bounds__(1024, 1) norm_ring_kernel(const NormArgs a, in
       a.rstd[row] = rstd;
     }
     TY* y = static_cast<TY*>(a.y) + row * a.cols;
+    const uint64_t mm = f32x2_splat(mean), rr = f32x2_splat(rstd);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int at = (k * G + t) * VE;
       if (at >= a.cols) continue;
-      float w[VE], b[VE], o[VE];
-      load_affine<VE>(a, at, w, b);
+      float o[VE];
+      if constexpr (VE == 1) {
+        const float2 wb = *reinterpret_cast<const float2*>(ws + 2 * at);
+        o[0] = norm_value(v[k][0], mean, rstd, wb.x, wb.y);
+      } else {
+        float w[VE], b[VE];
+        staged<VE>(ws, at, a.cols, w);
+        staged<VE>(ws + a.cols, at, a.cols, b);
 #pragma unroll
-      for (int j = 0; j < VE; ++j) o[j] = norm_value(v[k][j], mean, rstd, w[j], b[j]);
+        for (int j = 0; j < VE; j += 2)
+          f32x2_unpack(f32x2_fma(f32x2_mul(f32x2_sub(f32x2_pack(v[k][j], v[k][j + 1]), mm), rr), f32x2_pack(w[j], w[j + 1]),
+                                 f32x2_pack(b[j], b[j + 1])),
+                       o[j], o[j + 1]);
+      }
       store_vec<TY, VE>(y + at, o);
     }
   }
@@ -684,15 +790,17 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) 
 }
 
 // The same for many rows, through rings of rows (x and dy side by side in a
-// slot).  Each thread keeps NV * VE columns' sums; with 32 of them the
-// weights stay in shared memory.
+// slot).  Up to 16 elements a thread: h and g = dy * w stay in registers from
+// the sums to dx.  More (KEEP false): the slot is read again for dx and given
+// back after the next row's barrier, and the weights are read from shared
+// memory, because the column sums fill the registers.
 template <typename TX, typename TD, int VE, int NV>
-__global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const BwdArgs a, int G, int stages, int* status) {
-  constexpr int E = VE * NV;
-  constexpr bool KEEP = E <= 16;             // h and g live in registers between the passes, else x and dy do
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const BwdArgs a, int G, int stages, int* status) {
+  constexpr bool KEEP = VE * NV <= 16;
+  constexpr int KV = KEEP ? NV : 1;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ float red[16][2][2][16];        // [group][buffer][sum][warp]
-  __shared__ __align__(8) uint64_t full[16][MAX_STAGES];
+  __shared__ float red[MAX_GROUPS][2][2][16];        // [group][buffer][sum][warp]
+  __shared__ __align__(8) uint64_t full[MAX_GROUPS][MAX_STAGES];
   const int lane = threadIdx.x & 31;
   const int P = blockDim.x / G, g = threadIdx.x / G, t = threadIdx.x - g * G;
   const int gw = t >> 5, wpg = G >> 5;
@@ -701,38 +809,57 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const BwdArgs a, 
     fence_mbar_init();
   }
   const int nvec = a.cols / VE;
-  const int xb = a.cols * static_cast<int>(sizeof(TX)), db = a.cols * static_cast<int>(sizeof(TD));
-  float* ws = reinterpret_cast<float*>(ring);                       // !KEEP: the weights
-  uint8_t* slots = ring + (KEEP ? 0 : a.cols * 4) + static_cast<size_t>(g) * stages * (xb + db);
+  const RowSource<TX> sx{static_cast<const TX*>(a.x), a.ld_x, a.cols, a.rows};
+  const RowSource<TD> sd{static_cast<const TD*>(a.dy), a.ld_dy, a.cols, a.rows};
+  const int xb = slot_bytes(a.cols * static_cast<int>(sizeof(TX)), VE > 1);
+  const int sb = xb + slot_bytes(a.cols * static_cast<int>(sizeof(TD)), VE > 1);
+  const int wsize = a.w_f32 ? 4 : 2;
+  uint8_t* ws = ring;                                // !KEEP: the weights, as they are
+  uint8_t* slots = ring + (KEEP ? 0 : slot_bytes(wsize * a.cols, true)) + static_cast<size_t>(g) * stages * sb;
   grid_dep_wait();
-  float w[KEEP ? NV : 1][VE], aw[NV][VE], ab[NV][VE];
+  float w[KV][VE], aw[NV][VE], ab[NV][VE];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
     for (int j = 0; j < VE; ++j) aw[k][j] = ab[k][j] = 0.f;
-  if constexpr (KEEP) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
+  for (int k = 0; k < KV; ++k) {
 #pragma unroll
-      for (int j = 0; j < VE; ++j) w[k][j] = 1.f;
-      if (a.w && k * G + t < nvec) load_param<VE>(a.w, a.w_f32, (k * G + t) * VE, w[k]);
-    }
-  } else {
-    for (int i = threadIdx.x; i < a.cols; i += blockDim.x) {
-      float one[1] = {1.f};
-      if (a.w) load_param<1>(a.w, a.w_f32, i, one);
-      ws[i] = one[0];
-    }
+    for (int j = 0; j < VE; ++j) w[k][j] = 1.f;
+    if (KEEP && a.w && k * G + t < nvec) load_param<VE>(a.w, a.w_f32, (k * G + t) * VE, w[k]);
   }
+  if (!KEEP && a.w)
+    for (int i = threadIdx.x; i < a.cols; i += blockDim.x) {
+      if (a.w_f32) reinterpret_cast<float*>(ws)[i] = static_cast<const float*>(a.w)[i];
+      else reinterpret_cast<uint16_t*>(ws)[i] = static_cast<const uint16_t*>(a.w)[i];
+    }
   __syncthreads();
   const float inv_c = 1.f / static_cast<float>(a.cols);
   const int64_t gi = static_cast<int64_t>(blockIdx.x) * P + g, step = static_cast<int64_t>(gridDim.x) * P;
   bool alive = true;
+  const auto copied = [&](int64_t row) { return VE > 1 || (sx.copied(row) && sd.copied(row)); };
   const auto issue = [&](int slot, int64_t row) {
     const uint32_t bar = smem_u32(&full[g][slot]);
-    mbar_arrive_expect_tx(bar, xb + db);
-    issue_row<TX>(slots + slot * (xb + db), bar, a.x, a.ld_x, row, a.cols);
-    issue_row<TD>(slots + slot * (xb + db) + xb, bar, a.dy, a.ld_dy, row, a.cols);
+    const bool copy = copied(row);
+    mbar_arrive_expect_tx(bar, copy ? sx.bytes(row) + sd.bytes(row) : 0u);
+    if (copy) {
+      sx.issue(slots + slot * sb, bar, row);
+      sd.issue(slots + slot * sb + xb, bar, row);
+    }
+  };
+  // a vector of x and dy of the row in `slot`
+  const auto take = [&](int slot, int64_t row, bool in_ring, int k, Vec<TX, VE>& xv, Vec<TD, VE>& dv) {
+    xv.fill(0);
+    dv.fill(0);
+    if (k * G + t >= nvec) return;
+    if (in_ring) {
+      const uint8_t* p = slots + slot * sb;
+      xv.load(reinterpret_cast<const TX*>(p + (VE > 1 ? 0 : sx.head(row))) + (k * G + t) * VE);
+      dv.load(reinterpret_cast<const TD*>(p + xb + (VE > 1 ? 0 : sd.head(row))) + (k * G + t) * VE);
+    } else {
+      xv.load(sx.row(row) + (k * G + t) * VE);
+      dv.load(sd.row(row) + (k * G + t) * VE);
+    }
   };
   if (t == 0)
     for (int i = 0; i < stages; ++i)
@@ -743,43 +870,52 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const BwdArgs a, 
   for (int64_t row = gi; row < a.rows; row += step) {
     const float mean = mean_n, rstd = rstd_n;
     if (row + step < a.rows) mean_n = a.mean[row + step], rstd_n = a.rstd[row + step];
+    const uint64_t mm = f32x2_splat(mean), rr = f32x2_splat(rstd);
+    const bool in_ring = copied(row);
     if (alive) alive = mbar_wait(smem_u32(&full[g][slot]), phase, status);
-    const uint8_t* sx = slots + slot * (xb + db);
-    Vec<TX, VE> xr[NV];
-    Vec<TD, VE> dr[NV];
-    float h[KEEP ? NV : 1][VE], u[KEEP ? NV : 1][VE];
+    float h[KV][VE], u[KV][VE];
     float s1[NV], s2[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      xr[k].fill(0);
-      dr[k].fill(0);
-      if (k * G + t < nvec) {
-        xr[k].load(reinterpret_cast<const TX*>(sx) + (k * G + t) * VE);
-        dr[k].load(reinterpret_cast<const TD*>(sx + xb) + (k * G + t) * VE);
-      }
-    }
+      Vec<TX, VE> xv;
+      Vec<TD, VE> dv;
+      take(slot, row, in_ring, k, xv, dv);
+      float hk[VE], uk[VE], wk[VE];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      float wk[VE], p[VE], q[VE];
+      for (int j = 0; j < VE; ++j) wk[j] = KEEP ? w[KEEP ? k : 0][j] : 1.f;
+      if (!KEEP && a.w && k * G + t < nvec) load_param<VE>(ws, a.w_f32, (k * G + t) * VE, wk);
+      if constexpr (VE == 1) {
+        const float d = dv.get(0);
+        hk[0] = (xv.get(0) - mean) * rstd;
+        uk[0] = d * wk[0];
+        aw[k][0] = fmaf(d, hk[0], aw[k][0]);
+        ab[k][0] += d;
+        s1[k] = uk[0];
+        s2[k] = uk[0] * hk[0];
+      } else {
+        uint64_t p1, p2;
+#pragma unroll
+        for (int j = 0; j < VE; j += 2) {
+          const uint64_t hh = f32x2_mul(f32x2_sub(f32x2_pack(xv.get(j), xv.get(j + 1)), mm), rr);
+          const uint64_t dd = f32x2_pack(dv.get(j), dv.get(j + 1));
+          const uint64_t uu = f32x2_mul(dd, f32x2_pack(wk[j], wk[j + 1]));
+          f32x2_unpack(f32x2_fma(dd, hh, f32x2_pack(aw[k][j], aw[k][j + 1])), aw[k][j], aw[k][j + 1]);
+          f32x2_unpack(f32x2_add(dd, f32x2_pack(ab[k][j], ab[k][j + 1])), ab[k][j], ab[k][j + 1]);
+          p1 = j ? f32x2_add(p1, uu) : uu;
+          p2 = j ? f32x2_fma(uu, hh, p2) : f32x2_mul(uu, hh);
+          f32x2_unpack(hh, hk[j], hk[j + 1]);
+          f32x2_unpack(uu, uk[j], uk[j + 1]);
+        }
+        float x, y;
+        f32x2_unpack(p1, x, y);
+        s1[k] = x + y;
+        f32x2_unpack(p2, x, y);
+        s2[k] = x + y;
+      }
       if constexpr (KEEP) {
 #pragma unroll
-        for (int j = 0; j < VE; ++j) wk[j] = w[k][j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) wk[j] = 0.f;
-        if (k * G + t < nvec) load_param<VE>(ws, 1, (k * G + t) * VE, wk);
+        for (int j = 0; j < VE; ++j) h[k][j] = hk[j], u[k][j] = uk[j];
       }
-#pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        const float hj = (xr[k].get(j) - mean) * rstd, d = dr[k].get(j);
-        p[j] = d * wk[j];
-        q[j] = p[j] * hj;
-        aw[k][j] = fmaf(d, hj, aw[k][j]);
-        ab[k][j] += d;
-        if constexpr (KEEP) h[k][j] = hj, u[k][j] = p[j];
-      }
-      s1[k] = tree_sum(p);
-      s2[k] = tree_sum(q);
     }
     // both sums in one butterfly: the lower half of the warp takes the first,
     // the upper half the second
@@ -794,8 +930,14 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const BwdArgs a, 
     } else {
       __syncwarp();
     }
-    if (t == 0 && row + stages * step < a.rows) issue(slot, row + stages * step);   // read by all
-    if (++slot == stages) slot = 0, phase ^= 1;
+    if (t == 0) {
+      if constexpr (KEEP) {                  // all have read this slot
+        if (row + stages * step < a.rows) issue(slot, row + stages * step);
+      } else {                               // all are done with the last one
+        const int64_t next = row + (stages - 1) * step;
+        if (row != gi && next < a.rows) issue(slot ? slot - 1 : stages - 1, next);
+      }
+    }
     if (wpg > 1) {
       v = (lane & 15) < wpg ? red[g][buf][lane >> 4][lane & 15] : 0.f;
 #pragma unroll
@@ -804,24 +946,41 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(const BwdArgs a, 
     }
     const float m1 = __shfl_sync(0xFFFFFFFFu, v, 0) * inv_c, m2 = __shfl_sync(0xFFFFFFFFu, v, 16) * inv_c;
     TX* dx = static_cast<TX*>(a.dx) + row * a.cols;
+    const uint64_t c1c1 = f32x2_splat(m1), c2c2 = f32x2_splat(-m2);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (k * G + t >= nvec) continue;
-      float o[VE];
+      float hk[VE], uk[VE], o[VE];
       if constexpr (KEEP) {
 #pragma unroll
-        for (int j = 0; j < VE; ++j) o[j] = fmaf(h[k][j], -m2, u[k][j] - m1) * rstd;
+        for (int j = 0; j < VE; ++j) hk[j] = h[k][j], uk[j] = u[k][j];
       } else {
+        Vec<TX, VE> xv;
+        Vec<TD, VE> dv;
+        take(slot, row, in_ring, k, xv, dv);
         float wk[VE];
-        load_param<VE>(ws, 1, (k * G + t) * VE, wk);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) wk[j] = 1.f;
+        if (a.w) load_param<VE>(ws, a.w_f32, (k * G + t) * VE, wk);
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
-          const float hj = (xr[k].get(j) - mean) * rstd;
-          o[j] = fmaf(hj, -m2, dr[k].get(j) * wk[j] - m1) * rstd;
+          hk[j] = (xv.get(j) - mean) * rstd;
+          uk[j] = dv.get(j) * wk[j];
         }
+      }
+      if constexpr (VE == 1) {
+        o[0] = fmaf(hk[0], -m2, uk[0] - m1) * rstd;
+      } else {
+#pragma unroll
+        for (int j = 0; j < VE; j += 2)
+          f32x2_unpack(f32x2_mul(f32x2_fma(f32x2_pack(hk[j], hk[j + 1]), c2c2,
+                                           f32x2_sub(f32x2_pack(uk[j], uk[j + 1]), c1c1)),
+                                 rr),
+                       o[j], o[j + 1]);
       }
       store_vec<TX, VE>(dx + (k * G + t) * VE, o);
     }
+    if (++slot == stages) slot = 0, phase ^= 1;
   }
   if (!alive && t == 0) await_ring(full[g], stages, slot, phase, status);
   if (!a.part) return;
@@ -939,7 +1098,6 @@ using namespace mxq_host;
 
 constexpr int kMaxRowElems = 32768;       // forward: one CTA's registers
 constexpr int kMaxBwdElems = 16384;       // backward: data and two column sums
-constexpr int kBwdRingBytes = 208 * 1024;
 
 bool valid_type(int t) { return t == MXQ_BF16 || t == MXQ_F32; }
 int type_size(int t) { return t == MXQ_F32 ? 4 : 2; }
@@ -971,25 +1129,24 @@ int dispatch_row(const NormArgs& a, cudaStream_t st) {
   return launch_row<TX, OUT, VE, MAXV>(a, warp, threads, st);
 }
 
-// Rings for rows of whole 16-byte words, 1 KiB to 64 KiB each, when every
-// group gets four or more.  0: not taken.
-template <typename TX, typename TY>
+// Rings for rows of 512 bytes and more (up to what two slots hold) when every
+// group gets four or more.  False: not taken.
+template <typename TX, typename TY, int VE>
 bool try_norm_ring(const NormArgs& a, int* rc, cudaStream_t st) {
-  constexpr int VE = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
-  constexpr int NV = 16 / VE;
+  constexpr int NV = 32 / VE;
   const int nvec = a.cols / VE;
-  const int row_bytes = a.cols * static_cast<int>(sizeof(TX));
-  if (!a.y || row_bytes < 1024 || nvec > 1024 * NV || a.ld * sizeof(TX) % 16 || row_bytes % 16) return false;
-  const int G = round_up((nvec + NV - 1) / NV, 32), P = 1024 / G;
-  const int stages = std::min(MAX_STAGES, kRingBytes / (P * row_bytes));
-  if (stages < 2 || a.rows < 4ll * P * sm_count()) return false;
+  if (!a.y || a.cols * sizeof(TX) < 512 || nvec > RING_THREADS * NV) return false;
+  if (VE > 1 && (a.cols * sizeof(TX) % 16 || a.ld * sizeof(TX) % 16)) return false;
+  const int G = round_up((nvec + NV - 1) / NV, 32), P = std::min(MAX_GROUPS, RING_THREADS / G);
+  const int slot = slot_bytes(a.cols * static_cast<int>(sizeof(TX)), VE > 1), fixed = slot_bytes(8 * a.cols, true);
+  const int stages = std::min(MAX_STAGES, (kRingBytes - fixed) / (P * slot));
+  if (fixed > kRingBytes || stages < 2 || a.rows < 4ll * P * sm_count()) return false;
   int* status = status_ptr();
   auto kern = norm_ring_kernel<TX, TY, VE, NV>;
-  const int smem = P * stages * row_bytes;
   if (!status || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
     *rc = MXQ_ERR_CUDA;
   else
-    *rc = launch_pdl(kern, dim3(sm_count()), dim3(P * G), smem, st, a, G, stages, status);
+    *rc = launch_pdl(kern, dim3(sm_count()), dim3(P * G), fixed + P * stages * slot, st, a, G, stages, status);
   return true;
 }
 
@@ -998,10 +1155,10 @@ int norm_rows(const NormArgs& a, bool vec, cudaStream_t st) {
   constexpr int VE = sizeof(TX) == 2 && OUT != OUT_F32 ? 8 : 4;
   if constexpr (OUT < 0) {
     if (a.cols > kMaxRowElems) return launch_pdl(norm_long_kernel<TX, OUT>, dim3(a.rows), dim3(1024), 0, st, a);
-    if (!vec) return dispatch_row<TX, OUT, 1>(a, st);
     using TY = typename std::conditional<OUT == OUT_F32, float, __nv_bfloat16>::type;
     int rc;
-    if (try_norm_ring<TX, TY>(a, &rc, st)) return rc;
+    if (vec ? try_norm_ring<TX, TY, VE>(a, &rc, st) : try_norm_ring<TX, TY, 1>(a, &rc, st)) return rc;
+    if (!vec) return dispatch_row<TX, OUT, 1>(a, st);
   }
   return dispatch_row<TX, OUT, VE>(a, st);
 }
@@ -1075,19 +1232,19 @@ int launch_bwd(const BwdArgs& a, int G, int& parts, cudaStream_t st) {
   return launch_pdl(norm_bwd_kernel<TX, TD, VE, NV, 1>, dim3(parts), dim3(threads), smem, st, a, G);
 }
 
-// Rings while a slot (x and dy) is whole 16-byte words and every group gets
-// two rows or more.
+// Rings while a group's slots fit and every group gets two rows or more.
 template <typename TX, typename TD, int VE, int NV>
 bool launch_bwd_ring(const BwdArgs& a, int G, int P, int* rc, int& parts, cudaStream_t st) {
-  const int slot = a.cols * static_cast<int>(sizeof(TX) + sizeof(TD));
-  const int fixed = VE * NV <= 16 ? 0 : a.cols * 4;
-  const int stages = std::min(MAX_STAGES, (kBwdRingBytes - fixed) / (P * slot));
+  const int slot = slot_bytes(a.cols * static_cast<int>(sizeof(TX)), VE > 1) +
+                   slot_bytes(a.cols * static_cast<int>(sizeof(TD)), VE > 1);
+  const int fixed = VE * NV <= 16 ? 0 : slot_bytes((a.w_f32 ? 4 : 2) * a.cols, true);
+  const int stages = std::min(MAX_STAGES, (kRingBytes - fixed) / (P * slot));
   if (stages < 2) return false;
   int* status = status_ptr();
   auto kern = norm_bwd_ring_kernel<TX, TD, VE, NV>;
   const int smem = std::max(fixed + P * stages * slot, P > 1 ? 2 * VE * NV * G * 4 : 0);
   parts = sm_count();
-  if (!status || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdRingBytes) != cudaSuccess)
+  if (!status || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
     *rc = MXQ_ERR_CUDA;
   else
     *rc = launch_pdl(kern, dim3(parts), dim3(P * G), smem, st, a, G, stages, status);
@@ -1098,11 +1255,12 @@ template <typename TX, typename TD, int VE>
 bool try_bwd_ring(const BwdArgs& a, int* rc, int& parts, cudaStream_t st) {
   constexpr int N1 = 16 / VE, N2 = 32 / VE;
   const int nvec = a.cols / VE;
-  if (a.cols * sizeof(TX) % 16 || a.cols * sizeof(TD) % 16 || a.ld_x * sizeof(TX) % 16 || a.ld_dy * sizeof(TD) % 16)
+  if (VE > 1 && (a.cols * sizeof(TX) % 16 || a.cols * sizeof(TD) % 16 || a.ld_x * sizeof(TX) % 16 ||
+                 a.ld_dy * sizeof(TD) % 16))
     return false;
-  const int nv = nvec <= 512 * N1 ? N1 : N2;
-  if (nvec > 512 * N2) return false;
-  const int G = round_up((nvec + nv - 1) / nv, 32), P = 512 / G;
+  const int nv = nvec <= RING_THREADS * N1 ? N1 : N2;
+  if (nvec > RING_THREADS * N2) return false;
+  const int G = round_up((nvec + nv - 1) / nv, 32), P = std::min(MAX_GROUPS, RING_THREADS / G);
   if (a.rows < 2ll * P * sm_count()) return false;
   return nv == N1 ? launch_bwd_ring<TX, TD, VE, N1>(a, G, P, rc, parts, st)
                   : launch_bwd_ring<TX, TD, VE, N2>(a, G, P, rc, parts, st);
@@ -1122,7 +1280,7 @@ int norm_bwd(const BwdArgs& a, bool vec, int& parts, cudaStream_t st) {
   if (a.cols <= kMaxBwdElems) {
     constexpr int VE = sizeof(TX) == 2 && sizeof(TD) == 2 ? 8 : 4;
     int rc;
-    if (vec && try_bwd_ring<TX, TD, VE>(a, &rc, parts, st)) return rc;
+    if (vec ? try_bwd_ring<TX, TD, VE>(a, &rc, parts, st) : try_bwd_ring<TX, TD, 1>(a, &rc, parts, st)) return rc;
     return vec ? dispatch_bwd<TX, TD, VE>(a, parts, st) : dispatch_bwd<TX, TD, 1>(a, parts, st);
   }
   const int rc = launch_pdl(norm_bwd_long_rows_kernel<TX, TD>, dim3(a.rows), dim3(1024), 0, st, a);
