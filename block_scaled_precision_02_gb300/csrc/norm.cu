@@ -31,6 +31,12 @@ struct NormArgs {
   int ceil_mode, mma, pack_row;   // pack_row: the scales of four blocks go as one word
 };
 
+// 1 / sqrt(v): the hardware's estimate and one Newton step, within 2 ulp.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  return r * fmaf(-0.5f * v * r, r, 1.5f);
+}
+
 __device__ __forceinline__ float norm_value(float x, float mean, float rstd, float w, float b) {
   return __fmaf_rn(__fmul_rn(__fsub_rn(x, mean), rstd), w, b);
 }
@@ -193,10 +199,11 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_row_kernel(const NormA
 // reduction says that all have read it, and the slot takes a later row of the
 // group.  Loads stay in flight through reductions and stores, which registers
 // alone do not allow (the row kernel's CTAs load, reduce and store in turn).
-// A thread holds up to 32 elements, so the reductions' shuffles cost little
-// against the elements' own arithmetic, which runs on packed pairs.
-constexpr int MAX_GROUPS = 16, MAX_STAGES = 8;
-constexpr int RING_THREADS = 512;
+// The elements' arithmetic runs on packed pairs.
+constexpr int MAX_GROUPS = 32, MAX_STAGES = 8;
+constexpr int MAX_BARRIERS = 15;           // named barriers 1..15; a group of one warp needs none
+constexpr int FWD_THREADS = 640, BWD_THREADS = 512;
+constexpr int BWD_KEEP = 16;               // elements of a thread whose x and dy stay in registers
 constexpr int kRingBytes = 216 * 1024;
 
 __device__ __forceinline__ void group_barrier(int id, int threads) {
@@ -247,15 +254,18 @@ __device__ __forceinline__ int plane_at(int e, int cols) {
 }
 template <int VE>
 __device__ __forceinline__ void stage_affine(const NormArgs& a, float* ws) {
-  for (int i = threadIdx.x; i < a.cols; i += blockDim.x) {
-    float w[1], b[1];
-    load_affine<1>(a, i, w, b);
+  for (int i = threadIdx.x; i < a.cols / VE; i += blockDim.x) {
+    float w[VE], b[VE];
+    load_affine<VE>(a, i * VE, w, b);
     if constexpr (VE == 1) {
-      ws[2 * i] = w[0];
-      ws[2 * i + 1] = b[0];
+      *reinterpret_cast<float2*>(ws + 2 * i) = make_float2(w[0], b[0]);
     } else {
-      ws[plane_at<VE>(i, a.cols)] = w[0];
-      ws[a.cols + plane_at<VE>(i, a.cols)] = b[0];
+#pragma unroll
+      for (int j = 0; j < VE; j += 4) {
+        const int at = plane_at<VE>(i * VE + j, a.cols);
+        *reinterpret_cast<float4*>(ws + at) = make_float4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+        *reinterpret_cast<float4*>(ws + a.cols + at) = make_float4(b[j], b[j + 1], b[j + 2], b[j + 3]);
+      }
     }
   }
 }
@@ -298,10 +308,10 @@ __device__ __forceinline__ float vec_sq_dev(const float (&v)[VE], float m) {
   }
 }
 
-template <typename TX, typename TY, int VE, int NV>
-__global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormArgs a, int G, int stages, int* status) {
+template <typename TX, typename TY, int VE, int NV, bool FULL>
+__global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArgs a, int G, int stages, int* status) {
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ float2 part[MAX_GROUPS][2][16];
+  __shared__ float2 part[2][FWD_THREADS / 32];
   __shared__ __align__(8) uint64_t full[MAX_GROUPS][MAX_STAGES];
   const int lane = threadIdx.x & 31;
   const int P = blockDim.x / G, g = threadIdx.x / G, t = threadIdx.x - g * G;
@@ -312,8 +322,6 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
   }
   grid_dep_wait();
   float* ws = reinterpret_cast<float*>(ring);
-  stage_affine<VE>(a, ws);
-  __syncthreads();
   const RowSource<TX> src{static_cast<const TX*>(a.x), a.ld, a.cols, a.rows};
   const int nvec = a.cols / VE;
   const int sb = slot_bytes(a.cols * static_cast<int>(sizeof(TX)), VE > 1);
@@ -333,31 +341,44 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
   if (t == 0)
     for (int i = 0; i < stages; ++i)
       if (gi + i * step < a.rows) issue(i, gi + i * step);
+  stage_affine<VE>(a, ws);
+  __syncthreads();
 
   int slot = 0, phase = 0, buf = 0;
   for (int64_t row = gi; row < a.rows; row += step) {
     if (alive) alive = mbar_wait(smem_u32(&full[g][slot]), phase, status);
-    float v[NV][VE], s[NV];
+    Vec<TX, VE> v[NV];                                   // as loaded: widened anew at each use
+    float s[NV];
     const auto take = [&](const TX* from) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        Vec<TX, VE> r;
-        r.fill(0);
-        if (k * G + t < nvec) r.load(from + (k * G + t) * VE);
-#pragma unroll
-        for (int j = 0; j < VE; ++j) v[k][j] = r.get(j);
-        s[k] = vec_sum(v[k]);
+        if (!FULL) v[k].fill(0);
+        if (FULL || k * G + t < nvec) v[k].load(from + (k * G + t) * VE);
       }
+    };
+    const auto wide = [&](int k, float (&f)[VE]) {
+#pragma unroll
+      for (int j = 0; j < VE; ++j) f[j] = v[k].get(j);
     };
     if (VE > 1 || src.copied(row)) take(reinterpret_cast<const TX*>(slots + slot * sb + (VE > 1 ? 0 : src.head(row))));
     else take(src.row(row));
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float f[VE];
+      wide(k, f);
+      s[k] = vec_sum(f);
+    }
     float sum = warp_sum(tree_sum(s));
     const float near = wpg == 1 ? sum * inv_c : sum * inv_mine;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) s[k] = k * G + t < nvec ? vec_sq_dev(v[k], near) : 0.f;
+    for (int k = 0; k < NV; ++k) {
+      float f[VE];
+      wide(k, f);
+      s[k] = FULL || k * G + t < nvec ? vec_sq_dev(f, near) : 0.f;
+    }
     float mean = near, m2 = warp_sum(tree_sum(s));
     if (wpg > 1) {
-      if (lane == 0) part[g][buf][gw] = make_float2(sum, m2);
+      if (lane == 0) part[buf][g * wpg + gw] = make_float2(sum, m2);
       group_barrier(g, G);
     } else {
       __syncwarp();
@@ -365,20 +386,13 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
     if (t == 0 && row + stages * step < a.rows) issue(slot, row + stages * step);     // all have read the slot
     if (++slot == stages) slot = 0, phase ^= 1;
     if (wpg > 1) {
-      const float2 pw = lane < wpg ? part[g][buf][lane] : make_float2(0.f, 0.f);
+      const float2 pw = lane < wpg ? part[buf][g * wpg + lane] : make_float2(0.f, 0.f);
       buf ^= 1;
-      // at most sixteen warps: the lower half of the lanes has all of them
-      sum = pw.x;
-#pragma unroll
-      for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      mean = __shfl_sync(0xFFFFFFFFu, sum, 0) * inv_c;
+      mean = warp_sum(pw.x) * inv_c;
       const float d = n_lane ? pw.x * inv_lane - mean : 0.f;
-      m2 = pw.y + static_cast<float>(n_lane) * d * d;
-#pragma unroll
-      for (int o = 8; o; o >>= 1) m2 += __shfl_xor_sync(0xFFFFFFFFu, m2, o);
-      m2 = __shfl_sync(0xFFFFFFFFu, m2, 0);
+      m2 = warp_sum(pw.y + static_cast<float>(n_lane) * d * d);
     }
-    const float rstd = 1.f / sqrtf(m2 * inv_c + a.eps);
+    const float rstd = inv_sqrt(m2 * inv_c + a.eps);
     if (t == 0) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
@@ -388,18 +402,19 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const NormAr
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int at = (k * G + t) * VE;
-      if (at >= a.cols) continue;
-      float o[VE];
+      if (!FULL && at >= a.cols) continue;
+      float f[VE], o[VE];
+      wide(k, f);
       if constexpr (VE == 1) {
         const float2 wb = *reinterpret_cast<const float2*>(ws + 2 * at);
-        o[0] = norm_value(v[k][0], mean, rstd, wb.x, wb.y);
+        o[0] = norm_value(f[0], mean, rstd, wb.x, wb.y);
       } else {
         float w[VE], b[VE];
         staged<VE>(ws, at, a.cols, w);
         staged<VE>(ws + a.cols, at, a.cols, b);
 #pragma unroll
         for (int j = 0; j < VE; j += 2)
-          f32x2_unpack(f32x2_fma(f32x2_mul(f32x2_sub(f32x2_pack(v[k][j], v[k][j + 1]), mm), rr), f32x2_pack(w[j], w[j + 1]),
+          f32x2_unpack(f32x2_fma(f32x2_mul(f32x2_sub(f32x2_pack(f[j], f[j + 1]), mm), rr), f32x2_pack(w[j], w[j + 1]),
                                  f32x2_pack(b[j], b[j + 1])),
                        o[j], o[j + 1]);
       }
@@ -790,16 +805,16 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) 
 }
 
 // The same for many rows, through rings of rows (x and dy side by side in a
-// slot).  Up to 16 elements a thread: h and g = dy * w stay in registers from
-// the sums to dx.  More (KEEP false): the slot is read again for dx and given
+// slot).  Up to 16 elements a thread: x and dy stay in registers from the sums
+// to dx.  More (KEEP false): the slot is read again for dx and given
 // back after the next row's barrier, and the weights are read from shared
 // memory, because the column sums fill the registers.
-template <typename TX, typename TD, int VE, int NV>
-__global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const BwdArgs a, int G, int stages, int* status) {
-  constexpr bool KEEP = VE * NV <= 16;
+template <typename TX, typename TD, int VE, int NV, bool FULL>
+__global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const BwdArgs a, int G, int stages, int* status) {
+  constexpr bool KEEP = VE * NV <= BWD_KEEP;
   constexpr int KV = KEEP ? NV : 1;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ float red[MAX_GROUPS][2][2][16];        // [group][buffer][sum][warp]
+  __shared__ float red[2][2][BWD_THREADS / 32];     // [buffer][sum][warp of the CTA]
   __shared__ __align__(8) uint64_t full[MAX_GROUPS][MAX_STAGES];
   const int lane = threadIdx.x & 31;
   const int P = blockDim.x / G, g = threadIdx.x / G, t = threadIdx.x - g * G;
@@ -817,6 +832,38 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const Bw
   uint8_t* ws = ring;                                // !KEEP: the weights, as they are
   uint8_t* slots = ring + (KEEP ? 0 : slot_bytes(wsize * a.cols, true)) + static_cast<size_t>(g) * stages * sb;
   grid_dep_wait();
+  const float inv_c = 1.f / static_cast<float>(a.cols);
+  const int64_t gi = static_cast<int64_t>(blockIdx.x) * P + g, step = static_cast<int64_t>(gridDim.x) * P;
+  bool alive = true;
+  const auto copied = [&](int64_t row) { return VE > 1 || (sx.copied(row) && sd.copied(row)); };
+  const auto issue = [&](int slot, int64_t row) {
+    const uint32_t bar = smem_u32(&full[g][slot]);
+    const bool copy = copied(row);
+    mbar_arrive_expect_tx(bar, copy ? sx.bytes(row) + sd.bytes(row) : 0u);
+    if (copy) {
+      sx.issue(slots + slot * sb, bar, row);
+      sd.issue(slots + slot * sb + xb, bar, row);
+    }
+  };
+  // a vector of x and dy of the row in `slot`
+  const auto take = [&](int slot, int64_t row, bool in_ring, int k, Vec<TX, VE>& xv, Vec<TD, VE>& dv) {
+    if (!FULL) {
+      xv.fill(0);
+      dv.fill(0);
+      if (k * G + t >= nvec) return;
+    }
+    if (in_ring) {
+      const uint8_t* p = slots + slot * sb;
+      xv.load(reinterpret_cast<const TX*>(p + (VE > 1 ? 0 : sx.head(row))) + (k * G + t) * VE);
+      dv.load(reinterpret_cast<const TD*>(p + xb + (VE > 1 ? 0 : sd.head(row))) + (k * G + t) * VE);
+    } else {
+      xv.load(sx.row(row) + (k * G + t) * VE);
+      dv.load(sd.row(row) + (k * G + t) * VE);
+    }
+  };
+  if (t == 0)
+    for (int i = 0; i < stages; ++i)
+      if (gi + i * step < a.rows) issue(i, gi + i * step);
   float w[KV][VE], aw[NV][VE], ab[NV][VE];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
@@ -834,36 +881,6 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const Bw
       else reinterpret_cast<uint16_t*>(ws)[i] = static_cast<const uint16_t*>(a.w)[i];
     }
   __syncthreads();
-  const float inv_c = 1.f / static_cast<float>(a.cols);
-  const int64_t gi = static_cast<int64_t>(blockIdx.x) * P + g, step = static_cast<int64_t>(gridDim.x) * P;
-  bool alive = true;
-  const auto copied = [&](int64_t row) { return VE > 1 || (sx.copied(row) && sd.copied(row)); };
-  const auto issue = [&](int slot, int64_t row) {
-    const uint32_t bar = smem_u32(&full[g][slot]);
-    const bool copy = copied(row);
-    mbar_arrive_expect_tx(bar, copy ? sx.bytes(row) + sd.bytes(row) : 0u);
-    if (copy) {
-      sx.issue(slots + slot * sb, bar, row);
-      sd.issue(slots + slot * sb + xb, bar, row);
-    }
-  };
-  // a vector of x and dy of the row in `slot`
-  const auto take = [&](int slot, int64_t row, bool in_ring, int k, Vec<TX, VE>& xv, Vec<TD, VE>& dv) {
-    xv.fill(0);
-    dv.fill(0);
-    if (k * G + t >= nvec) return;
-    if (in_ring) {
-      const uint8_t* p = slots + slot * sb;
-      xv.load(reinterpret_cast<const TX*>(p + (VE > 1 ? 0 : sx.head(row))) + (k * G + t) * VE);
-      dv.load(reinterpret_cast<const TD*>(p + xb + (VE > 1 ? 0 : sd.head(row))) + (k * G + t) * VE);
-    } else {
-      xv.load(sx.row(row) + (k * G + t) * VE);
-      dv.load(sd.row(row) + (k * G + t) * VE);
-    }
-  };
-  if (t == 0)
-    for (int i = 0; i < stages; ++i)
-      if (gi + i * step < a.rows) issue(i, gi + i * step);
 
   int slot = 0, phase = 0, buf = 0;
   float mean_n = gi < a.rows ? a.mean[gi] : 0.f, rstd_n = gi < a.rows ? a.rstd[gi] : 0.f;
@@ -873,17 +890,21 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const Bw
     const uint64_t mm = f32x2_splat(mean), rr = f32x2_splat(rstd);
     const bool in_ring = copied(row);
     if (alive) alive = mbar_wait(smem_u32(&full[g][slot]), phase, status);
-    float h[KV][VE], u[KV][VE];
+    Vec<TX, VE> xs[KV];
+    Vec<TD, VE> ds[KV];
+    if (KEEP)
+#pragma unroll
+      for (int k = 0; k < NV; ++k) take(slot, row, in_ring, k, xs[KEEP ? k : 0], ds[KEEP ? k : 0]);
     float s1[NV], s2[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      Vec<TX, VE> xv;
-      Vec<TD, VE> dv;
-      take(slot, row, in_ring, k, xv, dv);
+      Vec<TX, VE>& xv = xs[KEEP ? k : 0];
+      Vec<TD, VE>& dv = ds[KEEP ? k : 0];
+      if (!KEEP) take(slot, row, in_ring, k, xv, dv);
       float hk[VE], uk[VE], wk[VE];
 #pragma unroll
       for (int j = 0; j < VE; ++j) wk[j] = KEEP ? w[KEEP ? k : 0][j] : 1.f;
-      if (!KEEP && a.w && k * G + t < nvec) load_param<VE>(ws, a.w_f32, (k * G + t) * VE, wk);
+      if (!KEEP && a.w && (FULL || k * G + t < nvec)) load_param<VE>(ws, a.w_f32, (k * G + t) * VE, wk);
       if constexpr (VE == 1) {
         const float d = dv.get(0);
         hk[0] = (xv.get(0) - mean) * rstd;
@@ -912,10 +933,6 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const Bw
         f32x2_unpack(p2, x, y);
         s2[k] = x + y;
       }
-      if constexpr (KEEP) {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) h[k][j] = hk[j], u[k][j] = uk[j];
-      }
     }
     // both sums in one butterfly: the lower half of the warp takes the first,
     // the upper half the second
@@ -925,7 +942,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const Bw
 #pragma unroll
     for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if (wpg > 1) {
-      if ((lane & 15) == 0) red[g][buf][lane >> 4][gw] = v;
+      if ((lane & 15) == 0) red[buf][lane >> 4][g * wpg + gw] = v;
       group_barrier(g, G);
     } else {
       __syncwarp();
@@ -939,7 +956,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const Bw
       }
     }
     if (wpg > 1) {
-      v = (lane & 15) < wpg ? red[g][buf][lane >> 4][lane & 15] : 0.f;
+      const float* half = red[buf][lane >> 4] + g * wpg + (lane & 15);
+      v = (lane & 15) < wpg ? half[0] : 0.f;
+      if (wpg > 16) v += (lane & 15) + 16 < wpg ? half[16] : 0.f;
 #pragma unroll
       for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
       buf ^= 1;
@@ -949,23 +968,23 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const Bw
     const uint64_t c1c1 = f32x2_splat(m1), c2c2 = f32x2_splat(-m2);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (k * G + t >= nvec) continue;
+      if (!FULL && k * G + t >= nvec) continue;
       float hk[VE], uk[VE], o[VE];
-      if constexpr (KEEP) {
+      Vec<TX, VE>& xv = xs[KEEP ? k : 0];
+      Vec<TD, VE>& dv = ds[KEEP ? k : 0];
+      if (!KEEP) take(slot, row, in_ring, k, xv, dv);
+      float wk[VE];
 #pragma unroll
-        for (int j = 0; j < VE; ++j) hk[j] = h[k][j], uk[j] = u[k][j];
+      for (int j = 0; j < VE; ++j) wk[j] = KEEP ? w[KEEP ? k : 0][j] : 1.f;
+      if (!KEEP && a.w) load_param<VE>(ws, a.w_f32, (k * G + t) * VE, wk);
+      if constexpr (VE == 1) {
+        hk[0] = (xv.get(0) - mean) * rstd;
+        uk[0] = dv.get(0) * wk[0];
       } else {
-        Vec<TX, VE> xv;
-        Vec<TD, VE> dv;
-        take(slot, row, in_ring, k, xv, dv);
-        float wk[VE];
 #pragma unroll
-        for (int j = 0; j < VE; ++j) wk[j] = 1.f;
-        if (a.w) load_param<VE>(ws, a.w_f32, (k * G + t) * VE, wk);
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          hk[j] = (xv.get(j) - mean) * rstd;
-          uk[j] = dv.get(j) * wk[j];
+        for (int j = 0; j < VE; j += 2) {
+          f32x2_unpack(f32x2_mul(f32x2_sub(f32x2_pack(xv.get(j), xv.get(j + 1)), mm), rr), hk[j], hk[j + 1]);
+          f32x2_unpack(f32x2_mul(f32x2_pack(dv.get(j), dv.get(j + 1)), f32x2_pack(wk[j], wk[j + 1])), uk[j], uk[j + 1]);
         }
       }
       if constexpr (VE == 1) {
@@ -1129,20 +1148,25 @@ int dispatch_row(const NormArgs& a, cudaStream_t st) {
   return launch_row<TX, OUT, VE, MAXV>(a, warp, threads, st);
 }
 
+// Groups of G threads in a CTA: more than one warp takes a named barrier each.
+int ring_groups(int threads, int G) { return std::min(G > 32 ? MAX_BARRIERS : MAX_GROUPS, threads / G); }
+
 // Rings for rows of 512 bytes and more (up to what two slots hold) when every
 // group gets four or more.  False: not taken.
 template <typename TX, typename TY, int VE>
 bool try_norm_ring(const NormArgs& a, int* rc, cudaStream_t st) {
-  constexpr int NV = 32 / VE;
+  constexpr int NV = VE > 1 ? 64 / (VE * static_cast<int>(sizeof(TX))) : 16;     // 64 bytes of a row
   const int nvec = a.cols / VE;
-  if (!a.y || a.cols * sizeof(TX) < 512 || nvec > RING_THREADS * NV) return false;
+  if (!a.y || a.cols * sizeof(TX) < 512 || nvec > FWD_THREADS * NV) return false;
   if (VE > 1 && (a.cols * sizeof(TX) % 16 || a.ld * sizeof(TX) % 16)) return false;
-  const int G = round_up((nvec + NV - 1) / NV, 32), P = std::min(MAX_GROUPS, RING_THREADS / G);
+  const int G = round_up((nvec + NV - 1) / NV, 32), P = ring_groups(FWD_THREADS, G);
   const int slot = slot_bytes(a.cols * static_cast<int>(sizeof(TX)), VE > 1), fixed = slot_bytes(8 * a.cols, true);
   const int stages = std::min(MAX_STAGES, (kRingBytes - fixed) / (P * slot));
   if (fixed > kRingBytes || stages < 2 || a.rows < 4ll * P * sm_count()) return false;
   int* status = status_ptr();
-  auto kern = norm_ring_kernel<TX, TY, VE, NV>;
+  auto kern = norm_ring_kernel<TX, TY, VE, NV, false>;
+  if constexpr (VE > 1)
+    if (nvec == G * NV) kern = norm_ring_kernel<TX, TY, VE, NV, true>;
   if (!status || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
     *rc = MXQ_ERR_CUDA;
   else
@@ -1237,11 +1261,13 @@ template <typename TX, typename TD, int VE, int NV>
 bool launch_bwd_ring(const BwdArgs& a, int G, int P, int* rc, int& parts, cudaStream_t st) {
   const int slot = slot_bytes(a.cols * static_cast<int>(sizeof(TX)), VE > 1) +
                    slot_bytes(a.cols * static_cast<int>(sizeof(TD)), VE > 1);
-  const int fixed = VE * NV <= 16 ? 0 : slot_bytes((a.w_f32 ? 4 : 2) * a.cols, true);
+  const int fixed = VE * NV <= BWD_KEEP ? 0 : slot_bytes((a.w_f32 ? 4 : 2) * a.cols, true);
   const int stages = std::min(MAX_STAGES, (kRingBytes - fixed) / (P * slot));
   if (stages < 2) return false;
   int* status = status_ptr();
-  auto kern = norm_bwd_ring_kernel<TX, TD, VE, NV>;
+  auto kern = norm_bwd_ring_kernel<TX, TD, VE, NV, false>;
+  if constexpr (VE > 1)
+    if (a.cols / VE == G * NV) kern = norm_bwd_ring_kernel<TX, TD, VE, NV, true>;
   const int smem = std::max(fixed + P * stages * slot, P > 1 ? 2 * VE * NV * G * 4 : 0);
   parts = sm_count();
   if (!status || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
@@ -1253,14 +1279,14 @@ bool launch_bwd_ring(const BwdArgs& a, int G, int P, int* rc, int& parts, cudaSt
 
 template <typename TX, typename TD, int VE>
 bool try_bwd_ring(const BwdArgs& a, int* rc, int& parts, cudaStream_t st) {
-  constexpr int N1 = 16 / VE, N2 = 32 / VE;
+  constexpr int N1 = BWD_KEEP / VE, N2 = 2 * BWD_KEEP / VE;
   const int nvec = a.cols / VE;
   if (VE > 1 && (a.cols * sizeof(TX) % 16 || a.cols * sizeof(TD) % 16 || a.ld_x * sizeof(TX) % 16 ||
                  a.ld_dy * sizeof(TD) % 16))
     return false;
-  const int nv = nvec <= RING_THREADS * N1 ? N1 : N2;
-  if (nvec > RING_THREADS * N2) return false;
-  const int G = round_up((nvec + nv - 1) / nv, 32), P = std::min(MAX_GROUPS, RING_THREADS / G);
+  const int nv = nvec <= BWD_THREADS * N1 ? N1 : N2;
+  if (nvec > BWD_THREADS * N2) return false;
+  const int G = round_up((nvec + nv - 1) / nv, 32), P = ring_groups(BWD_THREADS, G);
   if (a.rows < 2ll * P * sm_count()) return false;
   return nv == N1 ? launch_bwd_ring<TX, TD, VE, N1>(a, G, P, rc, parts, st)
                   : launch_bwd_ring<TX, TD, VE, N2>(a, G, P, rc, parts, st);
