@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArg
     fence_mbar_init();
   }
   grid_dep_wait();
+  grid_dep_launch();
   float* ws = reinterpret_cast<float*>(ring);
   const RowSource<TX> src{static_cast<const TX*>(a.x), a.ld, a.cols, a.rows};
   const int nvec = a.cols / VE;
@@ -832,6 +833,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
   uint8_t* ws = ring;                                // !KEEP: the weights, as they are
   uint8_t* slots = ring + (KEEP ? 0 : slot_bytes(wsize * a.cols, true)) + static_cast<size_t>(g) * stages * sb;
   grid_dep_wait();
+  grid_dep_launch();
   const float inv_c = 1.f / static_cast<float>(a.cols);
   const int64_t gi = static_cast<int64_t>(blockIdx.x) * P + g, step = static_cast<int64_t>(gridDim.x) * P;
   bool alive = true;
@@ -1097,8 +1099,11 @@ __global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* part, in
   const int cx = threadIdx.x & 31, sy = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + cx;      // over both sums
   float s = 0.f;
-  if (c < 2ll * cols)
-    for (int i = sy; i < parts; i += 8) s += part[static_cast<int64_t>(i) * 2 * cols + c];
+  if (c < 2ll * cols) {
+    const float* p = part + c;
+#pragma unroll 8
+    for (int i = sy; i < parts; i += 8) s += p[static_cast<int64_t>(i) * 2 * cols];
+  }
   red[sy][cx] = s;
   __syncthreads();
   if (sy == 0 && c < 2ll * cols) {
@@ -1130,22 +1135,29 @@ int launch_row(const NormArgs& a, bool warp, int threads, cudaStream_t st) {
   return launch_pdl(norm_row_kernel<TX, OUT, VE, NV, false>, dim3(a.rows), dim3(threads), 0, st, a);
 }
 
-// One row per warp while a lane holds at most 32 elements, else one per CTA of
-// just enough warps that a thread holds at most 32 elements.
+// One row per warp while a lane holds at most 32 elements (8 without vectors),
+// else one per CTA of just enough warps that a thread does.  Single elements
+// go eight to a thread while 1024 threads hold the row: with 32 the loads
+// spill (1531 x 2049 float32: PLACEHOLDER).
 template <typename TX, int OUT, int VE>
 int dispatch_row(const NormArgs& a, cudaStream_t st) {
-  constexpr int MAXV = 32 / VE;
   const int nvec = a.cols / VE;
-  const bool warp = nvec <= 32 * MAXV;
-  const int threads = warp ? 32 : round_up((nvec + MAXV - 1) / MAXV, 32);
-  const int nv = (nvec + threads - 1) / threads;
-  if constexpr (VE > 1) {
+  if constexpr (VE == 1) {
+    const int nv = nvec <= 8 * 1024 ? 8 : 32;
+    const bool warp = nvec <= 32 * 8;
+    const int threads = round_up((nvec + nv - 1) / nv, 32);
+    return nv == 8 ? launch_row<TX, OUT, 1, 8>(a, warp, threads, st) : launch_row<TX, OUT, 1, 32>(a, false, threads, st);
+  } else {
+    constexpr int MAXV = 32 / VE;
+    const bool warp = nvec <= 32 * MAXV;
+    const int threads = warp ? 32 : round_up((nvec + MAXV - 1) / MAXV, 32);
+    const int nv = (nvec + threads - 1) / threads;
     if (nv <= 1) return launch_row<TX, OUT, VE, 1>(a, warp, threads, st);
     if (nv <= 2) return launch_row<TX, OUT, VE, 2>(a, warp, threads, st);
+    if constexpr (MAXV >= 8)
+      if (nv <= MAXV / 2) return launch_row<TX, OUT, VE, MAXV / 2>(a, warp, threads, st);
+    return launch_row<TX, OUT, VE, MAXV>(a, warp, threads, st);
   }
-  if constexpr (MAXV >= 8)
-    if (nv <= MAXV / 2) return launch_row<TX, OUT, VE, MAXV / 2>(a, warp, threads, st);
-  return launch_row<TX, OUT, VE, MAXV>(a, warp, threads, st);
 }
 
 // Groups of G threads in a CTA: more than one warp takes a named barrier each.
