@@ -273,9 +273,9 @@ constexpr int RING_TPB = 512, RING_WARPS = RING_TPB / 32;
 constexpr float kLowest = -3.402823466e38f;
 
 // exp(v - m) of a pair, m and log2(e) splat.
-__device__ __forceinline__ void exp_pair(float a, float b, uint64_t mm, uint64_t l2e, float& x, float& y) {
+__device__ __forceinline__ void exp_pair(float a, float b, float2 mm, float2 l2e, float& x, float& y) {
   float p, q;
-  f32x2_unpack(f32x2_mul(f32x2_sub(f32x2_pack(a, b), mm), l2e), p, q);
+  halves(mul2(sub2(pair(a, b), mm), l2e), p, q);
   x = ex2(p);
   y = ex2(q);
 }
@@ -288,7 +288,7 @@ __device__ __forceinline__ void take_in(const float (&v)[VE], float& m, float& s
   for (int j = 0; j < VE; j += 2) top = fmax3_nan(top, v[j], v[j + 1]);
   s *= ex2((m - top) * kLog2e);
   m = top;
-  const uint64_t mm = f32x2_splat(m), l2e = f32x2_splat(kLog2e);
+  const float2 mm = splat(m), l2e = splat(kLog2e);
   float e[VE];
 #pragma unroll
   for (int j = 0; j < VE; j += 2) exp_pair(v[j], v[j + 1], mm, l2e, e[j], e[j + 1]);
@@ -298,8 +298,8 @@ __device__ __forceinline__ void take_in(const float (&v)[VE], float& m, float& s
 // The gradient's VE elements in place of the logits: exp(v - top) * f, and k
 // more at the target.
 template <int VE>
-__device__ __forceinline__ void to_gradient(float (&v)[VE], uint64_t top, float f, int target, float k) {
-  const uint64_t l2e = f32x2_splat(kLog2e);
+__device__ __forceinline__ void to_gradient(float (&v)[VE], float2 top, float f, int target, float k) {
+  const float2 l2e = splat(kLog2e);
 #pragma unroll
   for (int j = 0; j < VE; j += 2) {
     float x, y;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
       // second pass: the gradient, and the chunks are free
       const float k = a.scale * tok.w * slope;
       const int at = inside ? static_cast<int>(tok.target) : -VE;
-      const uint64_t tt = f32x2_splat(top);
+      const float2 tt = splat(top);
       const float f = -k / total;
       int sl = slot0;
       for (int w = w0; w < end; w += CV) {

@@ -7,6 +7,7 @@
 //   M2(A+B) = M2(A) + M2(B) + n_A (mean_A - mean)^2 + n_B (mean_B - mean)^2,
 // which does not cancel when the mean is large against the spread.
 #include <algorithm>
+#include <atomic>
 
 #include "rowops.cuh"
 
@@ -28,7 +29,9 @@ struct NormArgs {
   float* mean;
   float* rstd;
   uint8_t *q_row, *s_row, *q_col, *s_col;
-  int ceil_mode, mma, pack_row;   // pack_row: the scales of four blocks go as one word
+  int ceil_mode, mma;
+  int pack_row, pack_col;         // the scales of four blocks may go as one word
+  int wide_col;                   // q_col is 32-byte aligned
 };
 
 // 1 / sqrt(v): the hardware's estimate and one Newton step, within 2 ulp.
@@ -283,11 +286,11 @@ template <int VE>
 __device__ __forceinline__ float vec_sum(const float (&v)[VE]) {
   if constexpr (VE == 1) return v[0];
   else {
-    uint64_t p = f32x2_pack(v[0], v[1]);
+    float2 p = pair(v[0], v[1]);
 #pragma unroll
-    for (int j = 2; j < VE; j += 2) p = f32x2_add(p, f32x2_pack(v[j], v[j + 1]));
+    for (int j = 2; j < VE; j += 2) p = add2(p, pair(v[j], v[j + 1]));
     float x, y;
-    f32x2_unpack(p, x, y);
+    halves(p, x, y);
     return x + y;
   }
 }
@@ -295,15 +298,15 @@ template <int VE>
 __device__ __forceinline__ float vec_sq_dev(const float (&v)[VE], float m) {
   if constexpr (VE == 1) return (v[0] - m) * (v[0] - m);
   else {
-    const uint64_t mm = f32x2_splat(m);
-    uint64_t d = f32x2_sub(f32x2_pack(v[0], v[1]), mm), p = f32x2_mul(d, d);
+    const float2 mm = splat(m);
+    float2 d = sub2(pair(v[0], v[1]), mm), p = mul2(d, d);
 #pragma unroll
     for (int j = 2; j < VE; j += 2) {
-      d = f32x2_sub(f32x2_pack(v[j], v[j + 1]), mm);
-      p = f32x2_fma(d, d, p);
+      d = sub2(pair(v[j], v[j + 1]), mm);
+      p = fma2(d, d, p);
     }
     float x, y;
-    f32x2_unpack(p, x, y);
+    halves(p, x, y);
     return x + y;
   }
 }
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArg
       a.rstd[row] = rstd;
     }
     TY* y = static_cast<TY*>(a.y) + row * a.cols;
-    const uint64_t mm = f32x2_splat(mean), rr = f32x2_splat(rstd);
+    const float2 mm = splat(mean), rr = splat(rstd);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int at = (k * G + t) * VE;
@@ -415,8 +418,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArg
         staged<VE>(ws + a.cols, at, a.cols, b);
 #pragma unroll
         for (int j = 0; j < VE; j += 2)
-          f32x2_unpack(f32x2_fma(f32x2_mul(f32x2_sub(f32x2_pack(f[j], f[j + 1]), mm), rr), f32x2_pack(w[j], w[j + 1]),
-                                 f32x2_pack(b[j], b[j + 1])),
+          halves(fma2(mul2(sub2(pair(f[j], f[j + 1]), mm), rr), pair(w[j], w[j + 1]),
+                                 pair(b[j], b[j + 1])),
                        o[j], o[j + 1]);
       }
       store_vec<TY, VE>(y + at, o);
@@ -473,178 +476,255 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
   }
 }
 
-// Quantizing norm with column blocks: a CTA holds 32 rows of up to SLAB
-// columns, raw, in registers (the row pass) and in shared memory (the column
-// pass), so x is read from HBM once for both copies.  CLUSTER: the CTAs of a
-// cluster hold the slabs of the same 32 rows; each pushes its 32 partial
-// (sum, M2) pairs into every CTA's shared memory, and one cluster barrier
-// later each merges them.  Otherwise the statistics are given.
-template <typename TX> constexpr int slab_cols() { return sizeof(TX) == 2 ? 1024 : 512; }
+// Quantizing norm with column blocks.  A CTA walks over tiles of 32 rows and
+// up to S columns.  A warp holds its rows' words in registers, 16 consecutive
+// columns to a lane: it takes their statistics, then computes y once, encodes
+// the row blocks (two lanes each), and leaves y as float32 in shared memory,
+// where a thread then finds whole column blocks.  x is read from HBM once for
+// both copies.  CLUSTER: the CTAs of a cluster hold the slabs of the same
+// rows; each warp sends its rows' (sum, M2) of the slab to every CTA by
+// counted asynchronous stores and merges what arrives.  Otherwise the
+// statistics are given.
+//
+// y lies in four planes of S / 4: column 16 i + 4 p + q at p S/4 + 4 i + q,
+// so that a lane's sixteen values go out as four 16-byte stores without bank
+// conflicts.
+__device__ __forceinline__ void store32(uint8_t* p, const uint32_t (&q)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(q[0]), "r"(q[1]), "r"(q[2]),
+               "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7])
+               : "memory");
+}
 
-template <typename TX, int FMT, int ORIENT, bool CLUSTER>
-__global__ void __launch_bounds__(256, 2) norm_tile_kernel(const NormArgs a, int slabs) {
-  constexpr int SLAB = slab_cols<TX>();
-  constexpr int VE = 16 / static_cast<int>(sizeof(TX));
-  constexpr int NV = SLAB / (32 * VE);
-  constexpr int RW = 4;                                  // rows of a warp
-  constexpr int LPB = 32 / VE;
-  extern __shared__ __align__(16) uint8_t tile[];        // [32][SLAB] raw
-  __shared__ float2 parts[8][32];                        // [rank][row] (sum, M2)
-  __shared__ float2 stat[32];                            // [row] (mean, rstd)
-  if constexpr (CLUSTER) cluster_arrive();
+constexpr int TILE_SLABS = 8;                            // CTAs of a cluster (the portable limit)
+
+template <typename TX, int FMT, int ORIENT, bool CLUSTER, int S, int T>
+__global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const NormArgs a, int slabs, int* status) {
+  constexpr int RW = 32 / (T / 32);                      // rows of a warp
+  constexpr int GS = 32 / RW;                            // lanes that end up with a row's sums
+  constexpr int NV = S / 512;                            // runs of 16 columns of a lane
+  constexpr int WV = 16 / static_cast<int>(sizeof(TX));  // elements of a 16-byte word
+  constexpr int NW = 16 / WV;                            // words of a run
+  extern __shared__ __align__(16) float wtile[];         // weight [S], bias [S], y [32][S], in planes
+  float* const btile = wtile + S;
+  float* const ytile = wtile + 2 * S;
+  __shared__ float2 parts[2][TILE_SLABS][32];            // [buffer][rank][row] (sum, M2)
+  __shared__ __align__(8) uint64_t bar[2];
+  if constexpr (CLUSTER) {
+    if (threadIdx.x == 0) {
+      mbar_init(smem_u32(&bar[0]), 1);
+      mbar_init(smem_u32(&bar[1]), 1);
+      fence_mbar_init();
+    }
+    cluster_sync();
+  }
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % slabs;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x / slabs) * 32;
-  const int c0 = rank * SLAB;
-  const int nc = min(SLAB, a.cols - c0);                 // columns of this slab (a multiple of 32)
-  const TX* x = static_cast<const TX*>(a.x) + row0 * a.ld + c0;
+  const int tiles = a.rows / 32;
+  const int team = blockIdx.x / slabs, teams = gridDim.x / slabs;
+  // a contiguous range of tiles: four in a row share a word of column scales
+  const int first = static_cast<int>(static_cast<int64_t>(tiles) * team / teams);
+  const int last = static_cast<int>(static_cast<int64_t>(tiles) * (team + 1) / teams);
+  const int c0 = rank * S;
+  const int nc = min(S, a.cols - c0);                    // columns of this slab (a multiple of 32)
+  const float inv_nc = 1.f / static_cast<float>(nc), inv_c = 1.f / static_cast<float>(a.cols);
+  const int lr = lane / GS, lk = lane % GS;              // this lane's row and slab in the merge
+  const float n_k = static_cast<float>(lk < slabs ? min(S, a.cols - lk * S) : 0);
+  bool alive = true;
 
-  Vec<TX, VE> raw[RW][NV];
-#pragma unroll
-  for (int r = 0; r < RW; ++r)
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      raw[r][k].fill(0);
-      const int at = (k * 32 + lane) * VE;
-      if (at < nc) raw[r][k].load(x + (warp * RW + r) * a.ld + at);
-    }
-  if constexpr (ORIENT & MXQ_COL) {
+  Vec<TX, WV> raw[RW][NV][NW];
+  const auto load = [&](int tile) {
+    const TX* x = static_cast<const TX*>(a.x) + (static_cast<int64_t>(tile) * 32 + warp * RW) * a.ld + c0 + lane * 16;
 #pragma unroll
     for (int r = 0; r < RW; ++r)
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-        *reinterpret_cast<uint4*>(tile + ((warp * RW + r) * SLAB + (k * 32 + lane) * VE) * sizeof(TX)) =
-            make_uint4(raw[r][k].w[0], raw[r][k].w[1], raw[r][k].w[2], raw[r][k].w[3]);
-  }
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+          raw[r][v][i].fill(0);
+          if (v * 512 + lane * 16 < nc) raw[r][v][i].load(x + r * a.ld + v * 512 + i * WV);
+        }
+  };
+  const auto run = [&](int r, int v, float (&f)[16]) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+#pragma unroll
+      for (int j = 0; j < WV; ++j) f[i * WV + j] = raw[r][v][i].get(j);
+  };
+  // one value per row, added over the warp: the lanes of group r end with row r's
+  const auto rows_sum = [&](const float (&s)[RW]) {
+    float b;
+    if constexpr (RW == 4) {
+      const bool hi = lane & 16;
+      const float a0 = (hi ? s[2] : s[0]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? s[0] : s[2], 16);
+      const float a1 = (hi ? s[3] : s[1]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? s[1] : s[3], 16);
+      const bool up = lane & 8;
+      b = (up ? a1 : a0) + __shfl_xor_sync(0xFFFFFFFFu, up ? a0 : a1, 8);
+    } else {
+      const bool hi = lane & 16;
+      b = (hi ? s[1] : s[0]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? s[0] : s[1], 16);
+    }
+#pragma unroll
+    for (int o = GS / 2; o; o >>= 1) b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    return b;
+  };
+  const auto group_sum = [&](float b) {
+#pragma unroll
+    for (int o = GS / 2; o; o >>= 1) b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    return b;
+  };
 
-  if constexpr (CLUSTER) {
-    float2 mine = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int r = 0; r < RW; ++r) {
-      float s[NV], d[NV];
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        float v[VE];
-#pragma unroll
-        for (int j = 0; j < VE; ++j) v[j] = raw[r][k].get(j);
-        s[k] = tree_sum(v);
-      }
-      const float sum = warp_sum(tree_sum(s));
-      const float m = sum / static_cast<float>(nc);
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        float v[VE];
-#pragma unroll
-        for (int j = 0; j < VE; ++j) v[j] = (raw[r][k].get(j) - m) * (raw[r][k].get(j) - m);
-        d[k] = (k * 32 + lane) * VE < nc ? tree_sum(v) : 0.f;
-      }
-      const float m2 = warp_sum(tree_sum(d));
-      if (lane == r) mine = make_float2(sum, m2);
-    }
-    cluster_wait();                                      // every CTA of the cluster has started
-    if (lane < RW)
-      for (int k = 0; k < slabs; ++k)
-        st_cluster_f2(smem_u32(&parts[rank][warp * RW + lane]), k, mine.x, mine.y);
-    cluster_sync();
-    if (warp == 0) {
-      float sum = 0.f, m2 = 0.f;
-      for (int k = 0; k < slabs; ++k) sum += parts[k][lane].x;
-      const float mean = sum / static_cast<float>(a.cols);
-      for (int k = 0; k < slabs; ++k) {
-        const float n = static_cast<float>(min(SLAB, a.cols - k * SLAB));
-        const float d = parts[k][lane].x / n - mean;
-        m2 += parts[k][lane].y + n * d * d;
-      }
-      const float rstd = 1.f / sqrtf(m2 / static_cast<float>(a.cols) + a.eps);
-      stat[lane] = make_float2(mean, rstd);
-      if (rank == 0) {
-        a.mean[row0 + lane] = mean;
-        a.rstd[row0 + lane] = rstd;
-      }
-    }
-  } else {
-    if (warp == 0) stat[lane] = make_float2(a.mean[row0 + lane], a.rstd[row0 + lane]);
+  uint32_t col_scales[S / T];                            // this thread's columns, a byte per tile
+  if (first < last) load(first);
+  for (int c = threadIdx.x * 4; c < nc; c += T * 4) {
+    float w[4], b[4];
+    load_affine<4>(a, c0 + c, w, b);
+    const int at = (c & 15) / 4 * (S / 4) + c / 16 * 4;
+    *reinterpret_cast<float4*>(wtile + at) = make_float4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<float4*>(btile + at) = make_float4(b[0], b[1], b[2], b[3]);
   }
   __syncthreads();
-
-  if constexpr (ORIENT & MXQ_ROW) {
-    constexpr int QW = code_words<FMT, VE>();
-    const int kb = a.cols / 32;
+  for (int tile = first; tile < last; ++tile) {
+    const int64_t row0 = static_cast<int64_t>(tile) * 32;
+    float mean, rstd;                                    // of row lr of this warp
+    if constexpr (CLUSTER) {
+      const int buf = (tile - first) & 1;
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(smem_u32(&bar[buf]), 256 * slabs);
+      float s[RW];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int at = (k * 32 + lane) * VE;
+      for (int r = 0; r < RW; ++r) {
+        s[r] = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          float f[16];
+          run(r, v, f);
+          s[r] += vec_sum(f);
+        }
+      }
+      const float sum = rows_sum(s);
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        const float near = __shfl_sync(0xFFFFFFFFu, sum, r * GS) * inv_nc;
+        s[r] = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          float f[16];
+          run(r, v, f);
+          if (v * 512 + lane * 16 < nc) s[r] += vec_sq_dev(f, near);
+        }
+      }
+      const float m2 = rows_sum(s);
+      if (lk < slabs)
+        st_async_f2(smem_u32(&parts[buf][rank][warp * RW + lr]), smem_u32(&bar[buf]), lk, sum, m2);
+      if (alive) alive = mbar_wait_sleep(smem_u32(&bar[buf]), ((tile - first) >> 1) & 1, status);
+      const float2 p = lk < slabs ? parts[buf][lk][warp * RW + lr] : make_float2(0.f, 0.f);
+      mean = group_sum(p.x) * inv_c;
+      const float d = lk < slabs ? p.x / n_k - mean : 0.f;
+      rstd = inv_sqrt(group_sum(p.y + n_k * d * d) * inv_c + a.eps);
+      if (rank == 0 && lk == 0) {
+        a.mean[row0 + warp * RW + lr] = mean;
+        a.rstd[row0 + warp * RW + lr] = rstd;
+      }
+    } else {
+      mean = a.mean[row0 + warp * RW + lr];
+      rstd = a.rstd[row0 + warp * RW + lr];
+    }
+
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = v * 512 + lane * 16;
       const bool valid = at < nc;
-      float w[VE], b[VE];
-      if (valid) load_affine<VE>(a, c0 + at, w, b);
 #pragma unroll
       for (int r = 0; r < RW; ++r) {
         const int64_t row = row0 + warp * RW + r;
-        const float2 st = stat[warp * RW + r];
-        float o[VE];
+        const float2 mm = splat(__shfl_sync(0xFFFFFFFFu, mean, r * GS));
+        const float2 rr = splat(__shfl_sync(0xFFFFFFFFu, rstd, r * GS));
+        float y[16];
         float m = 0.f;
         if (valid) {
+          run(r, v, y);
 #pragma unroll
-          for (int j = 0; j < VE; ++j) {
-            o[j] = norm_value(raw[r][k].get(j), st.x, st.y, w[j], b[j]);
-            m = fmax3_nan(m, fabsf(o[j]), 0.f);
+          for (int p = 0; p < 4; ++p) {
+            const int po = p * (S / 4) + at / 4;
+            const float4 w = *reinterpret_cast<const float4*>(wtile + po), b = *reinterpret_cast<const float4*>(btile + po);
+            const float2 u0 = fma2(mul2(sub2(pair(y[4 * p], y[4 * p + 1]), mm), rr), pair(w.x, w.y), pair(b.x, b.y));
+            const float2 u1 = fma2(mul2(sub2(pair(y[4 * p + 2], y[4 * p + 3]), mm), rr), pair(w.z, w.w), pair(b.z, b.w));
+            y[4 * p] = u0.x, y[4 * p + 1] = u0.y, y[4 * p + 2] = u1.x, y[4 * p + 3] = u1.y;
+            m = fmax3_nan(m, fabsf(u0.x), fabsf(u0.y));
+            m = fmax3_nan(m, fabsf(u1.x), fabsf(u1.y));
+            if constexpr (ORIENT & MXQ_COL)
+              *reinterpret_cast<float4*>(ytile + (warp * RW + r) * S + po) = make_float4(u0.x, u0.y, u1.x, u1.y);
           }
         }
-#pragma unroll
-        for (int i = 1; i < LPB; i <<= 1) m = fmax3_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, i), 0.f);
-        float mult;
-        const uint32_t code = mx_scale<FMT>(__float_as_uint(m) & 0x7FFFFFFFu, a.ceil_mode, mult);
-        if (valid) {
-          uint32_t q[QW];
-          mx_codes<FMT, VE>(o, mult, code == 0xFFu, q);
-          const int64_t el = row * a.cols + c0 + at;
-          uint8_t* dst = a.q_row + (FMT == MXQ_E2M1 ? el / 2 : el);
-          if constexpr (FMT == MXQ_E2M1 && VE == 4) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(q[0]);
-          else if constexpr (QW == 1) *reinterpret_cast<uint32_t*>(dst) = q[0];
-          else *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
-        }
-        if (a.pack_row) {
-          uint32_t word = code << (8 * ((lane / LPB) & 3));
-          word |= __shfl_xor_sync(0xFFFFFFFFu, word, LPB);
-          word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * LPB);
-          if (valid && lane % (4 * LPB) == 0)
-            *reinterpret_cast<uint32_t*>(a.s_row + scale_at(row, (c0 + at) / 32, kb, a.mma)) = word;
-        } else if (valid && lane % LPB == 0) {
-          a.s_row[scale_at(row, (c0 + at) / 32, kb, a.mma)] = static_cast<uint8_t>(code);
+        if constexpr (ORIENT & MXQ_ROW) {
+          m = fmax3_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1), 0.f);
+          float mult;
+          const uint32_t code = mx_scale<FMT>(__float_as_uint(m) & 0x7FFFFFFFu, a.ceil_mode, mult);
+          if (valid) {
+            uint32_t q[code_words<FMT, 16>()];
+            mx_codes<FMT, 16>(y, mult, code == 0xFFu, q);
+            const int64_t el = row * a.cols + c0 + at;
+            uint8_t* dst = a.q_row + (FMT == MXQ_E2M1 ? el / 2 : el);
+            if constexpr (FMT == MXQ_E2M1) *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+            else *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
+          }
+          const int kb = a.cols / 32, k = (c0 + at) / 32;
+          if (a.pack_row) {                              // the scales of four neighbouring blocks as one word
+            uint32_t word = code << (8 * ((lane >> 1) & 3));
+            word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
+            word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
+            if (valid && lane % 8 == 0) *reinterpret_cast<uint32_t*>(a.s_row + scale_at(row, k, kb, a.mma)) = word;
+          } else if (valid && lane % 2 == 0) {
+            a.s_row[scale_at(row, k, kb, a.mma)] = static_cast<uint8_t>(code);
+          }
         }
       }
     }
-  }
+    if (tile + 1 < last) load(tile + 1);                 // in flight through the column pass
 
-  if constexpr (ORIENT & MXQ_COL) {
-    // one column per thread and turn: its 32 rows are one block
-    constexpr int QW = code_words<FMT, 32>();
-    const int kb = a.rows / 32;
-    for (int c = threadIdx.x; c < nc; c += 256) {
-      float w[1], b[1], o[32];
-      load_affine<1>(a, c0 + c, w, b);
+    if constexpr (ORIENT & MXQ_COL) {
+      __syncthreads();
+      const int kb = a.rows / 32;
+      // the word of scales is complete when its four tiles are all this CTA's
+      const bool flush = (tile & 3) == 3 || tile + 1 == last;
+      const bool word = a.pack_col && (tile & 3) == 3 && tile - 3 >= first;
 #pragma unroll
-      for (int r = 0; r < 32; ++r) {
-        const float2 st = stat[r];
-        float xv;
-        if constexpr (sizeof(TX) == 2)
-          xv = bf16lo(*reinterpret_cast<const uint16_t*>(tile + (r * SLAB + c) * 2));
-        else
-          xv = *reinterpret_cast<const float*>(tile + (r * SLAB + c) * 4);
-        o[r] = norm_value(xv, st.x, st.y, w[0], b[0]);
+      for (int u = 0; u < S / T; ++u) {
+        const int pos = threadIdx.x + u * T;             // a column of a plane
+        const int c = (pos % (S / 4)) / 4 * 16 + pos / (S / 4) * 4 + pos % 4;
+        if (c >= nc) continue;
+        float y[32];
+#pragma unroll
+        for (int r = 0; r < 32; ++r) y[r] = ytile[r * S + pos];
+        float mult;
+        const uint32_t code = mx_scale<FMT>(amax32_tree([&](int j) { return fabsf(y[j]); }), a.ceil_mode, mult);
+        uint32_t q[code_words<FMT, 32>()];
+        mx_codes<FMT, 32>(y, mult, code == 0xFFu, q);
+        const int64_t el = static_cast<int64_t>(c0 + c) * a.rows + row0;
+        uint8_t* dst = a.q_col + (FMT == MXQ_E2M1 ? el / 2 : el);
+        if constexpr (FMT == MXQ_E2M1) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
+        } else if (a.wide_col) {
+          store32(dst, q);
+        } else {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
+          *reinterpret_cast<uint4*>(dst + 16) = make_uint4(q[4], q[5], q[6], q[7]);
+        }
+        uint32_t& acc = col_scales[u];
+        acc = ((tile & 3) == 0 || tile == first ? 0u : acc) | code << (8 * (tile & 3));
+        if (word) {
+          *reinterpret_cast<uint32_t*>(a.s_col + scale_at(c0 + c, tile - 3, kb, a.mma)) = acc;
+        } else if (flush) {
+          for (int k = max(first, tile & ~3); k <= tile; ++k)
+            a.s_col[scale_at(c0 + c, k, kb, a.mma)] = static_cast<uint8_t>(acc >> (8 * (k & 3)));
+        }
       }
-      float mult;
-      const uint32_t code = mx_scale<FMT>(amax32_tree([&](int j) { return fabsf(o[j]); }), a.ceil_mode, mult);
-      uint32_t q[QW];
-      mx_codes<FMT, 32>(o, mult, code == 0xFFu, q);
-      const int64_t el = static_cast<int64_t>(c0 + c) * a.rows + row0;
-      uint8_t* dst = a.q_col + (FMT == MXQ_E2M1 ? el / 2 : el);
-#pragma unroll
-      for (int i = 0; i < QW; i += 4)
-        *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(q[i], q[i + 1], q[i + 2], q[i + 3]);
-      a.s_col[scale_at(c0 + c, row0 / 32, kb, a.mma)] = static_cast<uint8_t>(code);
+      __syncthreads();
     }
   }
+  // peers may still be sending: they wait for this CTA's sums, it for theirs,
+  // so nothing is on its way once every tile is merged -- unless a wait gave up
+  if constexpr (CLUSTER) cluster_sync();
 }
 
 // ---------------------------------------------------------------- backward
@@ -889,7 +969,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
   for (int64_t row = gi; row < a.rows; row += step) {
     const float mean = mean_n, rstd = rstd_n;
     if (row + step < a.rows) mean_n = a.mean[row + step], rstd_n = a.rstd[row + step];
-    const uint64_t mm = f32x2_splat(mean), rr = f32x2_splat(rstd);
+    const float2 mm = splat(mean), rr = splat(rstd);
     const bool in_ring = copied(row);
     if (alive) alive = mbar_wait(smem_u32(&full[g][slot]), phase, status);
     Vec<TX, VE> xs[KV];
@@ -916,23 +996,23 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
         s1[k] = uk[0];
         s2[k] = uk[0] * hk[0];
       } else {
-        uint64_t p1, p2;
+        float2 p1, p2;
 #pragma unroll
         for (int j = 0; j < VE; j += 2) {
-          const uint64_t hh = f32x2_mul(f32x2_sub(f32x2_pack(xv.get(j), xv.get(j + 1)), mm), rr);
-          const uint64_t dd = f32x2_pack(dv.get(j), dv.get(j + 1));
-          const uint64_t uu = f32x2_mul(dd, f32x2_pack(wk[j], wk[j + 1]));
-          f32x2_unpack(f32x2_fma(dd, hh, f32x2_pack(aw[k][j], aw[k][j + 1])), aw[k][j], aw[k][j + 1]);
-          f32x2_unpack(f32x2_add(dd, f32x2_pack(ab[k][j], ab[k][j + 1])), ab[k][j], ab[k][j + 1]);
-          p1 = j ? f32x2_add(p1, uu) : uu;
-          p2 = j ? f32x2_fma(uu, hh, p2) : f32x2_mul(uu, hh);
-          f32x2_unpack(hh, hk[j], hk[j + 1]);
-          f32x2_unpack(uu, uk[j], uk[j + 1]);
+          const float2 hh = mul2(sub2(pair(xv.get(j), xv.get(j + 1)), mm), rr);
+          const float2 dd = pair(dv.get(j), dv.get(j + 1));
+          const float2 uu = mul2(dd, pair(wk[j], wk[j + 1]));
+          halves(fma2(dd, hh, pair(aw[k][j], aw[k][j + 1])), aw[k][j], aw[k][j + 1]);
+          halves(add2(dd, pair(ab[k][j], ab[k][j + 1])), ab[k][j], ab[k][j + 1]);
+          p1 = j ? add2(p1, uu) : uu;
+          p2 = j ? fma2(uu, hh, p2) : mul2(uu, hh);
+          halves(hh, hk[j], hk[j + 1]);
+          halves(uu, uk[j], uk[j + 1]);
         }
         float x, y;
-        f32x2_unpack(p1, x, y);
+        halves(p1, x, y);
         s1[k] = x + y;
-        f32x2_unpack(p2, x, y);
+        halves(p2, x, y);
         s2[k] = x + y;
       }
     }
@@ -967,7 +1047,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
     }
     const float m1 = __shfl_sync(0xFFFFFFFFu, v, 0) * inv_c, m2 = __shfl_sync(0xFFFFFFFFu, v, 16) * inv_c;
     TX* dx = static_cast<TX*>(a.dx) + row * a.cols;
-    const uint64_t c1c1 = f32x2_splat(m1), c2c2 = f32x2_splat(-m2);
+    const float2 c1c1 = splat(m1), c2c2 = splat(-m2);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (!FULL && k * G + t >= nvec) continue;
@@ -985,8 +1065,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
       } else {
 #pragma unroll
         for (int j = 0; j < VE; j += 2) {
-          f32x2_unpack(f32x2_mul(f32x2_sub(f32x2_pack(xv.get(j), xv.get(j + 1)), mm), rr), hk[j], hk[j + 1]);
-          f32x2_unpack(f32x2_mul(f32x2_pack(dv.get(j), dv.get(j + 1)), f32x2_pack(wk[j], wk[j + 1])), uk[j], uk[j + 1]);
+          halves(mul2(sub2(pair(xv.get(j), xv.get(j + 1)), mm), rr), hk[j], hk[j + 1]);
+          halves(mul2(pair(dv.get(j), dv.get(j + 1)), pair(wk[j], wk[j + 1])), uk[j], uk[j + 1]);
         }
       }
       if constexpr (VE == 1) {
@@ -994,8 +1074,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
       } else {
 #pragma unroll
         for (int j = 0; j < VE; j += 2)
-          f32x2_unpack(f32x2_mul(f32x2_fma(f32x2_pack(hk[j], hk[j + 1]), c2c2,
-                                           f32x2_sub(f32x2_pack(uk[j], uk[j + 1]), c1c1)),
+          halves(mul2(fma2(pair(hk[j], hk[j + 1]), c2c2,
+                                           sub2(pair(uk[j], uk[j + 1]), c1c1)),
                                  rr),
                        o[j], o[j + 1]);
       }
@@ -1199,32 +1279,65 @@ int norm_rows(const NormArgs& a, bool vec, cudaStream_t st) {
   return dispatch_row<TX, OUT, VE>(a, st);
 }
 
-template <typename TX, int FMT, int ORIENT, bool CLUSTER>
-int launch_tile(const NormArgs& a, cudaStream_t st) {
-  constexpr int SLAB = slab_cols<TX>();
-  const int slabs = (a.cols + SLAB - 1) / SLAB;
-  const int smem = (ORIENT & MXQ_COL) ? 32 * SLAB * static_cast<int>(sizeof(TX)) : 0;
-  auto kern = norm_tile_kernel<TX, FMT, ORIENT, CLUSTER>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return MXQ_ERR_CUDA;
-  const int64_t grid = static_cast<int64_t>(slabs) * (a.rows / 32);
-  if (grid > 0x7FFFFFFF) return MXQ_ERR_BAD_SHAPE;
-  if (CLUSTER) return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(grid)), dim3(256), smem, st, slabs, a, slabs);
-  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(256), smem, st, a, slabs);
+// CTAs (clusters of `slabs`) of a tile kernel that run at once, asked once per
+// device and size.
+template <typename K>
+int resident(K kern, int slabs, int threads, int smem, std::atomic<int>& known) {
+  int n = known.load(std::memory_order_relaxed);
+  if (n) return n;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(slabs * 4 * sm_count());
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = slabs;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) return 0;
+  known.store(n, std::memory_order_relaxed);
+  return n;
 }
 
-// Rows only: the row kernel.  With column blocks: one cluster per 32 rows
-// while a portable cluster (8 CTAs) holds them, else the statistics first and
-// then the slabs on their own (x is read twice).
-template <typename TX, int FMT>
-int norm_mx(const NormArgs& a, int orient, cudaStream_t st) {
-  if (orient == MXQ_ROW && a.cols <= kMaxRowElems) return norm_rows<TX, FMT>(a, true, st);
-  if (a.cols <= 8 * slab_cols<TX>())
-    return orient == MXQ_DUAL ? launch_tile<TX, FMT, MXQ_DUAL, true>(a, st) : launch_tile<TX, FMT, MXQ_COL, true>(a, st);
+template <typename TX, int FMT, int ORIENT, bool CLUSTER, int S, int T>
+int launch_tile(const NormArgs& a, cudaStream_t st) {
+  static std::atomic<int> known[64][TILE_SLABS + 1];
+  const int slabs = (a.cols + S - 1) / S, cluster = CLUSTER ? slabs : 1;
+  const int smem = ((ORIENT & MXQ_COL) ? 34 : 2) * S * 4;
+  auto kern = norm_tile_kernel<TX, FMT, ORIENT, CLUSTER, S, T>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ERR_CUDA;
+  const int n = resident(kern, cluster, T, smem, known[dev][cluster]);
+  int* status = status_ptr();
+  if (!n || !status) return MXQ_ERR_CUDA;
+  const int64_t teams = std::min<int64_t>(a.rows / 32, CLUSTER ? n : std::max(1, n / slabs));
+  if (CLUSTER)
+    return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(teams * slabs)), dim3(T), smem, st, slabs, a, slabs, status);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(teams * slabs)), dim3(T), smem, st, a, slabs, status);
+}
+
+// Rows only: the row kernel.  With column blocks: a portable cluster (8 CTAs)
+// holds 32 rows of up to 4096 columns in slabs of 512, or 8192 in slabs of
+// 1024; longer rows get their statistics first, then slab by slab (x is read
+// twice).
+template <typename TX, int FMT, int ORIENT>
+int norm_mx_tiles(const NormArgs& a, cudaStream_t st) {
+  if constexpr (ORIENT != MXQ_ROW) {
+    if (a.cols <= TILE_SLABS * 512) return launch_tile<TX, FMT, ORIENT, true, 512, 256>(a, st);
+    if (a.cols <= TILE_SLABS * 1024) return launch_tile<TX, FMT, ORIENT, true, 1024, 512>(a, st);
+  }
   NormArgs s = a;
   s.y = nullptr;
   if (const int rc = norm_rows<TX, OUT_BF16>(s, true, st)) return rc;
-  if (orient == MXQ_ROW) return launch_tile<TX, FMT, MXQ_ROW, false>(a, st);
-  return orient == MXQ_DUAL ? launch_tile<TX, FMT, MXQ_DUAL, false>(a, st) : launch_tile<TX, FMT, MXQ_COL, false>(a, st);
+  return launch_tile<TX, FMT, ORIENT, false, 512, 256>(a, st);
+}
+
+template <typename TX, int FMT>
+int norm_mx(const NormArgs& a, int orient, cudaStream_t st) {
+  if (orient == MXQ_ROW) return a.cols <= kMaxRowElems ? norm_rows<TX, FMT>(a, true, st) : norm_mx_tiles<TX, FMT, MXQ_ROW>(a, st);
+  return orient == MXQ_DUAL ? norm_mx_tiles<TX, FMT, MXQ_DUAL>(a, st) : norm_mx_tiles<TX, FMT, MXQ_COL>(a, st);
 }
 
 template <typename TX>
@@ -1380,6 +1493,8 @@ extern "C" int mxq_layer_norm_mx(const void* x, int64_t rows, int64_t cols, int6
   a.ceil_mode = scale_mode == MXQ_SCALE_CEIL;
   a.mma = sf_layout == MXQ_SF_MMA;
   a.pack_row = cols % 128 == 0 && aligned_to(s_row, 4);
+  a.pack_col = rows % 128 == 0 && aligned_to(s_col, 4);
+  a.wide_col = aligned_to(q_col, 32);
   const auto st = static_cast<cudaStream_t>(stream);
   return x_type == MXQ_BF16 ? norm_mx_fmt<__nv_bfloat16>(a, fmt, orient, st) : norm_mx_fmt<float>(a, fmt, orient, st);
 }

@@ -111,12 +111,15 @@ __device__ __forceinline__ float tree_sum(const float (&v)[N]) {
   return t[0];
 }
 
-// a * b + c on packed pairs, one rounding each.
-__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
+// Pairs of float32 and the packed operations on them: each half rounds to
+// nearest exactly as the scalar operation would.
+__device__ __forceinline__ float2 pair(float a, float b) { return make_float2(a, b); }
+__device__ __forceinline__ float2 splat(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return __fadd2_rn(a, make_float2(-b.x, -b.y)); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ void halves(float2 p, float& x, float& y) { x = p.x, y = p.y; }
 
 // One cluster barrier, in two halves: what a thread did before the arrive is
 // visible to every thread of the cluster after the wait.
@@ -170,19 +173,22 @@ constexpr int code_words() { return FMT == MXQ_E2M1 ? (N + 7) / 8 : N / 4; }
 template <int FMT, int N>
 __device__ __forceinline__ void mx_codes(const float (&y)[N], float mult, bool bad,
                                          uint32_t (&out)[code_words<FMT, N>()]) {
+  const float2 mm = splat(mult);
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; i += 2) halves(mul2(pair(y[i], y[i + 1]), mm), v[i], v[i + 1]);
   if constexpr (FMT == MXQ_E2M1) {
 #pragma unroll
     for (int k = 0; k < code_words<FMT, N>(); ++k) {
       uint32_t w = 0;
 #pragma unroll
-      for (int i = 8 * k; i < N && i < 8 * k + 8; i += 2)
-        w |= cvt_e2m1x2(y[i] * mult, y[i + 1] * mult) << (4 * (i - 8 * k));
+      for (int i = 8 * k; i < N && i < 8 * k + 8; i += 2) w |= cvt_e2m1x2(v[i], v[i + 1]) << (4 * (i - 8 * k));
       out[k] = bad ? 0u : w;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const uint32_t w = cvt_fp8x4<FMT>(y[i] * mult, y[i + 1] * mult, y[i + 2] * mult, y[i + 3] * mult);
+      const uint32_t w = cvt_fp8x4<FMT>(v[i], v[i + 1], v[i + 2], v[i + 3]);
       out[i / 4] = bad ? 0u : w;
     }
   }
