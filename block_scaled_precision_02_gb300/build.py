@@ -18,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxq.so")
-SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "norm.cu", "loss.cu", "gradnorm.cu"]
+SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "norm.cu", "norm_mx.cu", "norm_bwd.cu", "loss.cu", "gradnorm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fno-strict-aliasing",
                 "--expt-relaxed-constexpr", "-diag-suppress", "177"]

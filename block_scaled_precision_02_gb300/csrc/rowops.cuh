@@ -183,14 +183,17 @@ __device__ __forceinline__ void mx_codes(const float (&y)[N], float mult, bool b
       uint32_t w = 0;
 #pragma unroll
       for (int i = 8 * k; i < N && i < 8 * k + 8; i += 2) w |= cvt_e2m1x2(v[i], v[i + 1]) << (4 * (i - 8 * k));
-      out[k] = bad ? 0u : w;
+      out[k] = w;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const uint32_t w = cvt_fp8x4<FMT>(v[i], v[i + 1], v[i + 2], v[i + 3]);
-      out[i / 4] = bad ? 0u : w;
+      out[i / 4] = cvt_fp8x4<FMT>(v[i], v[i + 1], v[i + 2], v[i + 3]);
     }
+  }
+  if (bad) {                                 // rare: a branch costs less than a select per word
+#pragma unroll
+    for (int k = 0; k < code_words<FMT, N>(); ++k) out[k] = 0u;
   }
 }
 
