@@ -28,7 +28,7 @@ __device__ __forceinline__ void store32(uint8_t* p, const uint32_t (&q)[8]) {
 
 constexpr int TILE_SLABS = 8;                            // CTAs of a cluster (the portable limit)
 
-template <typename TX, int FMT, int ORIENT, bool CLUSTER, int S, int T>
+template <typename TX, int FMT, int ORIENT, bool CLUSTER, int S, int T, bool FULL>
 __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const NormArgs a, int slabs, int* status) {
   constexpr int RW = 32 / (T / 32);                      // rows of a warp
   constexpr int GS = 32 / RW;                            // lanes that end up with a row's sums
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
   const int first = static_cast<int>(static_cast<int64_t>(tiles) * team / teams);
   const int last = static_cast<int>(static_cast<int64_t>(tiles) * (team + 1) / teams);
   const int c0 = rank * S;
-  const int nc = min(S, a.cols - c0);                    // columns of this slab (a multiple of 32)
+  const int nc = FULL ? S : min(S, a.cols - c0);         // columns of this slab (a multiple of 32)
   const float inv_nc = 1.f / static_cast<float>(nc), inv_c = 1.f / static_cast<float>(a.cols);
   const int lr = lane / GS, lk = lane % GS;              // this lane's row and slab in the merge
   const float n_k = static_cast<float>(lk < slabs ? min(S, a.cols - lk * S) : 0);
@@ -72,8 +72,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-          raw[r][v][i].fill(0);
-          if (v * 512 + lane * 16 < nc) raw[r][v][i].load(x + r * a.ld + v * 512 + i * WV);
+          if (!FULL) raw[r][v][i].fill(0);
+          if (FULL || v * 512 + lane * 16 < nc) raw[r][v][i].load(x + r * a.ld + v * 512 + i * WV);
         }
   };
   const auto run = [&](int r, int v, float (&f)[16]) {
@@ -105,6 +105,38 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
     return b;
   };
 
+  // the slab's part of the statistics of the rows in registers, to every CTA
+  const auto send_stats = [&](int tile) {
+    const int buf = (tile - first) & 1;
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(smem_u32(&bar[buf]), 256 * slabs);
+    float s[RW];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      s[r] = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[16];
+        run(r, v, f);
+        s[r] += vec_sum(f);
+      }
+    }
+    const float sum = rows_sum(s);
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      const float near = __shfl_sync(0xFFFFFFFFu, sum, r * GS) * inv_nc;
+      s[r] = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[16];
+        run(r, v, f);
+        if (FULL || v * 512 + lane * 16 < nc) s[r] += vec_sq_dev(f, near);
+      }
+    }
+    const float m2 = rows_sum(s);
+    if (lk < slabs)
+      st_async_f2(smem_u32(&parts[buf][rank][warp * RW + lr]), smem_u32(&bar[buf]), lk, sum, m2);
+  };
+
   uint32_t col_scales[S / T];                            // this thread's columns, a byte per tile
   if (first < last) load(first);
   for (int c = threadIdx.x * 4; c < nc; c += T * 4) {
@@ -115,38 +147,12 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
     *reinterpret_cast<float4*>(btile + at) = make_float4(b[0], b[1], b[2], b[3]);
   }
   __syncthreads();
+  if (CLUSTER && first < last) send_stats(first);
   for (int tile = first; tile < last; ++tile) {
     const int64_t row0 = static_cast<int64_t>(tile) * 32;
     float mean, rstd;                                    // of row lr of this warp
     if constexpr (CLUSTER) {
       const int buf = (tile - first) & 1;
-      if (threadIdx.x == 0) mbar_arrive_expect_tx(smem_u32(&bar[buf]), 256 * slabs);
-      float s[RW];
-#pragma unroll
-      for (int r = 0; r < RW; ++r) {
-        s[r] = 0.f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          float f[16];
-          run(r, v, f);
-          s[r] += vec_sum(f);
-        }
-      }
-      const float sum = rows_sum(s);
-#pragma unroll
-      for (int r = 0; r < RW; ++r) {
-        const float near = __shfl_sync(0xFFFFFFFFu, sum, r * GS) * inv_nc;
-        s[r] = 0.f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          float f[16];
-          run(r, v, f);
-          if (v * 512 + lane * 16 < nc) s[r] += vec_sq_dev(f, near);
-        }
-      }
-      const float m2 = rows_sum(s);
-      if (lk < slabs)
-        st_async_f2(smem_u32(&parts[buf][rank][warp * RW + lr]), smem_u32(&bar[buf]), lk, sum, m2);
       if (alive) alive = mbar_wait_sleep(smem_u32(&bar[buf]), ((tile - first) >> 1) & 1, status);
       const float2 p = lk < slabs ? parts[buf][lk][warp * RW + lr] : make_float2(0.f, 0.f);
       mean = group_sum(p.x) * inv_c;
@@ -164,7 +170,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int at = v * 512 + lane * 16;
-      const bool valid = at < nc;
+      const bool valid = FULL || at < nc;
       float y[RW][16], m[RW];
       float2 mm[RW], rr[RW];
 #pragma unroll
@@ -219,7 +225,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
         }
       }
     }
-    if (tile + 1 < last) load(tile + 1);                 // in flight through the column pass
+    if (tile + 1 < last) load(tile + 1);           // in flight through the column pass
 
     if constexpr (ORIENT & MXQ_COL) {
       __syncthreads();
@@ -229,9 +235,12 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
       const bool word = a.pack_col && (tile & 3) == 3 && tile - 3 >= first;
 #pragma unroll
       for (int u = 0; u < S / T; ++u) {
+        // between the columns: the next tile has arrived, and its statistics
+        // travel while the remaining columns are encoded
+        if (CLUSTER && u == S / T - 1 && tile + 1 < last) send_stats(tile + 1);
         const int pos = threadIdx.x + u * T;             // a column of a plane
         const int c = (pos % (S / 4)) / 4 * 16 + pos / (S / 4) * 4 + pos % 4;
-        if (c >= nc) continue;
+        if (!FULL && c >= nc) continue;                  // (the last turn: no exchange is skipped)
         float y[32];
 #pragma unroll
         for (int r = 0; r < 32; ++r) y[r] = ytile[r * S + pos];
@@ -289,12 +298,12 @@ int resident(K kern, int slabs, int threads, int smem, std::atomic<int>& known) 
   return n;
 }
 
-template <typename TX, int FMT, int ORIENT, bool CLUSTER, int S, int T>
+template <typename TX, int FMT, int ORIENT, bool CLUSTER, int S, int T, bool FULL>
 int launch_tile(const NormArgs& a, cudaStream_t st) {
   static std::atomic<int> known[64][TILE_SLABS + 1];
   const int slabs = (a.cols + S - 1) / S, cluster = CLUSTER ? slabs : 1;
   const int smem = ((ORIENT & MXQ_COL) ? 34 : 2) * S * 4;
-  auto kern = norm_tile_kernel<TX, FMT, ORIENT, CLUSTER, S, T>;
+  auto kern = norm_tile_kernel<TX, FMT, ORIENT, CLUSTER, S, T, FULL>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ERR_CUDA;
   const int n = resident(kern, cluster, T, smem, known[dev][cluster]);
@@ -306,6 +315,12 @@ int launch_tile(const NormArgs& a, cudaStream_t st) {
   return launch_pdl(kern, dim3(static_cast<unsigned>(teams * slabs)), dim3(T), smem, st, a, slabs, status);
 }
 
+template <typename TX, int FMT, int ORIENT, bool CLUSTER, int S, int T>
+int choose_tile(const NormArgs& a, cudaStream_t st) {
+  return a.cols % S == 0 ? launch_tile<TX, FMT, ORIENT, CLUSTER, S, T, true>(a, st)
+                         : launch_tile<TX, FMT, ORIENT, CLUSTER, S, T, false>(a, st);
+}
+
 // Rows only: the row kernel.  With column blocks: a portable cluster (8 CTAs)
 // holds 32 rows of up to 4096 columns in slabs of 512, or 8192 in slabs of
 // 1024; longer rows get their statistics first, then slab by slab (x is read
@@ -313,11 +328,11 @@ int launch_tile(const NormArgs& a, cudaStream_t st) {
 template <typename TX, int FMT, int ORIENT>
 int norm_mx_tiles(const NormArgs& a, cudaStream_t st) {
   if constexpr (ORIENT != MXQ_ROW) {
-    if (a.cols <= TILE_SLABS * 512) return launch_tile<TX, FMT, ORIENT, true, 512, sizeof(TX) == 2 ? 256 : 512>(a, st);
-    if (a.cols <= TILE_SLABS * 1024) return launch_tile<TX, FMT, ORIENT, true, 1024, 512>(a, st);
+    if (a.cols <= TILE_SLABS * 512) return choose_tile<TX, FMT, ORIENT, true, 512, sizeof(TX) == 2 ? 256 : 512>(a, st);
+    if (a.cols <= TILE_SLABS * 1024) return choose_tile<TX, FMT, ORIENT, true, 1024, 512>(a, st);
   }
   if (const int rc = norm_stats(a, sizeof(TX) == 2 ? MXQ_BF16 : MXQ_F32, st)) return rc;
-  return launch_tile<TX, FMT, ORIENT, false, 512, sizeof(TX) == 2 ? 256 : 512>(a, st);
+  return choose_tile<TX, FMT, ORIENT, false, 512, sizeof(TX) == 2 ? 256 : 512>(a, st);
 }
 
 template <typename TX, int FMT>
