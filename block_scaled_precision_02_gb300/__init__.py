@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 import os
 from typing import Optional
 
@@ -556,7 +557,8 @@ def _scratch(device: torch.device, nbytes: int) -> torch.Tensor:
 def _matrix(t: torch.Tensor, name: str):
     """(type code, rows, cols, row stride) of a 2-D bf16 or float32 tensor
     whose rows are contiguous (the row stride may exceed cols)."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPE:
+    code = _TYPE.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None:
         raise ValueError(f"{name} must be a bf16 or float32 tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D with contiguous rows")
@@ -564,29 +566,32 @@ def _matrix(t: torch.Tensor, name: str):
     if cols < 1:
         raise ValueError(f"{name} must have at least one column")
     if t.is_contiguous():
-        return _TYPE[t.dtype], rows, cols, cols
+        return code, rows, cols, cols
     ld, step = t.stride()
     if rows < 2:
         ld = cols
     if (cols > 1 and step != 1) or ld < cols:
         raise ValueError(f"{name} must be 2-D with contiguous rows")
-    return _TYPE[t.dtype], rows, cols, ld
+    return code, rows, cols, ld
 
 
-def _vector(t: torch.Tensor, name: str, n: int, dtypes) -> None:
+def _vector(t: torch.Tensor, name: str, n: int, dtypes) -> int:
+    """Pointer of a contiguous vector of n elements."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != 1 or not t.is_contiguous():
         names = " or ".join(str(d).replace("torch.", "") for d in dtypes)
         raise ValueError(f"{name} must be a contiguous {names} vector")
     if t.numel() != n:
         raise ValueError(f"{name} holds {t.numel()} elements, expected {n}")
+    return t.data_ptr()
 
 
-def _same_device(first: torch.Tensor, *others) -> torch.device:
-    """The CUDA device of ``first``, which every (tensor, name) must share."""
+def _same_device(names: str, *tensors) -> torch.device:
+    """The CUDA device that all tensors given (None aside) share."""
+    first = tensors[0]
     index = first.get_device()
-    for t, name in others:
+    for k, t in enumerate(tensors):
         if t is not None and (t.get_device() != index or index < 0):
-            _on_device(((t, name),), first.device)
+            _on_device(((t, names.split()[k]),), first.device)
     return first.device
 
 
@@ -594,8 +599,12 @@ def _param(t: Optional[torch.Tensor], name: str, n: int):
     """(pointer, type code) of a weight or bias vector, or of none."""
     if t is None:
         return 0, 0
-    _vector(t, name, n, _PARAM)
-    return t.data_ptr(), _TYPE[t.dtype]
+    return _vector(t, name, n, _PARAM), _TYPE[t.dtype]
+
+
+def _stats(rows: int, dev: torch.device):
+    """mean and rstd: one allocation, two rows of it."""
+    return torch.empty(2, rows, dtype=torch.float32, device=dev).unbind(0)
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -611,10 +620,9 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     out_dtype = x.dtype if out_dtype is None else out_dtype
     if out_dtype not in _TYPE:
         raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
-    dev = _same_device(x, (x, "x"), (weight, "weight"), (bias, "bias"))
+    dev = _same_device("x weight bias", x, weight, bias)
     y = torch.empty(rows, cols, dtype=out_dtype, device=dev)
-    mean = torch.empty(rows, dtype=torch.float32, device=dev)
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    mean, rstd = _stats(rows, dev)
     _launch("mxq_layer_norm", dev, x.data_ptr(), rows, cols, ld, xt, w, wt, b, bt, eps, _TYPE[out_dtype], y.data_ptr(),
             mean.data_ptr(), rstd.data_ptr())
     return y, mean, rstd
@@ -630,7 +638,7 @@ def mx_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
     xt, rows, cols, ld = _matrix(x, "x")
     w, wt = _param(weight, "weight", cols)
     b, bt = _param(bias, "bias", cols)
-    dev = _same_device(x, (x, "x"), (weight, "weight"), (bias, "bias"))
+    dev = _same_device("x weight bias", x, weight, bias)
     qb = 2 if f == E2M1 else 1
     q_row = s_row = q_col = s_col = None
     rp = rs = cp = cs = 0
@@ -642,8 +650,7 @@ def mx_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
         q_col = torch.empty(cols, rows // qb, dtype=torch.uint8, device=dev)
         s_col = torch.empty(cols, rows // 32, dtype=torch.uint8, device=dev)
         cp, cs = q_col.data_ptr(), s_col.data_ptr()
-    mean = torch.empty(rows, dtype=torch.float32, device=dev)
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    mean, rstd = _stats(rows, dev)
     _launch("mxq_layer_norm_mx", dev, x.data_ptr(), rows, cols, ld, xt, w, wt, b, bt, eps, f, o, sm, sf, rp, rs, cp, cs,
             mean.data_ptr(), rstd.data_ptr())
     return q_row, s_row, q_col, s_col, mean, rstd
@@ -661,21 +668,20 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
         raise ValueError(f"dy is {tuple(dy.shape)}, x {tuple(x.shape)}")
     if mean is None or rstd is None:
         raise ValueError("mean and rstd are the forward pass's")
-    _vector(mean, "mean", rows, _F32_ONLY)
-    _vector(rstd, "rstd", rows, _F32_ONLY)
+    mp = _vector(mean, "mean", rows, _F32_ONLY)
+    rp = _vector(rstd, "rstd", rows, _F32_ONLY)
     w, wt = _param(weight, "weight", cols)
-    dev = _same_device(x, (x, "x"), (dy, "dy"), (mean, "mean"), (rstd, "rstd"), (weight, "weight"))
+    dev = _same_device("x dy mean rstd weight", x, dy, mean, rstd, weight)
     dx = torch.empty(rows, cols, dtype=x.dtype, device=dev)
     dw = db = None
     wp = bp = 0
     if param_grads:
-        dw = torch.empty(cols, dtype=torch.float32, device=dev)
-        db = torch.empty(cols, dtype=torch.float32, device=dev)
+        dw, db = torch.empty(2, cols, dtype=torch.float32, device=dev).unbind(0)
         wp, bp = dw.data_ptr(), db.data_ptr()
     need = _size("mxq_layer_norm_backward_workspace_size", dev, rows, cols)
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch("mxq_layer_norm_backward", dev, dy.data_ptr(), ld_dy, dt, x.data_ptr(), ld, xt, rows, cols, mean.data_ptr(),
-            rstd.data_ptr(), w, wt, dx.data_ptr(), wp, bp, ws.data_ptr(), need)
+    _launch("mxq_layer_norm_backward", dev, dy.data_ptr(), ld_dy, dt, x.data_ptr(), ld, xt, rows, cols, mp, rp, w, wt,
+            dx.data_ptr(), wp, bp, ws.data_ptr(), need)
     return dx, dw, db
 
 
@@ -703,18 +709,17 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Ten
     for t, name in ((targets, "targets"), (old_logp, "old_logp"), (advantages, "advantages"), (weights, "weights")):
         if t is None:
             raise ValueError(f"{name} is needed")
-    _vector(targets, "targets", tokens, (torch.int64, torch.int32))
-    _vector(old_logp, "old_logp", tokens, _F32_ONLY)
-    _vector(advantages, "advantages", tokens, _F32_ONLY)
-    _vector(weights, "weights", tokens, _F32_ONLY)
-    ref = 0
+    tp = _vector(targets, "targets", tokens, (torch.int64, torch.int32))
+    op = _vector(old_logp, "old_logp", tokens, _F32_ONLY)
+    ap = _vector(advantages, "advantages", tokens, _F32_ONLY)
+    wp = _vector(weights, "weights", tokens, _F32_ONLY)
+    rp = 0
     if ref_logp is not None:
-        _vector(ref_logp, "ref_logp", tokens, _F32_ONLY)
-        ref = ref_logp.data_ptr()
+        rp = _vector(ref_logp, "ref_logp", tokens, _F32_ONLY)
     elif beta != 0:
         raise ValueError("ref_logp is needed")
-    dev = _same_device(logits, (logits, "logits"), (targets, "targets"), (old_logp, "old_logp"),
-                       (advantages, "advantages"), (weights, "weights"), (ref_logp, "ref_logp"))
+    dev = _same_device("logits targets old_logp advantages weights ref_logp", logits, targets, old_logp, advantages,
+                       weights, ref_logp)
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     logp = torch.empty(tokens, dtype=torch.float32, device=dev)
     dz = None
@@ -723,9 +728,8 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Ten
         dz = torch.empty(tokens, vocab, dtype=grad_dtype, device=dev)
         gp = dz.data_ptr()
     ws = _scratch(dev, _size("mxq_policy_loss_workspace_size", dev, tokens))
-    _launch("mxq_policy_loss", dev, logits.data_ptr(), tokens, vocab, ld, zt, targets.data_ptr(),
-            int(targets.dtype == torch.int64), old_logp.data_ptr(), advantages.data_ptr(), weights.data_ptr(), ref,
-            clip_low, clip_high, beta, grad_scale, loss.data_ptr(), logp.data_ptr(), gp, vocab, _TYPE[grad_dtype],
+    _launch("mxq_policy_loss", dev, logits.data_ptr(), tokens, vocab, ld, zt, tp,
+            int(targets.dtype == torch.int64), op, ap, wp, rp, clip_low, clip_high, beta, grad_scale, loss.data_ptr(), logp.data_ptr(), gp, vocab, _TYPE[grad_dtype],
             ws.data_ptr(), ws.numel())
     return loss, logp, dz
 
@@ -740,47 +744,57 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
-def _grad_tensors(ts, what: str):
+_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
+
+
+def _grad_types(ts, what: str):
     """Type codes of a list of gradient tensors, each filling its stretch of memory."""
-    types = []
     for k, t in enumerate(ts):
-        code = _TYPE.get(t.dtype) if isinstance(t, torch.Tensor) else None
-        if code is None:
+        if not isinstance(t, torch.Tensor) or t.dtype not in _TYPE:
             raise ValueError(f"{what}[{k}] must be a bf16 or float32 tensor")
-        if not t.is_contiguous() and not _dense(t):
-            raise ValueError(f"{what}[{k}] must fill its storage (contiguous, or a transpose of such)")
-        types.append(code)
-    return types
+    if not all(map(torch.Tensor.is_contiguous, ts)):
+        for k, t in enumerate(ts):
+            if not t.is_contiguous() and not _dense(t):
+                raise ValueError(f"{what}[{k}] must fill its storage (contiguous, or a transpose of such)")
+    return [_TYPE[d] for d in map(_dtype_of, ts)]
 
 
 def _grad_call(name: str, grads, out, *args) -> torch.Tensor:
     """Check the lists and run entry point ``name`` on them: one mxq_grad per
-    tensor, written as four 64-bit words."""
+    tensor, written as four 64-bit words.  Attributes are fetched list by
+    list: the loop over tensors is what a short call's time goes to."""
     grads = list(grads)
     if not grads:
         raise ValueError("at least one gradient tensor")
-    types = _grad_tensors(grads, "grads")
-    outs, out_types = grads, types
+    n = len(grads)
+    types = _grad_types(grads, "grads")
+    outs = grads
     if out is not None:
         outs = list(out)
-        if len(outs) != len(grads):
-            raise ValueError(f"{len(grads)} gradients, {len(outs)} outputs")
-        out_types = _grad_tensors(outs, "out")
-        for k, (g, o) in enumerate(zip(grads, outs)):
-            if o.shape != g.shape or not (g.is_contiguous() and o.is_contiguous() or g.stride() == o.stride()):
-                raise ValueError(f"out[{k}] must have the shape and strides of grads[{k}]")
+        if len(outs) != n:
+            raise ValueError(f"{n} gradients, {len(outs)} outputs")
+        types = [g | o << 32 for g, o in zip(types, _grad_types(outs, "out"))]
+        if list(map(_shape_of, grads)) != list(map(_shape_of, outs)) or not (
+                all(map(torch.Tensor.is_contiguous, grads)) and all(map(torch.Tensor.is_contiguous, outs))):
+            for k, (g, o) in enumerate(zip(grads, outs)):
+                if o.shape != g.shape or not (g.is_contiguous() and o.is_contiguous() or g.stride() == o.stride()):
+                    raise ValueError(f"out[{k}] must have the shape and strides of grads[{k}]")
+    else:
+        types = [g | g << 32 for g in types]
     dev, index = grads[0].device, grads[0].get_device()
-    for ts, what in ((grads, "grads"), (outs, "out")):
-        for k, t in enumerate(ts):
-            if t.get_device() != index or index < 0:
+    for ts, what in ((grads, "grads"),) if out is None else ((grads, "grads"), (outs, "out")):
+        if index < 0 or set(map(torch.Tensor.get_device, ts)) != {index}:
+            for k, t in enumerate(ts):
                 _on_device(((t, f"{what}[{k}]"),), dev)
-    words = array.array("q")
-    for g, o, gt, ot in zip(grads, outs, types, out_types):
-        words.extend((g.data_ptr(), o.data_ptr(), g.numel(), gt | ot << 32))
+    words = array.array("q", bytes(32 * n))
+    words[0::4] = pointers = array.array("q", map(torch.Tensor.data_ptr, grads))
+    words[1::4] = pointers if out is None else array.array("q", map(torch.Tensor.data_ptr, outs))
+    words[2::4] = array.array("q", map(torch.Tensor.numel, grads))
+    words[3::4] = array.array("q", types)
     norm = torch.empty(1, dtype=torch.float32, device=dev)
-    need = _size("mxq_grad_norm_workspace_size", dev, len(grads))
+    need = _size("mxq_grad_norm_workspace_size", dev, n)
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch(name, dev, words.buffer_info()[0], len(grads), *args, norm.data_ptr(), ws.data_ptr(), need)
+    _launch(name, dev, words.buffer_info()[0], n, *args, norm.data_ptr(), ws.data_ptr(), need)
     return norm
 
 

@@ -65,7 +65,7 @@ __device__ __forceinline__ void add_squares(const float (&v)[N], double& acc) {
 template <typename T>
 __device__ __forceinline__ void squares_of(const T* p, int len, double& acc) {
   constexpr int VE = 16 / static_cast<int>(sizeof(T));
-  constexpr int U = 4;                               // vectors in flight
+  constexpr int U = sizeof(T) == 2 ? 4 : 8;          // vectors in flight: 32 elements
   int done = 0;
   if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
     const int nvec = len / VE;
@@ -93,15 +93,18 @@ __device__ __forceinline__ void squares_of(const T* p, int len, double& acc) {
   }
 }
 
+// Sum over the CTA, in thread 0.  Float64 runs at two lanes a cycle on an SM,
+// so one warp finishes.
 __device__ __forceinline__ double block_sum(double v) {
   __shared__ double red[TPB / 32];
   v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  double s = red[0];
+  if (threadIdx.x >= 32) return 0.0;
+  v = threadIdx.x < TPB / 32 ? red[threadIdx.x] : 0.0;
 #pragma unroll
-  for (int i = 1; i < TPB / 32; ++i) s += red[i];
-  return s;
+  for (int o = TPB / 64; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
 }
 
 template <int N>
@@ -119,11 +122,17 @@ __global__ void __launch_bounds__(TPB) square_sum_kernel(const __grid_constant__
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-// The sum of all parts in a fixed order, the same in every CTA.
+// Root of the sum of all parts, added in a fixed order, the same in every CTA.
+// The float32 root of a sum within float32's range is within an ulp of the
+// float64 one and takes a fraction of its time.
 __device__ __forceinline__ float norm_of(const double* part, int parts) {
+  __shared__ float norm;
   double s = 0.0;
   for (int i = threadIdx.x; i < parts; i += TPB) s += part[i];
-  return static_cast<float>(sqrt(block_sum(s)));
+  s = block_sum(s);
+  if (threadIdx.x == 0) norm = s > 1e-30 && s < 1e30 ? sqrtf(static_cast<float>(s)) : static_cast<float>(sqrt(s));
+  __syncthreads();
+  return norm;
 }
 
 __global__ void __launch_bounds__(TPB) norm_kernel(const double* part, int parts, float* norm) {
