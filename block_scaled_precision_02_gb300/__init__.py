@@ -602,11 +602,6 @@ def _param(t: Optional[torch.Tensor], name: str, n: int):
     return _vector(t, name, n, _PARAM), _TYPE[t.dtype]
 
 
-def _stats(rows: int, dev: torch.device):
-    """mean and rstd: one allocation, two rows of it."""
-    return torch.empty(2, rows, dtype=torch.float32, device=dev).unbind(0)
-
-
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                eps: float = 1e-5, out_dtype: Optional[torch.dtype] = None):
     """Layer norm of the rows of ``x`` [rows][cols] (bf16 or float32, any
@@ -622,7 +617,8 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
     dev = _same_device("x weight bias", x, weight, bias)
     y = torch.empty(rows, cols, dtype=out_dtype, device=dev)
-    mean, rstd = _stats(rows, dev)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     _launch("mxq_layer_norm", dev, x.data_ptr(), rows, cols, ld, xt, w, wt, b, bt, eps, _TYPE[out_dtype], y.data_ptr(),
             mean.data_ptr(), rstd.data_ptr())
     return y, mean, rstd
@@ -650,7 +646,8 @@ def mx_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
         q_col = torch.empty(cols, rows // qb, dtype=torch.uint8, device=dev)
         s_col = torch.empty(cols, rows // 32, dtype=torch.uint8, device=dev)
         cp, cs = q_col.data_ptr(), s_col.data_ptr()
-    mean, rstd = _stats(rows, dev)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     _launch("mxq_layer_norm_mx", dev, x.data_ptr(), rows, cols, ld, xt, w, wt, b, bt, eps, f, o, sm, sf, rp, rs, cp, cs,
             mean.data_ptr(), rstd.data_ptr())
     return q_row, s_row, q_col, s_col, mean, rstd
@@ -676,7 +673,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     dw = db = None
     wp = bp = 0
     if param_grads:
-        dw, db = torch.empty(2, cols, dtype=torch.float32, device=dev).unbind(0)
+        dw = torch.empty(cols, dtype=torch.float32, device=dev)
+        db = torch.empty(cols, dtype=torch.float32, device=dev)
         wp, bp = dw.data_ptr(), db.data_ptr()
     need = _size("mxq_layer_norm_backward_workspace_size", dev, rows, cols)
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
