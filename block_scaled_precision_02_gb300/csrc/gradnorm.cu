@@ -26,20 +26,19 @@ struct Entry {
 template <int N>
 struct Table {
   Entry e[N];
+  uint16_t from[N / 4 + 1];  // the entry of chunk i << shift: where a search starts
+  int shift;
   int count;
   uint32_t chunks;
-  int chunk;               // elements (a multiple of 8)
+  int chunk;                 // elements (a multiple of 8)
 };
 
+// The last entry with first <= c: its bucket's first entry, then onwards.
 template <int N>
 __device__ __forceinline__ int entry_of(const Table<N>& t, uint32_t c) {
-  int lo = 0, hi = t.count - 1;                      // the last entry with first <= c
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.e[mid].first <= c) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
+  int i = t.from[c >> t.shift];
+  while (i + 1 < t.count && t.e[i + 1].first <= c) ++i;
+  return i;
 }
 
 // A thread's sum of squares.  Squares of ordinary values add up in float32
@@ -173,20 +172,29 @@ __device__ __forceinline__ void scale_of(const TI* p, TO* o, int len, float c) {
   }
 }
 
-// Every CTA derives the factor from the parts, then scales its chunks, last
-// first: the chunks that the norm kernel read last are still in L2.
-template <int N>
+// Scales its chunks, last first: the chunks that the norm kernel read last are
+// still in L2.  SUM: a few CTAs, each of which derives the norm from the parts
+// (a short list is one launch shorter); otherwise one CTA per chunk with the
+// norm given: launched in order, the chunks in flight stay close together in
+// memory, which HBM rewards (402.9 M bf16 to float32: 455 us with 608 CTAs
+// striding over 16384-element chunks, PLACEHOLDER us with one per 4096).
+template <int N, bool SUM>
 __global__ void __launch_bounds__(TPB) scale_kernel(const __grid_constant__ Table<N> t, const double* part, int parts,
                                                     float max_norm, float* norm) {
   grid_dep_wait();
-  const float n = norm_of(part, parts);
-  if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = n;
+  float n;
+  if constexpr (SUM) {
+    n = norm_of(part, parts);
+    if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = n;
+  } else {
+    n = norm[0];
+  }
   float c = max_norm / (n + 1e-6f);
   if (c > 1.f) c = 1.f;                              // a NaN norm stays NaN
   for (uint32_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
     const uint32_t ch = t.chunks - 1 - k;
     const Entry& e = t.e[entry_of(t, ch)];
-    if (c == 1.f && e.g == e.out) continue;          // in place and nothing to change
+    if (e.g == e.out && c == 1.f) continue;          // in place and nothing to change
     const int64_t off = static_cast<int64_t>(ch - e.first) * t.chunk;
     const int len = static_cast<int>(min(static_cast<int64_t>(t.chunk), e.n - off));
     const float* gf = static_cast<const float*>(e.g) + off;
@@ -244,6 +252,12 @@ bool next_table(const mxq_grad* g, int n, int chunk, int* i, Table<N>& t) {
                            static_cast<int16_t>(s.out_type == MXQ_F32)};
     t.chunks += static_cast<uint32_t>(c);
   }
+  t.shift = 0;
+  while ((t.chunks >> t.shift) > N / 4) ++t.shift;
+  for (uint32_t b = 0, k = 0; t.count && b <= (t.chunks - 1) >> t.shift; ++b) {
+    while (k + 1 < static_cast<uint32_t>(t.count) && t.e[k + 1].first <= b << t.shift) ++k;
+    t.from[b] = static_cast<uint16_t>(k);
+  }
   return t.count > 0;
 }
 
@@ -258,12 +272,16 @@ int run(const mxq_grad* g, int n, int64_t total, bool clip, float max_norm, floa
     if (rc) return rc;
     parts += grid;
   }
-  if (!clip || !parts)
-    return launch_pdl(norm_kernel, dim3(1), dim3(TPB), 0, st, static_cast<const double*>(part), parts, norm);
-  for (int i = 0; next_table(g, n, chunk, &i, t);) {
-    const int grid = static_cast<int>(std::min<int64_t>(t.chunks, grid_limit()));
-    const int rc = launch_pdl(scale_kernel<N>, dim3(grid), dim3(TPB), 0, st, t, static_cast<const double*>(part), parts,
-                              max_norm, norm);
+  const bool direct = total > 16ll * grid_limit() * 2048;       // every CTA of the norm kernel had 16 rounds or more
+  if (!clip || !parts || direct) {
+    const int rc = launch_pdl(norm_kernel, dim3(1), dim3(TPB), 0, st, static_cast<const double*>(part), parts, norm);
+    if (rc || !clip || !parts) return rc;
+  }
+  for (int i = 0; next_table(g, n, direct ? 4096 : chunk, &i, t);) {
+    const double* p = part;
+    const int rc = direct ? launch_pdl(scale_kernel<N, false>, dim3(t.chunks), dim3(TPB), 0, st, t, p, parts, max_norm, norm)
+                          : launch_pdl(scale_kernel<N, true>, dim3(std::min<int64_t>(t.chunks, grid_limit())), dim3(TPB), 0,
+                                       st, t, p, parts, max_norm, norm);
     if (rc) return rc;
   }
   return MXQ_OK;
