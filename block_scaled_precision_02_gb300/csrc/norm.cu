@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArg
   __shared__ __align__(8) uint64_t full[MAX_GROUPS][MAX_STAGES];
   const int lane = threadIdx.x & 31;
   const int P = blockDim.x / G, g = threadIdx.x / G, t = threadIdx.x - g * G;
-  const int gw = t >> 5, wpg = G >> 5;
+  const int gw = t >> 5, wpg = G >> 5, first = first_vec<NV>(gw, lane);
   if (t == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[g][i]), 1);
     fence_mbar_init();
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArg
   uint8_t* slots = ring + slot_bytes(8 * a.cols, true) + static_cast<size_t>(g) * stages * sb;
   const int64_t gi = static_cast<int64_t>(blockIdx.x) * P + g, step = static_cast<int64_t>(gridDim.x) * P;
   const float inv_c = 1.f / static_cast<float>(a.cols);
-  const int n_mine = warp_count<VE, NV>(a.cols, G, gw), n_lane = lane < wpg ? warp_count<VE, NV>(a.cols, G, lane) : 0;
+  const int n_mine = warp_count<VE, NV>(a.cols, gw), n_lane = lane < wpg ? warp_count<VE, NV>(a.cols, lane) : 0;
   const float inv_mine = n_mine ? 1.f / static_cast<float>(n_mine) : 0.f;
   const float inv_lane = n_lane ? 1.f / static_cast<float>(n_lane) : 0.f;
   bool alive = true;
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArg
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         if (!FULL) v[k].fill(0);
-        if (FULL || k * G + t < nvec) v[k].load(from + (k * G + t) * VE);
+        if (FULL || first + 32 * k < nvec) v[k].load(from + (first + 32 * k) * VE);
       }
     };
     const auto wide = [&](int k, float (&f)[VE]) {
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArg
     for (int k = 0; k < NV; ++k) {
       float f[VE];
       wide(k, f);
-      s[k] = FULL || k * G + t < nvec ? vec_sq_dev(f, near) : 0.f;
+      s[k] = FULL || first + 32 * k < nvec ? vec_sq_dev(f, near) : 0.f;
     }
     float mean = near, m2 = warp_sum(tree_sum(s));
     if (wpg > 1) {
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArg
     const float2 mm = splat(mean), rr = splat(rstd);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int at = (k * G + t) * VE;
+      const int at = (first + 32 * k) * VE;
       if (!FULL && at >= a.cols) continue;
       float f[VE], o[VE];
       wide(k, f);

@@ -57,26 +57,26 @@ __device__ __forceinline__ void load_affine(const NormArgs& a, int at, float (&w
     for (int j = 0; j < VE; ++j) b[j] = 0.f;
 }
 
-// Elements of a row of `cols` that warp w of a group of G threads holds, when
-// thread t holds the vectors k*G + t.
+// Where a thread's vectors lie in a row: warp w of a group holds 32 * NV
+// vectors in a row, lane l those at first + 32 k (fixed distances from one
+// address, so loads and stores need no arithmetic of their own).
+template <int NV>
+__device__ __forceinline__ int first_vec(int w, int lane) { return w * 32 * NV + lane; }
+
+// Elements of a row of `cols` that warp w holds.
 template <int VE, int NV>
-__device__ __forceinline__ int warp_count(int cols, int G, int w) {
-  int n = 0;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) n += max(0, min(32 * VE, cols - (k * G + 32 * w) * VE));
-  return n;
-}
+__device__ __forceinline__ int warp_count(int cols, int w) { return max(0, min(32 * NV * VE, cols - w * 32 * NV * VE)); }
 
 // Sum of squared deviations of a thread's valid vectors from m.
 template <int VE, int NV>
-__device__ __forceinline__ float sq_dev(const float (&v)[NV][VE], float m, int t, int G, int nvec) {
+__device__ __forceinline__ float sq_dev(const float (&v)[NV][VE], float m, int first, int nvec) {
   float s[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     float d[VE];
 #pragma unroll
     for (int j = 0; j < VE; ++j) d[j] = (v[k][j] - m) * (v[k][j] - m);
-    s[k] = k * G + t < nvec ? tree_sum(d) : 0.f;
+    s[k] = first + 32 * k < nvec ? tree_sum(d) : 0.f;
   }
   return tree_sum(s);
 }
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_row_kernel(const NormA
   __shared__ float2 part[32];
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = WARP ? 32 : blockDim.x, t = WARP ? lane : threadIdx.x;
+  const int first = first_vec<NV>(WARP ? 0 : warp, lane);
   const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
   if (WARP && row >= a.rows) return;
   const int nvec = a.cols / VE;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_row_kernel(const NormA
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       raw[k].fill(0);
-      if (k * G + t < nvec) raw[k].load(x + (k * G + t) * VE);
+      if (first + 32 * k < nvec) raw[k].load(x + (first + 32 * k) * VE);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -147,21 +147,21 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_row_kernel(const NormA
   float mean, m2;
   if constexpr (WARP) {
     mean = sum * inv_c;
-    m2 = warp_sum(sq_dev<VE, NV>(v, mean, t, G, nvec));
+    m2 = warp_sum(sq_dev<VE, NV>(v, mean, first, nvec));
   } else {
-    const int n = warp_count<VE, NV>(a.cols, G, warp);
-    m2 = warp_sum(sq_dev<VE, NV>(v, n ? sum / static_cast<float>(n) : 0.f, t, G, nvec));
+    const int n = warp_count<VE, NV>(a.cols, warp);
+    m2 = warp_sum(sq_dev<VE, NV>(v, n ? sum / static_cast<float>(n) : 0.f, first, nvec));
     if (lane == 0) part[warp] = make_float2(sum, m2);
     __syncthreads();
-    const bool have = lane < (G >> 5);
+    const bool have = lane < static_cast<int>(blockDim.x >> 5);
     const float2 pw = have ? part[lane] : make_float2(0.f, 0.f);
-    const int nw = have ? warp_count<VE, NV>(a.cols, G, lane) : 0;
+    const int nw = have ? warp_count<VE, NV>(a.cols, lane) : 0;
     mean = warp_sum(pw.x) * inv_c;
     const float d = nw ? pw.x / static_cast<float>(nw) - mean : 0.f;
     m2 = warp_sum(pw.y + static_cast<float>(nw) * d * d);
   }
   const float rstd = 1.f / sqrtf(m2 * inv_c + a.eps);
-  if (t == 0) {
+  if (first == 0) {
     a.mean[row] = mean;
     a.rstd[row] = rstd;
   }
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_row_kernel(const NormA
     TY* y = static_cast<TY*>(a.y) + row * a.cols;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int at = (k * G + t) * VE;
+      const int at = (first + 32 * k) * VE;
       if (at >= nvec * VE) continue;
       float w[VE], b[VE], o[VE];
       load_affine<VE>(a, at, w, b);
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_row_kernel(const NormA
     const int kb = a.cols / 32;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int at = (k * G + t) * VE;
+      const int at = (first + 32 * k) * VE;
       const bool valid = at < a.cols;
       float o[VE];
       float m = 0.f;

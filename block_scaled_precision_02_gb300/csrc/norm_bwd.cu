@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) 
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int P = blockDim.x / G, g = threadIdx.x / G, t = threadIdx.x - g * G;
-  const int wpg = G >> 5;
+  const int wpg = G >> 5, first = first_vec<NV>(t >> 5, lane);
   const int nvec = a.cols / VE;
   const float inv_c = 1.f / static_cast<float>(a.cols);
 
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) 
       w[k][j] = 1.f;
       aw[k][j] = ab[k][j] = 0.f;
     }
-    if (a.w && k * G + t < nvec) load_param<VE>(a.w, a.w_f32, (k * G + t) * VE, w[k]);
+    if (a.w && first + 32 * k < nvec) load_param<VE>(a.w, a.w_f32, (first + 32 * k) * VE, w[k]);
   }
 
   int buf = 0;
@@ -68,9 +68,9 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) 
       for (int k = 0; k < NV; ++k) {
         xr[r][k].fill(0);
         dr[r][k].fill(0);
-        if (in && k * G + t < nvec) {
-          xr[r][k].load(static_cast<const TX*>(a.x) + (row + r) * a.ld_x + (k * G + t) * VE);
-          dr[r][k].load(static_cast<const TD*>(a.dy) + (row + r) * a.ld_dy + (k * G + t) * VE);
+        if (in && first + 32 * k < nvec) {
+          xr[r][k].load(static_cast<const TX*>(a.x) + (row + r) * a.ld_x + (first + 32 * k) * VE);
+          dr[r][k].load(static_cast<const TD*>(a.dy) + (row + r) * a.ld_dy + (first + 32 * k) * VE);
         }
       }
     }
@@ -117,14 +117,14 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) 
       const float m1 = c1[r] * inv_c, m2 = c2[r] * inv_c;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if (k * G + t >= nvec) continue;
+        if (first + 32 * k >= nvec) continue;
         float o[VE];
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
           const float h = (xr[r][k].get(j) - mean[r]) * rstd[r];
           o[j] = (fmaf(dr[r][k].get(j), w[k][j], -m1) - h * m2) * rstd[r];
         }
-        store_vec<TX, VE>(static_cast<TX*>(a.dx) + (row + r) * a.cols + (k * G + t) * VE, o);
+        store_vec<TX, VE>(static_cast<TX*>(a.dx) + (row + r) * a.cols + (first + 32 * k) * VE, o);
       }
     }
   }
@@ -155,13 +155,13 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) 
   }
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    if (k * G + t >= nvec) continue;
+    if (first + 32 * k >= nvec) continue;
     if constexpr (VE == 1) {
-      out[k * G + t] = aw[k][0];
-      out[a.cols + k * G + t] = ab[k][0];
+      out[first + 32 * k] = aw[k][0];
+      out[a.cols + first + 32 * k] = ab[k][0];
     } else {
-      store_vec<float, VE>(out + (k * G + t) * VE, aw[k]);
-      store_vec<float, VE>(out + a.cols + (k * G + t) * VE, ab[k]);
+      store_vec<float, VE>(out + (first + 32 * k) * VE, aw[k]);
+      store_vec<float, VE>(out + a.cols + (first + 32 * k) * VE, ab[k]);
     }
   }
 }
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
   __shared__ __align__(8) uint64_t full[MAX_GROUPS][MAX_STAGES];
   const int lane = threadIdx.x & 31;
   const int P = blockDim.x / G, g = threadIdx.x / G, t = threadIdx.x - g * G;
-  const int gw = t >> 5, wpg = G >> 5;
+  const int gw = t >> 5, wpg = G >> 5, first = first_vec<NV>(gw, lane);
   if (t == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[g][i]), 1);
     fence_mbar_init();
@@ -213,15 +213,15 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
     if (!FULL) {
       xv.fill(0);
       dv.fill(0);
-      if (k * G + t >= nvec) return;
+      if (first + 32 * k >= nvec) return;
     }
     if (in_ring) {
       const uint8_t* p = slots + slot * sb;
-      xv.load(reinterpret_cast<const TX*>(p + (VE > 1 ? 0 : sx.head(row))) + (k * G + t) * VE);
-      dv.load(reinterpret_cast<const TD*>(p + xb + (VE > 1 ? 0 : sd.head(row))) + (k * G + t) * VE);
+      xv.load(reinterpret_cast<const TX*>(p + (VE > 1 ? 0 : sx.head(row))) + (first + 32 * k) * VE);
+      dv.load(reinterpret_cast<const TD*>(p + xb + (VE > 1 ? 0 : sd.head(row))) + (first + 32 * k) * VE);
     } else {
-      xv.load(sx.row(row) + (k * G + t) * VE);
-      dv.load(sd.row(row) + (k * G + t) * VE);
+      xv.load(sx.row(row) + (first + 32 * k) * VE);
+      dv.load(sd.row(row) + (first + 32 * k) * VE);
     }
   };
   if (t == 0)
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
   for (int k = 0; k < KV; ++k) {
 #pragma unroll
     for (int j = 0; j < VE; ++j) w[k][j] = 1.f;
-    if (KEEP && a.w && k * G + t < nvec) load_param<VE>(a.w, a.w_f32, (k * G + t) * VE, w[k]);
+    if (KEEP && a.w && first + 32 * k < nvec) load_param<VE>(a.w, a.w_f32, (first + 32 * k) * VE, w[k]);
   }
   if (!KEEP && a.w)
     for (int i = threadIdx.x; i < a.cols; i += blockDim.x) {
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
       float hk[VE], uk[VE], wk[VE];
 #pragma unroll
       for (int j = 0; j < VE; ++j) wk[j] = KEEP ? w[KEEP ? k : 0][j] : 1.f;
-      if (!KEEP && a.w && (FULL || k * G + t < nvec)) load_param<VE>(ws, a.w_f32, (k * G + t) * VE, wk);
+      if (!KEEP && a.w && (FULL || first + 32 * k < nvec)) load_param<VE>(ws, a.w_f32, (first + 32 * k) * VE, wk);
       if constexpr (VE == 1) {
         const float d = dv.get(0);
         hk[0] = (xv.get(0) - mean) * rstd;
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
     const float2 c1c1 = splat(m1), c2c2 = splat(-m2);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (!FULL && k * G + t >= nvec) continue;
+      if (!FULL && first + 32 * k >= nvec) continue;
       float hk[VE], uk[VE], o[VE];
       Vec<TX, VE>& xv = xs[KEEP ? k : 0];
       Vec<TD, VE>& dv = ds[KEEP ? k : 0];
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
       float wk[VE];
 #pragma unroll
       for (int j = 0; j < VE; ++j) wk[j] = KEEP ? w[KEEP ? k : 0][j] : 1.f;
-      if (!KEEP && a.w) load_param<VE>(ws, a.w_f32, (k * G + t) * VE, wk);
+      if (!KEEP && a.w) load_param<VE>(ws, a.w_f32, (first + 32 * k) * VE, wk);
       if constexpr (VE == 1) {
         hk[0] = (xv.get(0) - mean) * rstd;
         uk[0] = dv.get(0) * wk[0];
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
                                  rr),
                        o[j], o[j + 1]);
       }
-      store_vec<TX, VE>(dx + (k * G + t) * VE, o);
+      store_vec<TX, VE>(dx + (first + 32 * k) * VE, o);
     }
     if (++slot == stages) slot = 0, phase ^= 1;
   }
@@ -391,9 +391,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
   if (g) return;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    if (k * G + t >= nvec) continue;
-    store_vec<float, VE>(out + (k * G + t) * VE, aw[k]);
-    store_vec<float, VE>(out + a.cols + (k * G + t) * VE, ab[k]);
+    if (first + 32 * k >= nvec) continue;
+    store_vec<float, VE>(out + (first + 32 * k) * VE, aw[k]);
+    store_vec<float, VE>(out + a.cols + (first + 32 * k) * VE, ab[k]);
   }
 }
 
