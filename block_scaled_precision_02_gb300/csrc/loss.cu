@@ -105,17 +105,10 @@ __device__ __forceinline__ void token_loss(const LossArgs& a, int64_t row, float
   }
 }
 
-// The last of `ctas` CTAs to finish adds the tokens' terms in their order per
-// thread and the threads' sums in a fixed tree, in float64.
-__device__ __forceinline__ void finish_loss(const LossArgs& a, unsigned ctas) {
-  __shared__ unsigned last;
+// The tokens' terms in their order per thread and the threads' sums in a
+// fixed tree, in float64 (one CTA).
+__device__ __forceinline__ void add_terms(const LossArgs& a) {
   __shared__ double sums[32];
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) == ctas - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
   double s = 0.0;
   for (int i = threadIdx.x; i < a.tokens; i += blockDim.x) s += static_cast<double>(__ldcg(a.terms + i));
   s = warp_sum(s);
@@ -124,8 +117,20 @@ __device__ __forceinline__ void finish_loss(const LossArgs& a, unsigned ctas) {
   if (threadIdx.x == 0) {
     for (int i = 1; i < static_cast<int>(blockDim.x >> 5); ++i) s += sums[i];
     a.loss[0] = static_cast<float>(s);
-    *a.ticket = 0;
   }
+}
+
+// The last of `ctas` CTAs to finish adds them.
+__device__ __forceinline__ void finish_loss(const LossArgs& a, unsigned ctas) {
+  __shared__ unsigned last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) == ctas - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  add_terms(a);
+  if (threadIdx.x == 0) *a.ticket = 0;
 }
 
 // `slabs` CTAs (one cluster) per token; a thread holds NV vectors of VE
@@ -134,15 +139,21 @@ __device__ __forceinline__ void finish_loss(const LossArgs& a, unsigned ctas) {
 // move in whole words; only the first and the last vector are ragged.
 // LONG: rows beyond the registers of a cluster; two passes, the second from
 // L2.
-template <typename TZ, typename TG, int VE, int NV, bool LONG, int TPB>
-__global__ void __launch_bounds__(TPB, 1024 / TPB) policy_kernel(const LossArgs a, int slabs) {
+// TPB threads have a row (32: eight rows to a CTA, no barrier); CLUSTER: as
+// many CTAs as `slabs` says do, else one.
+template <typename TZ, typename TG, int VE, int NV, bool LONG, int TPB, bool CLUSTER>
+__global__ void __launch_bounds__(TPB == 32 ? 256 : TPB, TPB == 32 ? 4 : 1024 / TPB)
+    policy_kernel(const LossArgs a, int slabs, int ticket) {
   constexpr int WPB = TPB / 32;
-  __shared__ float2 pairs[MAX_SLABS * WPB];
-  cluster_arrive();
+  __shared__ float2 pairs[(CLUSTER ? MAX_SLABS : 1) * WPB];
+  if (CLUSTER) cluster_arrive();
   grid_dep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = blockIdx.x % slabs;
-  const int64_t row = blockIdx.x / slabs;
+  const int lane = threadIdx.x & 31, warp = TPB == 32 ? 0 : threadIdx.x >> 5;
+  const int t = TPB == 32 ? lane : threadIdx.x;
+  if (!CLUSTER) slabs = 1;
+  const int rank = CLUSTER ? blockIdx.x % slabs : 0;
+  const int64_t row = TPB == 32 ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x / slabs;
+  if (TPB == 32 && row >= a.tokens) return;
   const TZ* z = static_cast<const TZ*>(a.z) + row * a.ld_z;
   TG* g = a.g ? static_cast<TG*>(a.g) + row * a.ld_g : nullptr;
   const int V = a.vocab;
@@ -153,12 +164,12 @@ __global__ void __launch_bounds__(TPB, 1024 / TPB) policy_kernel(const LossArgs 
   if (wt == 0.f) {                       // nothing of the row is read
     const float zero[VE] = {};
     if (g)
-      for (int i = rank * TPB + threadIdx.x; i < nvec; i += slabs * TPB) store_edge<TG, VE>(g, i * VE - h, V, zero);
-    if (rank == 0 && threadIdx.x == 0) {
+      for (int i = rank * TPB + t; i < nvec; i += slabs * TPB) store_edge<TG, VE>(g, i * VE - h, V, zero);
+    if (rank == 0 && t == 0) {
       a.logp[row] = 0.f;
       a.terms[row] = 0.f;
     }
-    cluster_wait();
+    if (CLUSTER) cluster_wait();
   } else {
     const int64_t target = a.targets64 ? static_cast<const int64_t*>(a.targets)[row]
                                        : static_cast<int64_t>(static_cast<const int*>(a.targets)[row]);
@@ -169,7 +180,7 @@ __global__ void __launch_bounds__(TPB, 1024 / TPB) policy_kernel(const LossArgs 
       t.load(z + target);
       za = t.get(0);
     }
-    const int first = LONG ? rank * TPB + threadIdx.x : rank * TPB * NV + threadIdx.x;
+    const int first = LONG ? rank * TPB + t : rank * TPB * NV + t;
     float e[NV][VE];
     float m = -INFINITY, s = 0.f;
     if constexpr (LONG) {
@@ -211,19 +222,27 @@ __global__ void __launch_bounds__(TPB, 1024 / TPB) policy_kernel(const LossArgs 
       }
       s = warp_sum(tree_sum(part));
     }
-    cluster_wait();                      // every CTA of the cluster has started
-    if (lane < slabs) st_cluster_f2(smem_u32(&pairs[rank * WPB + warp]), lane, m, s);
-    cluster_sync();
-    float top = -INFINITY;
-    for (int i = lane; i < slabs * WPB; i += 32) top = fmaxf(top, pairs[i].x);
-    top = warp_max(top);
-    float total = 0.f;
-    for (int i = lane; i < slabs * WPB; i += 32) total += pairs[i].y * exp_rel(pairs[i].x, top);
-    total = warp_sum(total);
+    float top = m, total = m == -INFINITY ? __int_as_float(0x7FFFFFFF) : s;
+    if constexpr (TPB > 32) {
+      if constexpr (CLUSTER) {
+        cluster_wait();                  // every CTA of the cluster has started
+        if (lane < slabs) st_cluster_f2(smem_u32(&pairs[rank * WPB + warp]), lane, m, s);
+        cluster_sync();
+      } else {
+        if (lane == 0) pairs[warp] = make_float2(m, s);
+        __syncthreads();
+      }
+      top = -INFINITY;
+      for (int i = lane; i < slabs * WPB; i += 32) top = fmaxf(top, pairs[i].x);
+      top = warp_max(top);
+      total = 0.f;
+      for (int i = lane; i < slabs * WPB; i += 32) total += pairs[i].y * exp_rel(pairs[i].x, top);
+      total = warp_sum(total);
+    }
     const float lp = (za - top) - logf(total);
     float l, slope;
     token_loss(a, row, lp, l, slope);
-    if (rank == 0 && threadIdx.x == 0) {
+    if (rank == 0 && t == 0) {
       a.logp[row] = lp;
       a.terms[row] = wt * l;
     }
@@ -255,7 +274,13 @@ __global__ void __launch_bounds__(TPB, 1024 / TPB) policy_kernel(const LossArgs 
       }
     }
   }
-  if (rank == 0) finish_loss(a, a.tokens);
+  if (ticket && rank == 0) finish_loss(a, a.tokens);
+}
+
+// The sum alone, where thousands of CTAs on one ticket would take longer.
+__global__ void __launch_bounds__(512) loss_sum_kernel(const LossArgs a) {
+  grid_dep_wait();
+  add_terms(a);
 }
 
 // ---------------------------------------------------------------- long rows of many tokens
@@ -276,6 +301,10 @@ __global__ void __launch_bounds__(TPB, 1024 / TPB) policy_kernel(const LossArgs 
 // 187 us: PLACEHOLDER).
 constexpr int RING_CHUNK = 16384, RING_SLOTS = 6, RING_AHEAD = 2;
 constexpr int RING_TPB = 512, RING_WARPS = RING_TPB / 32;
+#ifndef RING_MIN_KB
+#define RING_MIN_KB 40
+#endif
+constexpr int RING_MIN = RING_MIN_KB * 1024;
 constexpr int RING_LIST = 128;                               // a CTA's tokens of either kind in a window
 constexpr float kLowest = -3.402823466e38f;
 
@@ -582,12 +611,20 @@ bool valid_type(int t) { return t == MXQ_BF16 || t == MXQ_F32; }
 int type_size(int t) { return t == MXQ_F32 ? 4 : 2; }
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-template <typename TZ, typename TG, int VE, int NV, bool LONG, int TPB>
+// Up to this many CTAs share the ticket; more are followed by a kernel that
+// adds the terms (16384 tokens of 1000: PLACEHOLDER).
+constexpr int TICKET_MAX = 1024;
+
+template <typename TZ, typename TG, int VE, int NV, bool LONG, int TPB, bool CLUSTER>
 int launch_policy(const LossArgs& a, int slabs, cudaStream_t st) {
-  const int64_t grid = static_cast<int64_t>(a.tokens) * slabs;
+  const int64_t grid = TPB == 32 ? (static_cast<int64_t>(a.tokens) + 7) / 8 : static_cast<int64_t>(a.tokens) * slabs;
   if (grid > 0x7FFFFFFF) return MXQ_ERR_BAD_SHAPE;
-  return launch_pdl_cluster(policy_kernel<TZ, TG, VE, NV, LONG, TPB>, dim3(static_cast<unsigned>(grid)), dim3(TPB), 0, st,
-                            slabs, a, slabs);
+  const int ticket = TPB > 32 && a.tokens <= TICKET_MAX;
+  auto kern = policy_kernel<TZ, TG, VE, NV, LONG, TPB, CLUSTER>;
+  const dim3 g(static_cast<unsigned>(grid)), b(TPB == 32 ? 256 : TPB);
+  const int rc = CLUSTER ? launch_pdl_cluster(kern, g, b, 0, st, slabs, a, slabs, ticket) : launch_pdl(kern, g, b, 0, st, a, 1, ticket);
+  if (rc || ticket) return rc;
+  return launch_pdl(loss_sum_kernel, dim3(1), dim3(512), 0, st, a);
 }
 
 // Clusters of `slabs` CTAs that run at once (asked once per device and size).
@@ -624,12 +661,12 @@ int64_t row_words(const LossArgs& a) {
   return (static_cast<int64_t>(a.vocab) + (flush ? 0 : VE - 1) + VE - 1) / VE;
 }
 
-// The ring kernel takes rows of at least a chunk when every CTA gets two
+// The ring kernel takes rows of RING_MIN bytes and more when every CTA gets two
 // tokens or more, in the smallest cluster whose CTAs keep RING_AHEAD chunks
 // of the ring for the next token.  0: not for it.
 template <typename TZ>
 int ring_slabs(const LossArgs& a) {
-  if (static_cast<int64_t>(a.vocab) * sizeof(TZ) < RING_CHUNK) return 0;
+  if (static_cast<int64_t>(a.vocab) * sizeof(TZ) < RING_MIN) return 0;
   for (int slabs = 1; slabs <= MAX_SLABS; slabs *= 2)
     if ((row_words<TZ>(a) + slabs - 1) / slabs <= (RING_SLOTS - RING_AHEAD) * (RING_CHUNK / 16))
       return static_cast<int64_t>(a.tokens) * slabs >= 4 * sm_count() ? slabs : 0;
@@ -646,28 +683,35 @@ int launch_ring(const LossArgs& a, int slabs, cudaStream_t st) {
                             RING_CHUNK * RING_SLOTS, st, slabs, a, slabs, part, status);
 }
 
-// Rows of up to 4096 elements in a CTA of four warps; longer ones in the
-// fewest CTAs of sixteen whose registers hold them, and with few tokens in
-// more, until there are two CTAs for every SM or eight to a row.
+// With enough tokens to fill the GPU, a row goes to the fewest threads that
+// hold it, 32 elements each: a warp, or a CTA of 4, 8 or 16.  Longer rows, and
+// rows of few tokens, to clusters: the fewest CTAs of 16 warps that hold a row,
+// and more with few tokens, until there are two for every SM or eight to a row.
 template <typename TZ, typename TG, int VE>
 int dispatch_policy(const LossArgs& a, cudaStream_t st) {
   constexpr int NMAX = MAX_E / VE;
   // the words of a row, whatever its shift
   const bool flush = a.ld_z % VE == 0 && reinterpret_cast<uintptr_t>(a.z) / sizeof(TZ) % VE == 0;
   const int64_t nvec = (static_cast<int64_t>(a.vocab) + (flush ? 0 : VE - 1) + VE - 1) / VE;
-  if (nvec <= 128 * NMAX && (nvec <= 512 || a.tokens >= sm_count())) {
-    if (nvec <= 128 * NMAX / 4) return launch_policy<TZ, TG, VE, NMAX / 4, false, 128>(a, 1, st);
-    return launch_policy<TZ, TG, VE, NMAX, false, 128>(a, 1, st);
+  if (a.tokens >= sm_count() && nvec <= 512 * NMAX) {
+    if (nvec <= 32 * NMAX)
+      return nvec <= 32 * NMAX / 4 ? launch_policy<TZ, TG, VE, NMAX / 4, false, 32, false>(a, 1, st)
+                                   : launch_policy<TZ, TG, VE, NMAX, false, 32, false>(a, 1, st);
+    if (nvec <= 128 * NMAX)
+      return nvec <= 64 * NMAX ? launch_policy<TZ, TG, VE, NMAX / 2, false, 128, false>(a, 1, st)
+                               : launch_policy<TZ, TG, VE, NMAX, false, 128, false>(a, 1, st);
+    if (nvec <= 256 * NMAX) return launch_policy<TZ, TG, VE, NMAX, false, 256, false>(a, 1, st);
+    return launch_policy<TZ, TG, VE, NMAX, false, 512, false>(a, 1, st);
   }
   constexpr int TPB = 512;
   int slabs = static_cast<int>(std::min<int64_t>((nvec + TPB * NMAX - 1) / (TPB * NMAX), MAX_SLABS + 1));
-  if (slabs > MAX_SLABS) return launch_policy<TZ, TG, VE, 1, true, TPB>(a, MAX_SLABS, st);
+  if (slabs > MAX_SLABS) return launch_policy<TZ, TG, VE, 1, true, TPB, true>(a, MAX_SLABS, st);
   while (slabs < MAX_SLABS && static_cast<int64_t>(a.tokens) * slabs < 2 * sm_count() && nvec > TPB * slabs)
     slabs = std::min(MAX_SLABS, 2 * slabs);
   const int64_t nv = (nvec + static_cast<int64_t>(TPB) * slabs - 1) / (static_cast<int64_t>(TPB) * slabs);
-  if (nv <= NMAX / 4) return launch_policy<TZ, TG, VE, NMAX / 4, false, TPB>(a, slabs, st);
-  if (nv <= NMAX / 2) return launch_policy<TZ, TG, VE, NMAX / 2, false, TPB>(a, slabs, st);
-  return launch_policy<TZ, TG, VE, NMAX, false, TPB>(a, slabs, st);
+  if (nv <= NMAX / 4) return launch_policy<TZ, TG, VE, NMAX / 4, false, TPB, true>(a, slabs, st);
+  if (nv <= NMAX / 2) return launch_policy<TZ, TG, VE, NMAX / 2, false, TPB, true>(a, slabs, st);
+  return launch_policy<TZ, TG, VE, NMAX, false, TPB, true>(a, slabs, st);
 }
 
 template <typename TZ, typename TG>
