@@ -300,11 +300,8 @@ __global__ void __launch_bounds__(512) loss_sum_kernel(const LossArgs a) {
 // (dealt by index instead, 2048 x 131072 bf16 with a quarter of weight 0 took
 // 187 us: PLACEHOLDER).
 constexpr int RING_CHUNK = 16384, RING_SLOTS = 6, RING_AHEAD = 2;
-constexpr int RING_TPB = 512, RING_WARPS = RING_TPB / 32;
-#ifndef RING_MIN_KB
-#define RING_MIN_KB 40
-#endif
-constexpr int RING_MIN = RING_MIN_KB * 1024;
+constexpr int RING_TPB = 256, RING_WARPS = RING_TPB / 32;
+constexpr int RING_MIN = 32 * 1024;
 constexpr int RING_LIST = 128;                               // a CTA's tokens of either kind in a window
 constexpr float kLowest = -3.402823466e38f;
 
@@ -499,13 +496,9 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
 #pragma unroll
           for (int j = 0; j < VE; ++j) v[j] = r.get(j);
         };
-        // word `at` of the chunk that starts at word w; false: not in the row
-        const auto fetch = [&](const uint8_t* chunk, int w, int at, float (&v)[VE]) {
-          if (w + at >= end) return false;
-          if (w + at >= whole_lo && w + at < whole_hi) whole(chunk, at, v);
-          else load_edge<TZ, VE>(z, (w + at) * VE - h, V, v);
-          return true;
-        };
+        // the ragged words, where this part has them: the first is thread 0's,
+        // the last thread 32's, straight from memory
+        const int edge = t == 0 && lo && w0 == 0 ? 0 : t == 32 && hi >= w0 && hi < end ? hi : -1;
 
         // first pass: running maximum and sum; the lowest float32 stands for
         // "none yet", so no difference is inf - inf
@@ -522,12 +515,22 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
               take_in(v, m, s);
             }
           } else {
+#pragma unroll
             for (int u = 0; u < U; ++u) {
               float v[VE];
-              if (fetch(chunk, w, t + u * RING_TPB, v)) take_in(v, m, s);
+              const int word = w + t + u * RING_TPB;
+              if (word >= whole_lo && word < whole_hi) {
+                whole(chunk, t + u * RING_TPB, v);
+                take_in(v, m, s);
+              }
             }
           }
           if (++slot == RING_SLOTS) slot = 0, phase ^= 1;
+        }
+        if (edge >= 0) {
+          float v[VE];
+          load_edge<TZ, VE>(z, edge * VE - h, V, v);
+          take_in(v, m, s);
         }
         const float wm = warp_max(m);
         s = warp_sum(s * ex2((m - wm) * kLog2e));
@@ -569,18 +572,27 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
               store_vec<TG, VE>(g + e0, v);
             }
           } else if (g) {
+#pragma unroll
             for (int u = 0; u < U; ++u) {
               float v[VE];
-              const int e0 = (w + t + u * RING_TPB) * VE - h;
-              if (fetch(chunk, w, t + u * RING_TPB, v)) {
+              const int word = w + t + u * RING_TPB, e0 = word * VE - h;
+              if (word >= whole_lo && word < whole_hi) {
+                whole(chunk, t + u * RING_TPB, v);
                 to_gradient(v, tt, f, at - e0, k);
-                store_edge<TG, VE>(g, e0, V, v);
+                store_vec<TG, VE>(g + e0, v);
               }
             }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&empty[sl]));
           if (++sl == RING_SLOTS) sl = 0;
+        }
+        if (g && edge >= 0) {
+          float v[VE];
+          const int e0 = edge * VE - h;
+          load_edge<TZ, VE>(z, e0, V, v);
+          to_gradient(v, tt, f, at - e0, k);
+          store_edge<TG, VE>(g, e0, V, v);
         }
       }
       for (int q = 0; q < mine[1]; ++q) {                      // weight 0: nothing of the row is read
@@ -639,7 +651,7 @@ int ring_clusters(int slabs) {
   const int smem = RING_CHUNK * RING_SLOTS;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(slabs * 2 * sm_count());
+  cfg.gridDim = dim3(slabs * 4 * sm_count());
   cfg.blockDim = dim3(RING_TPB + 32);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
