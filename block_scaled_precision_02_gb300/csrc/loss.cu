@@ -292,17 +292,12 @@ __global__ void __launch_bounds__(512) loss_sum_kernel(const LossArgs a) {
 // The ring holds a whole part and a share of the next token's, so loads run
 // ahead through the exchange and the stores, and two CTAs share an SM, so one
 // computes while the other waits.  Two exponentials per element instead of
-// one, but no data held in registers.
-//
-// Tokens of weight 0 cost half a token's traffic, so who takes which matters:
-// live tokens are dealt out by their rank among the live ones, the others by
-// theirs.  Every CTA ranks a window of tokens at a time from their weights
-// (dealt by index instead, 2048 x 131072 bf16 with a quarter of weight 0 took
-// 187 us: PLACEHOLDER).
+// one, but no data held in registers.  Eight warps to a CTA: with sixteen the
+// waits and branches of each chunk weigh twice as much (2048 x 131072 bf16, no
+// token masked: 229 us against 189, 84 % of the measured copy rate).
 constexpr int RING_CHUNK = 16384, RING_SLOTS = 6, RING_AHEAD = 2;
 constexpr int RING_TPB = 256, RING_WARPS = RING_TPB / 32;
 constexpr int RING_MIN = 32 * 1024;
-constexpr int RING_LIST = 128;                               // a CTA's tokens of either kind in a window
 constexpr float kLowest = -3.402823466e38f;
 
 // exp(v - m) of a pair, m and log2(e) splat.
@@ -371,7 +366,6 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float2 pairs[2][MAX_SLABS * RING_WARPS];
   __shared__ __align__(8) uint64_t full[RING_SLOTS], empty[RING_SLOTS], xbar[2];
-  __shared__ int list[2][RING_LIST + 1], counts[RING_WARPS];
   if (threadIdx.x == 0) {
     for (int i = 0; i < RING_SLOTS; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
@@ -397,222 +391,174 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
   };
 
   int slot = 0, phase = 0;                                   // the next chunk's slot and its parity
-  int n = 0, live = 0;                                       // chunks issued; tokens taken
-  int before[2] = {0, 0};                                    // tokens of either kind in earlier windows
-  const int t = threadIdx.x;
-  const int per = static_cast<int>((step * RING_LIST + RING_TPB - 1) / RING_TPB);   // consecutive tokens of a thread
-  for (int64_t base = 0; base < a.tokens; base += step * RING_LIST) {
-    // deal out the window: live tokens (0) and the others (1), each by rank
-    const int64_t stop = min(base + step * RING_LIST, static_cast<int64_t>(a.tokens));
-    __syncthreads();
-    int ones = 0, upto = 0;
-    if (warp < RING_WARPS) {
-      for (int64_t i = base + static_cast<int64_t>(t) * per; i < min(base + static_cast<int64_t>(t + 1) * per, stop); ++i)
-        ones += a.weights[i] != 0.f;
-      upto = ones;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      if (lane == 31) counts[warp] = upto;
-    }
-    __syncthreads();
-    int total = 0, ahead = 0;
-    for (int i = 0; i < RING_WARPS; ++i) {
-      if (i < warp) ahead += counts[i];
-      total += counts[i];
-    }
-    const int teams = static_cast<int>(step), team = static_cast<int>(row0);
-    const int size[2] = {total, static_cast<int>(stop - base) - total};
-    int mine[2], skip[2];                                    // this CTA's tokens here, and in earlier windows
-#pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      skip[kind] = (before[kind] + teams - 1 - team) / teams;
-      mine[kind] = (before[kind] + size[kind] + teams - 1 - team) / teams - skip[kind];
-    }
-    if (warp < RING_WARPS) {
-      const int64_t i0 = base + static_cast<int64_t>(t) * per;
-      int rank_of[2];
-      rank_of[0] = before[0] + ahead + upto - ones;
-      rank_of[1] = before[1] + static_cast<int>(min(i0, stop) - base) - (ahead + upto - ones);
-      for (int64_t i = i0; i < min(i0 + per, stop); ++i) {
-        const int kind = a.weights[i] == 0.f;
-        const int r = kind ? rank_of[1]++ : rank_of[0]++;
-        if (r % teams == team) list[kind][r / teams - skip[kind]] = static_cast<int>(i);
-      }
-    }
-    before[0] += size[0];
-    before[1] += size[1];
-    __syncthreads();
-
-    if (warp == RING_WARPS) {
-      if (lane == 0) {
-        for (int q = 0; q < mine[0] && alive; ++q) {
-          const int64_t row = list[0][q];
-          const int h = shift(row);
-          const uint8_t* base = static_cast<const uint8_t*>(a.z) + (row * a.ld_z - h) * static_cast<int64_t>(sizeof(TZ));
-          const int lo = h ? 1 : 0, hi = (V + h) / VE, end = min(w0 + part, (V + h + VE - 1) / VE);
-          for (int w = w0; w < end; w += CV) {
-            if (n >= RING_SLOTS) {
-              alive = mbar_wait_sleep(smem_u32(&empty[slot]), phase ^ 1, status);
-              if (!alive) break;
-            }
-            const int b = max(w, lo), e = min(min(w + CV, end), hi);
-            const uint32_t bytes = e > b ? static_cast<uint32_t>(e - b) * 16u : 0u;
-            mbar_arrive_expect_tx(smem_u32(&full[slot]), bytes);
-            if (bytes)
-              bulk_load_1d(smem_u32(ring + slot * RING_CHUNK + (b - w) * 16), base + static_cast<int64_t>(b) * 16, bytes,
-                           smem_u32(&full[slot]));
-            ++n;
-            if (++slot == RING_SLOTS) slot = 0, phase ^= 1;
-          }
-        }
-      }
-      __syncwarp();
-    } else {
-      TokenIn next = token_in(a, mine[0] ? list[0][0] : a.tokens);
-      for (int q = 0; q < mine[0]; ++q) {
-        const int64_t row = list[0][q];
-        const TokenIn tok = next;
-        next = token_in(a, q + 1 < mine[0] ? list[0][q + 1] : a.tokens);
-        const TZ* z = static_cast<const TZ*>(a.z) + row * a.ld_z;
-        TG* g = a.g ? static_cast<TG*>(a.g) + row * a.ld_g : nullptr;
+  if (warp == RING_WARPS) {
+    if (lane == 0) {
+      int n = 0;                                           // chunks issued
+      float next = row0 < a.tokens ? a.weights[row0] : 0.f;
+      for (int64_t row = row0; row < a.tokens && alive; row += step) {
+        const float wt = next;
+        if (row + step < a.tokens) next = a.weights[row + step];
+        if (wt == 0.f) continue;
         const int h = shift(row);
+        const uint8_t* base = static_cast<const uint8_t*>(a.z) + (row * a.ld_z - h) * static_cast<int64_t>(sizeof(TZ));
         const int lo = h ? 1 : 0, hi = (V + h) / VE, end = min(w0 + part, (V + h + VE - 1) / VE);
-        const bool inside = tok.target >= 0 && tok.target < V;
-        float za = __int_as_float(0x7FFFFFFF);
-        if (inside) {
-          Vec<TZ, 1> one;
-          one.load(z + tok.target);
-          za = one.get(0);
-        }
-        const int whole_lo = max(w0, lo), whole_hi = min(end, hi);   // this part's whole words
-
-        const auto whole = [&](const uint8_t* chunk, int at, float (&v)[VE]) {
-          const uint4 q = *reinterpret_cast<const uint4*>(chunk + at * 16);
-          Vec<TZ, VE> r;
-          r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
-#pragma unroll
-          for (int j = 0; j < VE; ++j) v[j] = r.get(j);
-        };
-        // the ragged words, where this part has them: the first is thread 0's,
-        // the last thread 32's, straight from memory
-        const int edge = t == 0 && lo && w0 == 0 ? 0 : t == 32 && hi >= w0 && hi < end ? hi : -1;
-
-        // first pass: running maximum and sum; the lowest float32 stands for
-        // "none yet", so no difference is inf - inf
-        float m = kLowest, s = 0.f;
-        const int slot0 = slot;
         for (int w = w0; w < end; w += CV) {
-          if (alive) alive = mbar_wait_sleep(smem_u32(&full[slot]), phase, status);
-          const uint8_t* chunk = ring + slot * RING_CHUNK;
-          if (w >= whole_lo && w + CV <= whole_hi) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              float v[VE];
-              whole(chunk, t + u * RING_TPB, v);
-              take_in(v, m, s);
-            }
-          } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              float v[VE];
-              const int word = w + t + u * RING_TPB;
-              if (word >= whole_lo && word < whole_hi) {
-                whole(chunk, t + u * RING_TPB, v);
-                take_in(v, m, s);
-              }
-            }
+          if (n >= RING_SLOTS) {
+            alive = mbar_wait_sleep(smem_u32(&empty[slot]), phase ^ 1, status);
+            if (!alive) break;
           }
+          const int b = max(w, lo), e = min(min(w + CV, end), hi);
+          const uint32_t bytes = e > b ? static_cast<uint32_t>(e - b) * 16u : 0u;
+          mbar_arrive_expect_tx(smem_u32(&full[slot]), bytes);
+          if (bytes)
+            bulk_load_1d(smem_u32(ring + slot * RING_CHUNK + (b - w) * 16), base + static_cast<int64_t>(b) * 16, bytes,
+                         smem_u32(&full[slot]));
+          ++n;
           if (++slot == RING_SLOTS) slot = 0, phase ^= 1;
         }
-        if (edge >= 0) {
-          float v[VE];
-          load_edge<TZ, VE>(z, edge * VE - h, V, v);
-          take_in(v, m, s);
-        }
-        const float wm = warp_max(m);
-        s = warp_sum(s * ex2((m - wm) * kLog2e));
-        const int par = live & 1;
-        if (t == 0) mbar_arrive_expect_tx(smem_u32(&xbar[par]), slabs * RING_WARPS * 8);
-        if (lane < slabs)
-          st_async_f2(smem_u32(&pairs[par][rank * RING_WARPS + warp]), smem_u32(&xbar[par]), lane, wm, s);
-        if (alive) alive = mbar_wait_sleep(smem_u32(&xbar[par]), (live >> 1) & 1, status);
-        ++live;
-        float top = kLowest;
-        for (int i = lane; i < slabs * RING_WARPS; i += 32) top = fmaxf(top, pairs[par][i].x);
-        top = warp_max(top);
-        float total = 0.f;
-        for (int i = lane; i < slabs * RING_WARPS; i += 32) total += pairs[par][i].y * ex2((pairs[par][i].x - top) * kLog2e);
-        total = warp_sum(total);
-        const float lp = (za - top) - logf(total);
-        float l, slope;
-        token_loss(a, row, lp, l, slope);
-        if (rank == 0 && t == 0) {
-          a.logp[row] = lp;
-          a.terms[row] = tok.w * l;
-        }
-
-        // second pass: the gradient, and the chunks are free
-        const float k = a.scale * tok.w * slope;
-        const int at = inside ? static_cast<int>(tok.target) : -VE;
-        const float2 tt = splat(top);
-        const float f = -k / total;
-        int sl = slot0;
-        for (int w = w0; w < end; w += CV) {
-          const uint8_t* chunk = ring + sl * RING_CHUNK;
-          if (g && w >= whole_lo && w + CV <= whole_hi) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              float v[VE];
-              const int e0 = (w + t + u * RING_TPB) * VE - h;
-              whole(chunk, t + u * RING_TPB, v);
-              to_gradient(v, tt, f, at - e0, k);
-              store_vec<TG, VE>(g + e0, v);
-            }
-          } else if (g) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              float v[VE];
-              const int word = w + t + u * RING_TPB, e0 = word * VE - h;
-              if (word >= whole_lo && word < whole_hi) {
-                whole(chunk, t + u * RING_TPB, v);
-                to_gradient(v, tt, f, at - e0, k);
-                store_vec<TG, VE>(g + e0, v);
-              }
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&empty[sl]));
-          if (++sl == RING_SLOTS) sl = 0;
-        }
-        if (g && edge >= 0) {
-          float v[VE];
-          const int e0 = edge * VE - h;
-          load_edge<TZ, VE>(z, e0, V, v);
-          to_gradient(v, tt, f, at - e0, k);
-          store_edge<TG, VE>(g, e0, V, v);
-        }
       }
-      for (int q = 0; q < mine[1]; ++q) {                      // weight 0: nothing of the row is read
-        const int64_t row = list[1][q];
-        const int h = shift(row), end = min(w0 + part, (V + h + VE - 1) / VE);
+      // no exit with copies in flight
+      for (int i = max(0, n - RING_SLOTS); i < n; ++i)
+        mbar_wait(smem_u32(&full[i % RING_SLOTS]), (i / RING_SLOTS) & 1, status);
+    }
+    __syncwarp();
+  } else {
+    const int t = threadIdx.x;
+    int live = 0;                                          // tokens taken
+    TokenIn next = token_in(a, row0);
+    for (int64_t row = row0; row < a.tokens; row += step) {
+      const TokenIn tok = next;
+      next = token_in(a, row + step);
+      const TZ* z = static_cast<const TZ*>(a.z) + row * a.ld_z;
+      TG* g = a.g ? static_cast<TG*>(a.g) + row * a.ld_g : nullptr;
+      const int h = shift(row);
+      const int lo = h ? 1 : 0, hi = (V + h) / VE, end = min(w0 + part, (V + h + VE - 1) / VE);
+      if (tok.w == 0.f) {                                  // nothing of the row is read
         const float zero[VE] = {};
-        if (a.g)
-          for (int w = w0 + t; w < end; w += RING_TPB)
-            store_edge<TG, VE>(static_cast<TG*>(a.g) + row * a.ld_g, w * VE - h, V, zero);
+        if (g)
+          for (int w = w0 + t; w < end; w += RING_TPB) store_edge<TG, VE>(g, w * VE - h, V, zero);
         if (rank == 0 && t == 0) {
           a.logp[row] = 0.f;
           a.terms[row] = 0.f;
         }
+        continue;
+      }
+      const bool inside = tok.target >= 0 && tok.target < V;
+      float za = __int_as_float(0x7FFFFFFF);
+      if (inside) {
+        Vec<TZ, 1> one;
+        one.load(z + tok.target);
+        za = one.get(0);
+      }
+      const int whole_lo = max(w0, lo), whole_hi = min(end, hi);   // this part's whole words
+
+      const auto whole = [&](const uint8_t* chunk, int at, float (&v)[VE]) {
+        const uint4 q = *reinterpret_cast<const uint4*>(chunk + at * 16);
+        Vec<TZ, VE> r;
+        r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[j] = r.get(j);
+      };
+      // the ragged words, where this part has them: the first is thread 0's,
+      // the last thread 32's, straight from memory
+      const int edge = t == 0 && lo && w0 == 0 ? 0 : t == 32 && hi >= w0 && hi < end ? hi : -1;
+
+      // first pass: running maximum and sum; the lowest float32 stands for
+      // "none yet", so no difference is inf - inf
+      float m = kLowest, s = 0.f;
+      const int slot0 = slot;
+      for (int w = w0; w < end; w += CV) {
+        if (alive) alive = mbar_wait_sleep(smem_u32(&full[slot]), phase, status);
+        const uint8_t* chunk = ring + slot * RING_CHUNK;
+        if (w >= whole_lo && w + CV <= whole_hi) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float v[VE];
+            whole(chunk, t + u * RING_TPB, v);
+            take_in(v, m, s);
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float v[VE];
+            const int word = w + t + u * RING_TPB;
+            if (word >= whole_lo && word < whole_hi) {
+              whole(chunk, t + u * RING_TPB, v);
+              take_in(v, m, s);
+            }
+          }
+        }
+        if (++slot == RING_SLOTS) slot = 0, phase ^= 1;
+      }
+      if (edge >= 0) {
+        float v[VE];
+        load_edge<TZ, VE>(z, edge * VE - h, V, v);
+        take_in(v, m, s);
+      }
+      const float wm = warp_max(m);
+      s = warp_sum(s * ex2((m - wm) * kLog2e));
+      const int par = live & 1;
+      if (t == 0) mbar_arrive_expect_tx(smem_u32(&xbar[par]), slabs * RING_WARPS * 8);
+      if (lane < slabs)
+        st_async_f2(smem_u32(&pairs[par][rank * RING_WARPS + warp]), smem_u32(&xbar[par]), lane, wm, s);
+      if (alive) alive = mbar_wait_sleep(smem_u32(&xbar[par]), (live >> 1) & 1, status);
+      ++live;
+      float top = kLowest;
+      for (int i = lane; i < slabs * RING_WARPS; i += 32) top = fmaxf(top, pairs[par][i].x);
+      top = warp_max(top);
+      float total = 0.f;
+      for (int i = lane; i < slabs * RING_WARPS; i += 32) total += pairs[par][i].y * ex2((pairs[par][i].x - top) * kLog2e);
+      total = warp_sum(total);
+      const float lp = (za - top) - logf(total);
+      float l, slope;
+      token_loss(a, row, lp, l, slope);
+      if (rank == 0 && t == 0) {
+        a.logp[row] = lp;
+        a.terms[row] = tok.w * l;
+      }
+
+      // second pass: the gradient, and the chunks are free
+      const float k = a.scale * tok.w * slope;
+      const int at = inside ? static_cast<int>(tok.target) : -VE;
+      const float2 tt = splat(top);
+      const float f = -k / total;
+      int sl = slot0;
+      for (int w = w0; w < end; w += CV) {
+        const uint8_t* chunk = ring + sl * RING_CHUNK;
+        if (g && w >= whole_lo && w + CV <= whole_hi) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float v[VE];
+            const int e0 = (w + t + u * RING_TPB) * VE - h;
+            whole(chunk, t + u * RING_TPB, v);
+            to_gradient(v, tt, f, at - e0, k);
+            store_vec<TG, VE>(g + e0, v);
+          }
+        } else if (g) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float v[VE];
+            const int word = w + t + u * RING_TPB, e0 = word * VE - h;
+            if (word >= whole_lo && word < whole_hi) {
+              whole(chunk, t + u * RING_TPB, v);
+              to_gradient(v, tt, f, at - e0, k);
+              store_vec<TG, VE>(g + e0, v);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&empty[sl]));
+        if (++sl == RING_SLOTS) sl = 0;
+      }
+      if (g && edge >= 0) {
+        float v[VE];
+        const int e0 = edge * VE - h;
+        load_edge<TZ, VE>(z, e0, V, v);
+        to_gradient(v, tt, f, at - e0, k);
+        store_edge<TG, VE>(g, e0, V, v);
       }
     }
   }
-  if (warp == RING_WARPS && lane == 0)                       // no exit with copies in flight
-    for (int i = max(0, n - RING_SLOTS); i < n; ++i)
-      mbar_wait(smem_u32(&full[i % RING_SLOTS]), (i / RING_SLOTS) & 1, status);
-  __syncwarp();
   cluster_sync();                                            // no peer writes here any more
   if (rank == 0) finish_loss(a, static_cast<unsigned>(step));
 }
@@ -624,7 +570,7 @@ int type_size(int t) { return t == MXQ_F32 ? 4 : 2; }
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // Up to this many CTAs share the ticket; more are followed by a kernel that
-// adds the terms (16384 tokens of 1000: PLACEHOLDER).
+// adds the terms (16384 tokens of 1000, bf16, on one ticket: 111 us, 37 without).
 constexpr int TICKET_MAX = 1024;
 
 template <typename TZ, typename TG, int VE, int NV, bool LONG, int TPB, bool CLUSTER>
