@@ -196,3 +196,31 @@ def test_c_clip_statuses(so):
     assert so.mxq_clip_grad_norm(None, 1, 1.0, P, P, 1 << 30, None) == -1
     assert so.mxq_grad_norm((Grad * 1)(Grad(P, None, 4, 0, 0)), 1, P, P, 1 << 30, None) == -4
     assert so.mxq_grad_norm_workspace_size(4, None) == -1
+
+
+def test_calls_enter_the_device_guard_only_for_another_device(monkeypatch):
+    """_launch runs the call with the tensors' device current and that device's stream."""
+    events = []
+
+    class FakeDevice:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            events.append(("enter", str(self.d)))
+
+        def __exit__(self, *a):
+            events.append(("exit", str(self.d)))
+
+    class FakeLib:
+        def mxq_grad_norm(self, *args):
+            events.append(("call", args[-1]))
+            return 0
+
+    monkeypatch.setattr(mxq, "_lib", FakeLib())
+    monkeypatch.setattr(mxq.torch.cuda, "device", FakeDevice)
+    monkeypatch.setattr(mxq.torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(mxq.torch._C, "_cuda_getCurrentRawStream", lambda i: f"stream {i}", raising=False)
+    mxq._launch("mxq_grad_norm", torch.device("cuda", 0), 1, 2)
+    mxq._launch("mxq_grad_norm", torch.device("cuda", 1), 1, 2)
+    assert events == [("call", "stream 0"), ("enter", "cuda:1"), ("call", "stream 1"), ("exit", "cuda:1")]
