@@ -137,6 +137,11 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
       st_async_f2(smem_u32(&parts[buf][rank][warp * RW + lr]), smem_u32(&bar[buf]), lk, sum, m2);
   };
 
+  // scale addresses: a part of the thread's own, and one of the tile
+  const int kbr = a.cols / 32, kbc = a.rows / 32;        // scales of a row of the row and the column copy
+  const int k0 = (c0 + lane * 16) / 32;
+  const int64_t row_step = a.mma ? 16 : kbr;
+  uint8_t* const my_rows = a.s_row + (a.mma ? (k0 >> 2) * 512 + (k0 & 3) : k0) + warp * RW * row_step;
   uint32_t col_scales[S / T];                            // this thread's columns, a byte per tile
   if (first < last) load(first);
   for (int c = threadIdx.x * 4; c < nc; c += T * 4) {
@@ -199,18 +204,19 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
         }
       }
       if constexpr (ORIENT & MXQ_ROW) {
-        const int kb = a.cols / 32, k = (c0 + at) / 32;
+        const int64_t el = (row0 + warp * RW) * a.cols + c0 + at;
+        uint8_t* const codes = a.q_row + (FMT == MXQ_E2M1 ? el / 2 : el);
+        uint8_t* const scales = my_rows + v * (a.mma ? 4 * 512 : 16) +
+                                (a.mma ? static_cast<int64_t>(tile >> 2) * (kbr >> 2) * 512 + (tile & 3) * 4 : row0 * kbr);
 #pragma unroll
         for (int r = 0; r < RW; ++r) {
-          const int64_t row = row0 + warp * RW + r;
           const float top = fmax3_nan(m[r], __shfl_xor_sync(0xFFFFFFFFu, m[r], 1), 0.f);
           float mult;
           const uint32_t code = mx_scale<FMT>(__float_as_uint(top) & 0x7FFFFFFFu, a.ceil_mode, mult);
           if (valid) {
             uint32_t q[code_words<FMT, 16>()];
             mx_codes<FMT, 16>(y[r], mult, code == 0xFFu, q);
-            const int64_t el = row * a.cols + c0 + at;
-            uint8_t* dst = a.q_row + (FMT == MXQ_E2M1 ? el / 2 : el);
+            uint8_t* dst = codes + (FMT == MXQ_E2M1 ? static_cast<int64_t>(r) * a.cols / 2 : static_cast<int64_t>(r) * a.cols);
             if constexpr (FMT == MXQ_E2M1) *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
             else *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
           }
@@ -218,9 +224,9 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
             uint32_t word = code << (8 * ((lane >> 1) & 3));
             word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
             word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-            if (valid && lane % 8 == 0) *reinterpret_cast<uint32_t*>(a.s_row + scale_at(row, k, kb, a.mma)) = word;
+            if (valid && lane % 8 == 0) *reinterpret_cast<uint32_t*>(scales + r * row_step) = word;
           } else if (valid && lane % 2 == 0) {
-            a.s_row[scale_at(row, k, kb, a.mma)] = static_cast<uint8_t>(code);
+            scales[r * row_step] = static_cast<uint8_t>(code);
           }
         }
       }
@@ -229,7 +235,6 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
 
     if constexpr (ORIENT & MXQ_COL) {
       __syncthreads();
-      const int kb = a.rows / 32;
       // the word of scales is complete when its four tiles are all this CTA's
       const bool flush = (tile & 3) == 3 || tile + 1 == last;
       const bool word = a.pack_col && (tile & 3) == 3 && tile - 3 >= first;
@@ -260,11 +265,11 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
         }
         uint32_t& acc = col_scales[u];
         acc = ((tile & 3) == 0 || tile == first ? 0u : acc) | code << (8 * (tile & 3));
-        if (word) {
-          *reinterpret_cast<uint32_t*>(a.s_col + scale_at(c0 + c, tile - 3, kb, a.mma)) = acc;
-        } else if (flush) {
-          for (int k = max(first, tile & ~3); k <= tile; ++k)
-            a.s_col[scale_at(c0 + c, k, kb, a.mma)] = static_cast<uint8_t>(acc >> (8 * (k & 3)));
+        if (flush) {
+          uint8_t* const scales = a.s_col + scale_at(c0 + c, tile & ~3, kbc, a.mma);     // four tiles, side by side
+          if (word) *reinterpret_cast<uint32_t*>(scales) = acc;
+          else
+            for (int k = max(first, tile & ~3); k <= tile; ++k) scales[k & 3] = static_cast<uint8_t>(acc >> (8 * (k & 3)));
         }
       }
       __syncthreads();
