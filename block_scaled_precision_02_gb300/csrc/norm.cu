@@ -49,7 +49,10 @@ __device__ __forceinline__ void staged(const float* ws, int at, int cols, float 
   }
 }
 
-template <typename TX, typename TY, int VE, int NV, bool FULL>
+// W16: bf16 weight and bias stay bf16 in shared memory, which halves their
+// reads: those weigh as much as the row's own traffic (4096 x 14336 bf16:
+// PLACEHOLDER).
+template <typename TX, typename TY, int VE, int NV, bool FULL, bool W16>
 __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArgs a, int G, int stages, int* status) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float2 part[2][FWD_THREADS / 32];
@@ -67,7 +70,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArg
   const RowSource<TX> src{static_cast<const TX*>(a.x), a.ld, a.cols, a.rows};
   const int nvec = a.cols / VE;
   const int sb = slot_bytes(a.cols * static_cast<int>(sizeof(TX)), VE > 1);
-  uint8_t* slots = ring + slot_bytes(8 * a.cols, true) + static_cast<size_t>(g) * stages * sb;
+  uint8_t* slots = ring + slot_bytes((W16 ? 4 : 8) * a.cols, true) + static_cast<size_t>(g) * stages * sb;
   const int64_t gi = static_cast<int64_t>(blockIdx.x) * P + g, step = static_cast<int64_t>(gridDim.x) * P;
   const float inv_c = 1.f / static_cast<float>(a.cols);
   const int n_mine = warp_count<VE, NV>(a.cols, gw), n_lane = lane < wpg ? warp_count<VE, NV>(a.cols, lane) : 0;
@@ -83,7 +86,15 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArg
   if (t == 0)
     for (int i = 0; i < stages; ++i)
       if (gi + i * step < a.rows) issue(i, gi + i * step);
-  stage_affine<VE>(a, ws);
+  uint32_t* const w16 = reinterpret_cast<uint32_t*>(ring);     // W16: weight [cols], bias [cols]
+  if constexpr (W16) {
+    for (int i = threadIdx.x; i < a.cols / 2; i += blockDim.x) {
+      w16[i] = a.w ? static_cast<const uint32_t*>(a.w)[i] : 0x3F803F80u;      // ones
+      w16[a.cols / 2 + i] = a.b ? static_cast<const uint32_t*>(a.b)[i] : 0u;
+    }
+  } else {
+    stage_affine<VE>(a, ws);
+  }
   __syncthreads();
 
   int slot = 0, phase = 0, buf = 0;
@@ -152,8 +163,16 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_ring_kernel(const NormArg
         o[0] = norm_value(f[0], mean, rstd, wb.x, wb.y);
       } else {
         float w[VE], b[VE];
-        staged<VE>(ws, at, a.cols, w);
-        staged<VE>(ws + a.cols, at, a.cols, b);
+        if constexpr (W16) {
+          Vec<__nv_bfloat16, VE> wv, bv;
+          wv.load(reinterpret_cast<const __nv_bfloat16*>(w16) + at);
+          bv.load(reinterpret_cast<const __nv_bfloat16*>(w16) + a.cols + at);
+#pragma unroll
+          for (int j = 0; j < VE; ++j) w[j] = wv.get(j), b[j] = bv.get(j);
+        } else {
+          staged<VE>(ws, at, a.cols, w);
+          staged<VE>(ws + a.cols, at, a.cols, b);
+        }
 #pragma unroll
         for (int j = 0; j < VE; j += 2)
           halves(fma2(mul2(sub2(pair(f[j], f[j + 1]), mm), rr), pair(w[j], w[j + 1]),
@@ -215,13 +234,17 @@ bool try_norm_ring(const NormArgs& a, int* rc, cudaStream_t st) {
   if (!a.y || a.cols * sizeof(TX) < 512 || nvec > FWD_THREADS * NV) return false;
   if (VE > 1 && (a.cols * sizeof(TX) % 16 || a.ld * sizeof(TX) % 16)) return false;
   const int G = round_up((nvec + NV - 1) / NV, 32), P = ring_groups(FWD_THREADS, G);
-  const int slot = slot_bytes(a.cols * static_cast<int>(sizeof(TX)), VE > 1), fixed = slot_bytes(8 * a.cols, true);
+  const bool w16 = VE == 8 && !(a.w && a.w_f32) && !(a.b && a.b_f32);
+  const int slot = slot_bytes(a.cols * static_cast<int>(sizeof(TX)), VE > 1);
+  const int fixed = slot_bytes((w16 ? 4 : 8) * a.cols, true);
   const int stages = std::min(MAX_STAGES, (kRingBytes - fixed) / (P * slot));
   if (fixed > kRingBytes || stages < 2 || a.rows < 4ll * P * sm_count()) return false;
   int* status = status_ptr();
-  auto kern = norm_ring_kernel<TX, TY, VE, NV, false>;
+  auto kern = norm_ring_kernel<TX, TY, VE, NV, false, false>;
   if constexpr (VE > 1)
-    if (nvec == G * NV) kern = norm_ring_kernel<TX, TY, VE, NV, true>;
+    if (nvec == G * NV) kern = norm_ring_kernel<TX, TY, VE, NV, true, false>;
+  if constexpr (VE == 8)
+    if (w16) kern = nvec == G * NV ? norm_ring_kernel<TX, TY, VE, NV, true, true> : norm_ring_kernel<TX, TY, VE, NV, false, true>;
   if (!status || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
     *rc = MXQ_ERR_CUDA;
   else

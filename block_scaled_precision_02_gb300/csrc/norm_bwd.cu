@@ -452,24 +452,25 @@ __global__ void __launch_bounds__(256) norm_bwd_long_cols_kernel(const BwdArgs a
   }
 }
 
-// dw[c], db[c] = sums over the parts, in their order: 32 columns per CTA,
-// eight threads per column.
-__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* part, int parts, int cols, float* dw, float* db) {
-  __shared__ float red[8][33];
+// dw[c], db[c] = sums over the parts, in a fixed order: 32 columns per CTA and
+// 32 threads per column, so that all of a thread's few loads are in flight at
+// once (the kernel is bound by their latency).
+__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, int parts, int cols, float* dw, float* db) {
+  __shared__ float red[32][33];
   grid_dep_wait();
   const int cx = threadIdx.x & 31, sy = threadIdx.x >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + cx;      // over both sums
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 32;          // over both sums
   float s = 0.f;
-  if (c < 2ll * cols) {
-    const float* p = part + c;
-#pragma unroll 8
-    for (int i = sy; i < parts; i += 8) s += p[static_cast<int64_t>(i) * 2 * cols];
+  if (c0 + cx < 2ll * cols) {
+    const float* p = part + c0 + cx;
+#pragma unroll 5
+    for (int i = sy; i < parts; i += 32) s += p[static_cast<int64_t>(i) * 2 * cols];
   }
   red[sy][cx] = s;
   __syncthreads();
-  if (sy == 0 && c < 2ll * cols) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][cx];
+  s = warp_sum(red[cx][sy]);                                         // warp sy: column c0 + sy
+  const int64_t c = c0 + sy;
+  if (cx == 0 && c < 2ll * cols) {
     if (c < cols) {
       if (dw) dw[c] = s;
     } else if (db) {
@@ -607,6 +608,6 @@ extern "C" int mxq_layer_norm_backward(const void* dy, int64_t ld_dy, int dy_typ
     rc2 = dy_type == MXQ_BF16 ? norm_bwd<float, __nv_bfloat16>(a, vec, parts, st) : norm_bwd<float, float>(a, vec, parts, st);
   if (rc2 || !sums) return rc2;
   const int grid = static_cast<int>((2 * cols + 31) / 32);
-  return launch_pdl(norm_bwd_sum_kernel, dim3(grid), dim3(256), 0, st, static_cast<const float*>(workspace), parts,
+  return launch_pdl(norm_bwd_sum_kernel, dim3(grid), dim3(1024), 0, st, static_cast<const float*>(workspace), parts,
                     a.cols, dw, db);
 }
