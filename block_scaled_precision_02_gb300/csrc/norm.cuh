@@ -35,10 +35,11 @@ struct NormArgs {
   int wide_col;                   // q_col is 32-byte aligned
 };
 
-// 1 / sqrt(v): the hardware's estimate and one Newton step, within 2 ulp.
+// 1 / sqrt(v): the hardware's estimate and one Newton step, within 2 ulp; at
+// v = 0 or an infinity the estimate is the result.
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float r = rsqrtf(v);
-  return r * fmaf(-0.5f * v * r, r, 1.5f);
+  return v > 0.f && v < INFINITY ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
 }
 
 __device__ __forceinline__ float norm_value(float x, float mean, float rstd, float w, float b) {

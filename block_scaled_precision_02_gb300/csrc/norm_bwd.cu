@@ -25,14 +25,14 @@ struct BwdArgs {
 };
 
 // A thread owns VE * NV columns and keeps their two column sums in registers
-// while its CTA walks over rows, RB per step (their loads are in flight
-// together and share one barrier); a group of G threads has a row.  x and dy
-// are read once and dx written once, so HBM bounds it; the column sums of a
-// CTA go out once at the end and a second kernel adds them up in a fixed
-// order.
-template <typename TX, typename TD, int VE, int NV, int RB>
+// while its CTA walks over rows; a group of G threads has a row.  x and dy are
+// read once and dx written once; the column sums of a CTA go out once at the
+// end and a second kernel adds them up in a fixed order.  For few rows, and
+// for rows that the rings below do not take: bound by the latency of a row's
+// load, reduction and store.
+template <typename TX, typename TD, int VE, int NV>
 __global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) {
-  __shared__ float2 red[2][RB][32];
+  __shared__ float2 red[2][32];
   extern __shared__ __align__(16) float comb[];
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -53,79 +53,62 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) 
   }
 
   int buf = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * P * RB;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * P * RB; base < a.rows; base += step) {
-    const int64_t row = base + g * RB;
-    Vec<TX, VE> xr[RB][NV];
-    Vec<TD, VE> dr[RB][NV];
-    float mean[RB], rstd[RB], c1[RB], c2[RB];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * P;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * P; base < a.rows; base += step) {
+    const int64_t row = base + g;
+    const bool in = row < a.rows;            // a CTA's groups stay together for the barrier
+    const float mean = in ? a.mean[row] : 0.f, rstd = in ? a.rstd[row] : 0.f;
+    Vec<TX, VE> xr[NV];
+    Vec<TD, VE> dr[NV];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      const bool in = row + r < a.rows;
-      mean[r] = in ? a.mean[row + r] : 0.f;
-      rstd[r] = in ? a.rstd[row + r] : 0.f;
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        xr[r][k].fill(0);
-        dr[r][k].fill(0);
-        if (in && first + 32 * k < nvec) {
-          xr[r][k].load(static_cast<const TX*>(a.x) + (row + r) * a.ld_x + (first + 32 * k) * VE);
-          dr[r][k].load(static_cast<const TD*>(a.dy) + (row + r) * a.ld_dy + (first + 32 * k) * VE);
-        }
+    for (int k = 0; k < NV; ++k) {
+      xr[k].fill(0);
+      dr[k].fill(0);
+      if (in && first + 32 * k < nvec) {
+        xr[k].load(static_cast<const TX*>(a.x) + row * a.ld_x + (first + 32 * k) * VE);
+        dr[k].load(static_cast<const TD*>(a.dy) + row * a.ld_dy + (first + 32 * k) * VE);
       }
     }
+    float s1[NV], s2[NV];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      float s1[NV], s2[NV];
+    for (int k = 0; k < NV; ++k) {
+      float u[VE], v[VE];
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        float u[VE], v[VE];
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const float h = (xr[r][k].get(j) - mean[r]) * rstd[r];
-          const float d = dr[r][k].get(j);
-          u[j] = d * w[k][j];
-          v[j] = u[j] * h;
-          aw[k][j] = fmaf(d, h, aw[k][j]);
-          ab[k][j] += d;
-        }
-        s1[k] = tree_sum(u);
-        s2[k] = tree_sum(v);
+      for (int j = 0; j < VE; ++j) {
+        const float h = (xr[k].get(j) - mean) * rstd;
+        const float d = dr[k].get(j);
+        u[j] = d * w[k][j];
+        v[j] = u[j] * h;
+        aw[k][j] = fmaf(d, h, aw[k][j]);
+        ab[k][j] += d;
       }
-      c1[r] = warp_sum(tree_sum(s1));
-      c2[r] = warp_sum(tree_sum(s2));
+      s1[k] = tree_sum(u);
+      s2[k] = tree_sum(v);
     }
+    float c1 = warp_sum(tree_sum(s1)), c2 = warp_sum(tree_sum(s2));
     if (wpg > 1) {
-      if (lane == 0)
-#pragma unroll
-        for (int r = 0; r < RB; ++r) red[buf][r][warp] = make_float2(c1[r], c2[r]);
+      if (lane == 0) red[buf][warp] = make_float2(c1, c2);
       __syncthreads();
-#pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        c1[r] = c2[r] = 0.f;
-        for (int i = 0; i < wpg; ++i) {
-          const float2 v = red[buf][r][g * wpg + i];
-          c1[r] += v.x;
-          c2[r] += v.y;
-        }
+      c1 = c2 = 0.f;
+      for (int i = 0; i < wpg; ++i) {
+        const float2 v = red[buf][g * wpg + i];
+        c1 += v.x;
+        c2 += v.y;
       }
       buf ^= 1;
     }
+    if (!in) continue;
+    const float m1 = c1 * inv_c, m2 = c2 * inv_c;
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      if (row + r >= a.rows) continue;
-      const float m1 = c1[r] * inv_c, m2 = c2[r] * inv_c;
+    for (int k = 0; k < NV; ++k) {
+      if (first + 32 * k >= nvec) continue;
+      float o[VE];
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        if (first + 32 * k >= nvec) continue;
-        float o[VE];
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const float h = (xr[r][k].get(j) - mean[r]) * rstd[r];
-          o[j] = (fmaf(dr[r][k].get(j), w[k][j], -m1) - h * m2) * rstd[r];
-        }
-        store_vec<TX, VE>(static_cast<TX*>(a.dx) + (row + r) * a.cols + (first + 32 * k) * VE, o);
+      for (int j = 0; j < VE; ++j) {
+        const float h = (xr[k].get(j) - mean) * rstd;
+        o[j] = (fmaf(dr[k].get(j), w[k][j], -m1) - h * m2) * rstd;
       }
+      store_vec<TX, VE>(static_cast<TX*>(a.dx) + row * a.cols + (first + 32 * k) * VE, o);
     }
   }
   if (!a.part) return;
@@ -491,7 +474,7 @@ int launch_bwd(const BwdArgs& a, int G, int& parts, cudaStream_t st) {
   const int64_t groups = (a.rows + P - 1) / P;
   const int most = std::min(bwd_parts(), std::max(1, 2048 / threads) * sm_count());
   parts = static_cast<int>(std::min<int64_t>(most, groups));
-  return launch_pdl(norm_bwd_kernel<TX, TD, VE, NV, 1>, dim3(parts), dim3(threads), smem, st, a, G);
+  return launch_pdl(norm_bwd_kernel<TX, TD, VE, NV>, dim3(parts), dim3(threads), smem, st, a, G);
 }
 
 // Rings while a group's slots fit and every group gets two rows or more.

@@ -113,6 +113,19 @@ def test_forward_constant_zero_and_empty_rows(lib):
     assert y.shape == (0, 640) and mean.numel() == 0 and rstd.numel() == 0
 
 
+@pytest.mark.parametrize("rows", [3, 6000])
+def test_forward_variance_at_the_ends_of_float32(lib, rows):
+    """eps 0 on constant rows: rstd is infinite, y NaN (0 * inf), as the formula
+    says.  Variances beyond float32: rstd 0 and y = bias."""
+    x = torch.full((rows, 1024), 2.0, device=dev)
+    y, mean, rstd = lib.layer_norm(x, eps=0.0)
+    assert (mean == 2).all() and rstd.isinf().all() and y.isnan().all()
+    x[:, ::2] = 1e25
+    b = torch.full((1024,), 0.5, device=dev)
+    y, mean, rstd = lib.layer_norm(x, None, b)
+    assert (rstd == 0).all() and (y == 0.5).all()
+
+
 @pytest.mark.parametrize("cols", [640, 4096, 2049, 33000])
 def test_forward_nonfinite_rows_stay_alone(lib, cols):
     """NaN and infinities make their own row NaN and touch no other."""
