@@ -746,15 +746,20 @@ _dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape"
 
 
 def _grad_types(ts, what: str):
-    """Type codes of a list of gradient tensors, each filling its stretch of memory."""
-    for k, t in enumerate(ts):
-        if not isinstance(t, torch.Tensor) or t.dtype not in _TYPE:
-            raise ValueError(f"{what}[{k}] must be a bf16 or float32 tensor")
-    if not all(map(torch.Tensor.is_contiguous, ts)):
+    """Type codes of a list of gradient tensors, each filling its stretch of
+    memory, and whether all are contiguous."""
+    plain = set(map(type, ts)) <= {torch.Tensor, torch.nn.Parameter}
+    dtypes = list(map(_dtype_of, ts)) if plain else [getattr(t, "dtype", None) for t in ts]
+    if not plain or not _TYPE.keys() >= set(dtypes):
+        for k, t in enumerate(ts):
+            if not isinstance(t, torch.Tensor) or t.dtype not in _TYPE:
+                raise ValueError(f"{what}[{k}] must be a bf16 or float32 tensor")
+    contiguous = all(map(torch.Tensor.is_contiguous, ts))
+    if not contiguous:
         for k, t in enumerate(ts):
             if not t.is_contiguous() and not _dense(t):
                 raise ValueError(f"{what}[{k}] must fill its storage (contiguous, or a transpose of such)")
-    return [_TYPE[d] for d in map(_dtype_of, ts)]
+    return [_TYPE[d] for d in dtypes], contiguous
 
 
 def _grad_call(name: str, grads, out, *args) -> torch.Tensor:
@@ -765,15 +770,15 @@ def _grad_call(name: str, grads, out, *args) -> torch.Tensor:
     if not grads:
         raise ValueError("at least one gradient tensor")
     n = len(grads)
-    types = _grad_types(grads, "grads")
+    types, contiguous = _grad_types(grads, "grads")
     outs = grads
     if out is not None:
         outs = list(out)
         if len(outs) != n:
             raise ValueError(f"{n} gradients, {len(outs)} outputs")
-        types = [g | o << 32 for g, o in zip(types, _grad_types(outs, "out"))]
-        if list(map(_shape_of, grads)) != list(map(_shape_of, outs)) or not (
-                all(map(torch.Tensor.is_contiguous, grads)) and all(map(torch.Tensor.is_contiguous, outs))):
+        out_types, out_contiguous = _grad_types(outs, "out")
+        types = [g | o << 32 for g, o in zip(types, out_types)]
+        if not (contiguous and out_contiguous) or list(map(_shape_of, grads)) != list(map(_shape_of, outs)):
             for k, (g, o) in enumerate(zip(grads, outs)):
                 if o.shape != g.shape or not (g.is_contiguous() and o.is_contiguous() or g.stride() == o.stride()):
                     raise ValueError(f"out[{k}] must have the shape and strides of grads[{k}]")

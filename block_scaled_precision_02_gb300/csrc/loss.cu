@@ -89,16 +89,35 @@ __device__ __forceinline__ void store_edge(T* row, int e0, int V, const float (&
       }
 }
 
+// What a token brings besides its logits: loaded together, and ahead of use,
+// because each is a trip to memory of its own.
+struct TokenIn {
+  float w, adv, old_lp, ref_lp;
+  int64_t target;
+};
+
+__device__ __forceinline__ TokenIn token_in(const LossArgs& a, int64_t row) {
+  TokenIn t{0.f, 0.f, 0.f, 0.f, -1};
+  if (row < a.tokens) {
+    t.w = a.weights[row];
+    t.adv = a.adv[row];
+    t.old_lp = a.old_lp[row];
+    if (a.beta != 0.f) t.ref_lp = a.ref_lp[row];
+    t.target = a.targets64 ? static_cast<const int64_t*>(a.targets)[row]
+                           : static_cast<int64_t>(static_cast<const int*>(a.targets)[row]);
+  }
+  return t;
+}
+
 // Loss term and its slope dl/dlp of one token.
-__device__ __forceinline__ void token_loss(const LossArgs& a, int64_t row, float lp, float& l, float& slope) {
-  const float A = a.adv[row];
-  const float r = expf(lp - a.old_lp[row]);
-  const float ra = r * A, ca = fminf(fmaxf(r, 1.f - a.lo), 1.f + a.hi) * A;
+__device__ __forceinline__ void token_loss(const LossArgs& a, const TokenIn& t, float lp, float& l, float& slope) {
+  const float r = expf(lp - t.old_lp);
+  const float ra = r * t.adv, ca = fminf(fmaxf(r, 1.f - a.lo), 1.f + a.hi) * t.adv;
   const float nan = __int_as_float(0x7FFFFFFF);
   l = ra <= ca ? -ra : (ca < ra ? -ca : nan);
   slope = lp != lp ? nan : (ra <= ca ? -ra : 0.f);
   if (a.beta != 0.f) {
-    const float d = a.ref_lp[row] - lp;
+    const float d = t.ref_lp - lp;
     const float x = expm1f(d);
     l += a.beta * (x - d);
     slope -= a.beta * x;
@@ -159,9 +178,9 @@ __global__ void __launch_bounds__(TPB == 32 ? 256 : TPB, TPB == 32 ? 4 : 1024 / 
   const int V = a.vocab;
   const int h = static_cast<int>((reinterpret_cast<uintptr_t>(z) / sizeof(TZ)) % VE);
   const int nvec = (V + h + VE - 1) / VE;
-  const float wt = a.weights[row];
+  const TokenIn tok = token_in(a, row);
 
-  if (wt == 0.f) {                       // nothing of the row is read
+  if (tok.w == 0.f) {                    // nothing of the row is read
     const float zero[VE] = {};
     if (g)
       for (int i = rank * TPB + t; i < nvec; i += slabs * TPB) store_edge<TG, VE>(g, i * VE - h, V, zero);
@@ -171,14 +190,12 @@ __global__ void __launch_bounds__(TPB == 32 ? 256 : TPB, TPB == 32 ? 4 : 1024 / 
     }
     if (CLUSTER) cluster_wait();
   } else {
-    const int64_t target = a.targets64 ? static_cast<const int64_t*>(a.targets)[row]
-                                       : static_cast<int64_t>(static_cast<const int*>(a.targets)[row]);
-    const bool inside = target >= 0 && target < V;
+    const bool inside = tok.target >= 0 && tok.target < V;
     float za = __int_as_float(0x7FFFFFFF);
     if (inside) {
-      Vec<TZ, 1> t;
-      t.load(z + target);
-      za = t.get(0);
+      Vec<TZ, 1> one;
+      one.load(z + tok.target);
+      za = one.get(0);
     }
     const int first = LONG ? rank * TPB + t : rank * TPB * NV + t;
     float e[NV][VE];
@@ -241,14 +258,14 @@ __global__ void __launch_bounds__(TPB == 32 ? 256 : TPB, TPB == 32 ? 4 : 1024 / 
     }
     const float lp = (za - top) - logf(total);
     float l, slope;
-    token_loss(a, row, lp, l, slope);
+    token_loss(a, tok, lp, l, slope);
     if (rank == 0 && t == 0) {
       a.logp[row] = lp;
-      a.terms[row] = wt * l;
+      a.terms[row] = tok.w * l;
     }
     if (g) {
-      const float k = a.scale * wt * slope;
-      const int at = inside ? static_cast<int>(target) : -VE;
+      const float k = a.scale * tok.w * slope;
+      const int at = inside ? static_cast<int>(tok.target) : -VE;
       if constexpr (LONG) {
         const float f = -k / total;
         for (int i = first; i < nvec; i += slabs * TPB) {
@@ -340,22 +357,6 @@ __device__ __forceinline__ void to_gradient(float (&v)[VE], float2 top, float f,
     for (int j = 0; j < VE; ++j)
       if (j == target) v[j] += k;
   }
-}
-
-// What a token brings besides its logits, loaded one token ahead.
-struct TokenIn {
-  float w;
-  int64_t target;
-};
-
-__device__ __forceinline__ TokenIn token_in(const LossArgs& a, int64_t row) {
-  TokenIn t{0.f, -1};
-  if (row < a.tokens) {
-    t.w = a.weights[row];
-    t.target = a.targets64 ? static_cast<const int64_t*>(a.targets)[row]
-                           : static_cast<int64_t>(static_cast<const int*>(a.targets)[row]);
-  }
-  return t;
 }
 
 template <typename TZ, typename TG>
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
       total = warp_sum(total);
       const float lp = (za - top) - logf(total);
       float l, slope;
-      token_loss(a, row, lp, l, slope);
+      token_loss(a, tok, lp, l, slope);
       if (rank == 0 && t == 0) {
         a.logp[row] = lp;
         a.terms[row] = tok.w * l;
