@@ -49,6 +49,14 @@ __device__ __forceinline__ float ex2(float v) {
 // relative to the distance from the maximum and not to the logits' size.
 __device__ __forceinline__ float exp_rel(float v, float m) { return ex2((v - m) * kLog2e); }
 
+// exp(v - m) of a pair, m and log2(e) splat.
+__device__ __forceinline__ void exp_pair(float a, float b, float2 mm, float2 l2e, float& x, float& y) {
+  float p, q;
+  halves(mul2(sub2(pair(a, b), mm), l2e), p, q);
+  x = ex2(p);
+  y = ex2(q);
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
@@ -230,11 +238,14 @@ __global__ void __launch_bounds__(TPB == 32 ? 256 : TPB, TPB == 32 ? 4 : 1024 / 
         for (int j = 0; j < VE; ++j) m = fmaxf(m, e[k][j]);
       m = warp_max(m);
       const float ms = m == -INFINITY ? 0.f : m;
+      const float2 mm = splat(ms), l2e = splat(kLog2e);
       float part[NV];
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
+        if constexpr (VE == 1) e[k][0] = exp_rel(e[k][0], ms);
+        else
 #pragma unroll
-        for (int j = 0; j < VE; ++j) e[k][j] = exp_rel(e[k][j], ms);
+          for (int j = 0; j < VE; j += 2) exp_pair(e[k][j], e[k][j + 1], mm, l2e, e[k][j], e[k][j + 1]);
         part[k] = tree_sum(e[k]);
       }
       s = warp_sum(tree_sum(part));
@@ -285,7 +296,12 @@ __global__ void __launch_bounds__(TPB == 32 ? 256 : TPB, TPB == 32 ? 4 : 1024 / 
           const int e0 = (first + q * TPB) * VE - h;
           float o[VE];
 #pragma unroll
-          for (int j = 0; j < VE; ++j) o[j] = fmaf(e[q][j], f, e0 + j == at ? k : 0.f);
+          for (int j = 0; j < VE; ++j) o[j] = e[q][j] * f;
+          if (static_cast<unsigned>(at - e0) < static_cast<unsigned>(VE)) {
+#pragma unroll
+            for (int j = 0; j < VE; ++j)
+              if (e0 + j == at) o[j] += k;
+          }
           store_edge<TG, VE>(g, e0, V, o);
         }
       }
@@ -316,14 +332,6 @@ constexpr int RING_CHUNK = 16384, RING_SLOTS = 6, RING_AHEAD = 2;
 constexpr int RING_TPB = 256, RING_WARPS = RING_TPB / 32;
 constexpr int RING_MIN = 32 * 1024;
 constexpr float kLowest = -3.402823466e38f;
-
-// exp(v - m) of a pair, m and log2(e) splat.
-__device__ __forceinline__ void exp_pair(float a, float b, float2 mm, float2 l2e, float& x, float& y) {
-  float p, q;
-  halves(mul2(sub2(pair(a, b), mm), l2e), p, q);
-  x = ex2(p);
-  y = ex2(q);
-}
 
 // A thread's running maximum and sum over VE more elements.
 template <int VE>
