@@ -132,19 +132,30 @@ __device__ __forceinline__ void token_loss(const LossArgs& a, const TokenIn& t, 
   }
 }
 
-// The tokens' terms in their order per thread and the threads' sums in a
-// fixed tree, in float64 (one CTA).
+// The tokens' terms (one CTA): a thread adds its own in their order as an
+// unevaluated pair (the rounding error of each float32 addition is exactly
+// (a - (s - v)) + (b - v) with s = a + b, v = s - a, and is kept apart), the
+// threads' sums go up a fixed tree in float64.  All-float64 additions at two
+// lanes a cycle took longer than the loads.
 __device__ __forceinline__ void add_terms(const LossArgs& a) {
   __shared__ double sums[32];
-  double s = 0.0;
-  for (int i = threadIdx.x; i < a.tokens; i += blockDim.x) s += static_cast<double>(__ldcg(a.terms + i));
+  float hi = 0.f, lo = 0.f;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < a.tokens; i += blockDim.x) {
+    const float t = __ldcg(a.terms + i);
+    const float sum = __fadd_rn(hi, t), v = __fsub_rn(sum, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, v)), __fsub_rn(t, v)));
+    hi = sum;
+  }
+  // an infinite or NaN sum has no error term
+  double s = fabsf(hi) < INFINITY ? static_cast<double>(hi) + static_cast<double>(lo) : static_cast<double>(hi);
   s = warp_sum(s);
   if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < static_cast<int>(blockDim.x >> 5); ++i) s += sums[i];
-    a.loss[0] = static_cast<float>(s);
-  }
+  if (threadIdx.x >= 32) return;
+  s = threadIdx.x < (blockDim.x >> 5) ? sums[threadIdx.x] : 0.0;
+  s = warp_sum(s);
+  if (threadIdx.x == 0) a.loss[0] = static_cast<float>(s);
 }
 
 // The last of `ctas` CTAs to finish adds them.
@@ -311,7 +322,7 @@ __global__ void __launch_bounds__(TPB == 32 ? 256 : TPB, TPB == 32 ? 4 : 1024 / 
 }
 
 // The sum alone, where thousands of CTAs on one ticket would take longer.
-__global__ void __launch_bounds__(512) loss_sum_kernel(const LossArgs a) {
+__global__ void __launch_bounds__(1024) loss_sum_kernel(const LossArgs a) {
   grid_dep_wait();
   add_terms(a);
 }
@@ -591,7 +602,7 @@ int launch_policy(const LossArgs& a, int slabs, cudaStream_t st) {
   const dim3 g(static_cast<unsigned>(grid)), b(TPB == 32 ? 256 : TPB);
   const int rc = CLUSTER ? launch_pdl_cluster(kern, g, b, 0, st, slabs, a, slabs, ticket) : launch_pdl(kern, g, b, 0, st, a, 1, ticket);
   if (rc || ticket) return rc;
-  return launch_pdl(loss_sum_kernel, dim3(1), dim3(512), 0, st, a);
+  return launch_pdl(loss_sum_kernel, dim3(1), dim3(1024), 0, st, a);
 }
 
 // Clusters of `slabs` CTAs that run at once (asked once per device and size).
