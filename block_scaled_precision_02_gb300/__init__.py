@@ -742,24 +742,28 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
-_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _grad_types(ts, what: str):
     """Type codes of a list of gradient tensors, each filling its stretch of
-    memory, and whether all are contiguous."""
-    plain = set(map(type, ts)) <= {torch.Tensor, torch.nn.Parameter}
-    dtypes = list(map(_dtype_of, ts)) if plain else [getattr(t, "dtype", None) for t in ts]
-    if not plain or not _TYPE.keys() >= set(dtypes):
+    memory (an array, as 64-bit words), and whether all are contiguous."""
+    dtypes = list(map(_dtype_of, ts)) if set(map(type, ts)) <= {torch.Tensor, torch.nn.Parameter} else [None]
+    kinds = set(dtypes)
+    if not kinds <= _TYPE.keys():
         for k, t in enumerate(ts):
             if not isinstance(t, torch.Tensor) or t.dtype not in _TYPE:
                 raise ValueError(f"{what}[{k}] must be a bf16 or float32 tensor")
+        dtypes = list(map(_dtype_of, ts))
+        kinds = set(dtypes)
     contiguous = all(map(torch.Tensor.is_contiguous, ts))
     if not contiguous:
         for k, t in enumerate(ts):
             if not t.is_contiguous() and not _dense(t):
                 raise ValueError(f"{what}[{k}] must fill its storage (contiguous, or a transpose of such)")
-    return [_TYPE[d] for d in dtypes], contiguous
+    if len(kinds) == 1:
+        return array.array("q", (_TYPE[dtypes[0]],)) * len(ts), contiguous
+    return array.array("q", [_TYPE[d] for d in dtypes]), contiguous
 
 
 def _grad_call(name: str, grads, out, *args) -> torch.Tensor:
@@ -771,19 +775,22 @@ def _grad_call(name: str, grads, out, *args) -> torch.Tensor:
         raise ValueError("at least one gradient tensor")
     n = len(grads)
     types, contiguous = _grad_types(grads, "grads")
-    outs = grads
+    sizes = array.array("q", map(torch.Tensor.numel, grads))
+    outs, out_types = grads, types
     if out is not None:
         outs = list(out)
         if len(outs) != n:
             raise ValueError(f"{n} gradients, {len(outs)} outputs")
         out_types, out_contiguous = _grad_types(outs, "out")
-        types = [g | o << 32 for g, o in zip(types, out_types)]
-        if not (contiguous and out_contiguous) or list(map(_shape_of, grads)) != list(map(_shape_of, outs)):
+        if contiguous and out_contiguous:
+            if array.array("q", map(torch.Tensor.numel, outs)) != sizes:
+                k = [o.numel() != g.numel() for g, o in zip(grads, outs)].index(True)
+                raise ValueError(f"out[{k}] holds {outs[k].numel()} elements, grads[{k}] {grads[k].numel()}")
+        else:
             for k, (g, o) in enumerate(zip(grads, outs)):
-                if o.shape != g.shape or not (g.is_contiguous() and o.is_contiguous() or g.stride() == o.stride()):
+                if o.numel() != g.numel() or not (g.is_contiguous() and o.is_contiguous()) and (
+                        o.shape != g.shape or o.stride() != g.stride()):
                     raise ValueError(f"out[{k}] must have the shape and strides of grads[{k}]")
-    else:
-        types = [g | g << 32 for g in types]
     dev, index = grads[0].device, grads[0].get_device()
     for ts, what in ((grads, "grads"),) if out is None else ((grads, "grads"), (outs, "out")):
         if index < 0 or set(map(torch.Tensor.get_device, ts)) != {index}:
@@ -792,8 +799,8 @@ def _grad_call(name: str, grads, out, *args) -> torch.Tensor:
     words = array.array("q", bytes(32 * n))
     words[0::4] = pointers = array.array("q", map(torch.Tensor.data_ptr, grads))
     words[1::4] = pointers if out is None else array.array("q", map(torch.Tensor.data_ptr, outs))
-    words[2::4] = array.array("q", map(torch.Tensor.numel, grads))
-    words[3::4] = array.array("q", types)
+    words[2::4] = sizes
+    words[3::4] = array.array("q", [g | o << 32 for g, o in zip(types, out_types)])
     norm = torch.empty(1, dtype=torch.float32, device=dev)
     need = _size("mxq_grad_norm_workspace_size", dev, n)
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -810,8 +817,9 @@ def grad_norm(grads) -> torch.Tensor:
 def clip_grad_norm(grads, max_norm: float, out=None) -> torch.Tensor:
     """Scale ``grads`` by min(1, max_norm / (norm + 1e-6)), norm being their
     global 2-norm, which is returned (1-element float32, nothing is read back
-    to the host).  In place, or into the tensors of ``out`` (same shapes,
-    bf16 or float32, e.g. an optimizer's float32 buffers)."""
+    to the host).  In place, or into the tensors of ``out`` (bf16 or float32,
+    of as many elements each, e.g. stretches of an optimizer's float32 buffer;
+    a gradient that is not contiguous needs one of its own strides)."""
     if not max_norm >= 0:
         raise ValueError("max_norm must not be negative")
     return _grad_call("mxq_clip_grad_norm", grads, out, max_norm)

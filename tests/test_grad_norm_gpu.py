@@ -92,6 +92,22 @@ def test_transposed_gradients(lib):
     assert torch.equal(o, lib_scaled(lib, g).t())
 
 
+def test_outputs_of_other_shapes(lib):
+    """Stretches of a flat buffer take the elements in their order."""
+    gs = grads([(12, 7), (5,), (3, 4, 2)], [F32], 14)
+    flat = torch.zeros(200, device=dev)
+    outs = [flat[:84], flat[96:101], flat[128:152]]
+    lib.clip_grad_norm(gs, 0.5, out=outs)
+    want = [lib_scaled_by(gs, g, 0.5) for g in gs]
+    for o, w in zip(outs, want):
+        assert (np.abs(d(o) - w) <= 8 * U * np.abs(w)).all()
+    assert (flat[84:96] == 0).all() and (flat[152:] == 0).all()
+
+
+def lib_scaled_by(gs, g, max_norm):
+    return (d(g) * min(1.0, max_norm / (norm_ref(gs) + 1e-6))).reshape(-1)
+
+
 def lib_scaled(lib, g):
     o = torch.empty_like(g)
     lib.clip_grad_norm([g], 1.0, out=[o])

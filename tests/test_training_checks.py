@@ -80,6 +80,14 @@ def test_clip_checks():
         mxq.grad_norm([z(4)])
     with pytest.raises(ValueError, match="fill its storage"):
         mxq.grad_norm([z(8)[::2]])
+    with pytest.raises(ValueError, match=r"out\[0\] holds 5 elements, grads\[0\] 4"):
+        mxq.clip_grad_norm([z(4)], 1.0, out=[z(5)])
+    with pytest.raises(ValueError, match="shape and strides"):
+        mxq.clip_grad_norm([z(4, 8).t()], 1.0, out=[z(8, 4)])
+    with pytest.raises(ValueError, match=r"out\[1\] must be a bf16 or float32"):
+        mxq.clip_grad_norm([z(4), z(4)], 1.0, out=[z(4), z(4, dtype=torch.int32)])
+    with pytest.raises(ValueError, match=r"grads\[0\] must be a bf16 or float32"):
+        mxq.grad_norm([3.0])
     with pytest.raises(ValueError, match="1 gradients, 2 outputs"):
         mxq.clip_grad_norm([z(4)], 1.0, out=[z(4), z(4)])
     with pytest.raises(ValueError, match="must not be negative"):
