@@ -180,6 +180,13 @@ __device__ __forceinline__ void finish_loss(const LossArgs& a, unsigned ctas) {
   if (threadIdx.x == 0) *a.ticket = 0;
 }
 
+// CTAs of the register kernels that an SM holds, by registers: 42 a thread for
+// 16 elements or fewer, 56 or 64 for 32 (64 where single elements move).
+template <int VE, int NV, int TPB>
+constexpr int policy_ctas() {
+  return TPB == 32 ? 4 : (VE * NV <= 16 ? 1536 : VE > 1 && TPB % 3 == 0 ? 1152 : 1024) / TPB;
+}
+
 // `slabs` CTAs (one cluster) per token; a thread holds NV vectors of VE
 // elements.  Vectors start at the row's first 16-byte boundary at or before
 // its first element, `h` elements ahead of it, so rows of odd length still
@@ -192,9 +199,6 @@ __device__ __forceinline__ void finish_loss(const LossArgs& a, unsigned ctas) {
 // a CTA loads, reduces and stores in turn, and the few that fit an SM do not
 // cover one another's trip to memory (16384 x 8192 bf16: 158 us without, 125
 // with; 16384 x 1000: 30 and 25.5).
-template <int VE, int NV, int TPB>
-constexpr int policy_ctas() { return TPB == 32 ? 4 : (VE * NV <= 16 ? 1536 : 1024) / TPB; }
-
 template <typename TZ, typename TG, int VE, int NV, bool LONG, int TPB, bool CLUSTER>
 __global__ void __launch_bounds__(TPB == 32 ? 256 : TPB, policy_ctas<VE, NV, TPB>())
     policy_kernel(const LossArgs a, int slabs, int ticket, int64_t ahead) {
@@ -359,7 +363,6 @@ __global__ void __launch_bounds__(1024) loss_sum_kernel(const LossArgs a) {
 // token masked: 229 us against 189, 84 % of the measured copy rate).
 constexpr int RING_CHUNK = 16384, RING_SLOTS = 6, RING_AHEAD = 2;
 constexpr int RING_TPB = 256, RING_WARPS = RING_TPB / 32;
-constexpr int RING_MIN = 8192;                               // shorter rows stay in registers
 constexpr float kLowest = -3.402823466e38f;
 
 // A thread's running maximum and sum over VE more elements.
@@ -663,13 +666,15 @@ int64_t row_words(const LossArgs& a) {
   return (static_cast<int64_t>(a.vocab) + (flush ? 0 : VE - 1) + VE - 1) / VE;
 }
 
-// The ring kernel takes rows of more than RING_MIN elements (bf16, 16384 x 8192:
-// 174 us against 154 in registers; 16384 x 12000: 220 against 271) when every CTA
-// gets two tokens or more, in the smallest cluster whose CTAs keep RING_AHEAD
-// chunks of the ring for the next token.  0: not for it.
+// The ring kernel takes rows beyond the register kernels' (float32), or their
+// last step of 12288 to 16384 elements and on (bf16), when every CTA gets two
+// tokens or more, in the smallest cluster whose CTAs keep RING_AHEAD chunks of
+// the ring for the next token.  Here against in registers, us: bf16 16384 x
+// 12000 220 and 177, 8192 x 16384 121 and 131; float32 8192 x 12001 137 and 99,
+// 4096 x 16384 100 and 86.  0: not for it.
 template <typename TZ>
 int ring_slabs(const LossArgs& a) {
-  if (a.vocab <= RING_MIN) return 0;
+  if (a.vocab <= (sizeof(TZ) == 2 ? 12288 : 16384)) return 0;
   for (int slabs = 1; slabs <= MAX_SLABS; slabs *= 2)
     if ((row_words<TZ>(a) + slabs - 1) / slabs <= (RING_SLOTS - RING_AHEAD) * (RING_CHUNK / 16))
       return static_cast<int64_t>(a.tokens) * slabs >= 4 * sm_count() ? slabs : 0;
@@ -687,11 +692,12 @@ int launch_ring(const LossArgs& a, int slabs, cudaStream_t st) {
 }
 
 // With enough tokens to fill the GPU, a row goes to the fewest threads that
-// hold it, 32 elements each: a warp, or a CTA of 4, 8 or 16 (half as many
+// hold it, 32 elements each: a warp, or a CTA of 4, 6, 8, 12 or 16 (half as many
 // elements to twice the threads: 16384 x 1000 bf16 30 -> 38 us, 8192 columns
-// 154 -> 161).  Longer rows, and
-// rows of few tokens, to clusters: the fewest CTAs of 16 warps that hold a row,
-// and more with few tokens, until there are two for every SM or eight to a row.
+// 154 -> 161; without the CTAs of 6 and 12: 6000 columns 93 -> 114 us, 12000
+// columns 177 -> 228).  Longer rows, and rows of few tokens, to clusters: the
+// fewest CTAs of 16 warps that hold a row, and more with few tokens, until there
+// are two for every SM or eight to a row.
 template <typename TZ, typename TG, int VE>
 int dispatch_policy(const LossArgs& a, cudaStream_t st) {
   constexpr int NMAX = MAX_E / VE;
@@ -705,7 +711,9 @@ int dispatch_policy(const LossArgs& a, cudaStream_t st) {
     if (nvec <= 128 * NMAX)
       return nvec <= 64 * NMAX ? launch_policy<TZ, TG, VE, NMAX / 2, false, 128, false>(a, 1, st)
                                : launch_policy<TZ, TG, VE, NMAX, false, 128, false>(a, 1, st);
+    if (nvec <= 192 * NMAX) return launch_policy<TZ, TG, VE, NMAX, false, 192, false>(a, 1, st);
     if (nvec <= 256 * NMAX) return launch_policy<TZ, TG, VE, NMAX, false, 256, false>(a, 1, st);
+    if (nvec <= 384 * NMAX) return launch_policy<TZ, TG, VE, NMAX, false, 384, false>(a, 1, st);
     return launch_policy<TZ, TG, VE, NMAX, false, 512, false>(a, 1, st);
   }
   constexpr int TPB = 512;

@@ -118,6 +118,23 @@ def test_strided_logits_and_int32_targets(lib, V, shift):
         check(lib.policy_loss(z, a.int(), old, adv, w, grad_dtype=gt), r)
 
 
+@pytest.mark.parametrize("T,V", [(9800, 100), (3700, 1001), (1900, 5001), (1200, 7000), (200, 5000), (200, 8193),
+                                 (920, 9001), (700, 12290)])
+@pytest.mark.parametrize("zt,gt", [(BF, BF), (F32, BF)])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_many_tokens(lib, T, V, zt, gt, pad):
+    """Enough tokens that a row brings a later one near, masked ones among
+    them, up to the last row of the matrix; padded rows of any alignment."""
+    z, a, old, adv, w, ref = batch(T, V, zt, T + V, masked=0.8)
+    w[-1] = w[0] = 1.0 / T
+    if pad:
+        wide = torch.full((T, V + pad), 7.0, device=dev, dtype=zt)
+        wide[:, :V] = z
+        z = wide[:, :V]
+    r = reference(z, a, old, adv, w, ref)
+    check(lib.policy_loss(z, a, old, adv, w, grad_dtype=gt), r)
+
+
 def test_clipping_on_each_side(lib):
     """Ratios 0.5, 1, 2 with advantages of both signs, asymmetric clip: the
     slope is zero exactly where the clipped product is the smaller."""
