@@ -511,7 +511,6 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, trans_a: bool 
 _TYPE = {torch.bfloat16: BF16, torch.float32: F32}
 _PARAM = (torch.bfloat16, torch.float32)
 _F32_ONLY = (torch.float32,)
-_SCRATCH = {}
 _SIZES = {}
 
 
@@ -541,17 +540,6 @@ def _size(name: str, device: torch.device, *args) -> int:
             _SIZES.clear()
         n = _SIZES[key] = c.value
     return n
-
-
-def _scratch(device: torch.device, nbytes: int) -> torch.Tensor:
-    """Zero-filled scratch of at least ``nbytes`` for torch's current stream
-    on ``device``, kept and grown as needed: one per stream, because calls
-    that share it must not overlap on the GPU."""
-    key = (device.index, torch._C._cuda_getCurrentRawStream(device.index))
-    w = _SCRATCH.get(key)
-    if w is None or w.numel() < nbytes:
-        w = _SCRATCH[key] = torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=device)
-    return w
 
 
 def _matrix(t: torch.Tensor, name: str):
@@ -725,10 +713,11 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Ten
     if grad:
         dz = torch.empty(tokens, vocab, dtype=grad_dtype, device=dev)
         gp = dz.data_ptr()
-    ws = _scratch(dev, _size("mxq_policy_loss_workspace_size", dev, tokens))
+    need = _size("mxq_policy_loss_workspace_size", dev, tokens)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _launch("mxq_policy_loss", dev, logits.data_ptr(), tokens, vocab, ld, zt, tp,
-            int(targets.dtype == torch.int64), op, ap, wp, rp, clip_low, clip_high, beta, grad_scale, loss.data_ptr(), logp.data_ptr(), gp, vocab, _TYPE[grad_dtype],
-            ws.data_ptr(), ws.numel())
+            int(targets.dtype == torch.int64), op, ap, wp, rp, clip_low, clip_high, beta, grad_scale, loss.data_ptr(),
+            logp.data_ptr(), gp, vocab, _TYPE[grad_dtype], ws.data_ptr(), need)
     return loss, logp, dz
 
 

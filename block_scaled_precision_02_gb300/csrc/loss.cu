@@ -35,9 +35,8 @@ struct LossArgs {
   float lo, hi, beta, scale;
   int tokens, vocab;
   float* logp;
-  float* terms;                          // [tokens] w * l, summed by the last CTA
+  float* terms;                          // [tokens] w * l
   float* loss;
-  unsigned* ticket;                      // 0 on entry, left 0
 };
 
 __device__ __forceinline__ float ex2(float v) {
@@ -141,13 +140,17 @@ __device__ __forceinline__ void token_loss(const LossArgs& a, const TokenIn& t, 
   }
 }
 
-// The tokens' terms (one CTA): a thread adds its own in their order as an
-// unevaluated pair (the rounding error of each float32 addition is exactly
+// The loss: the tokens' terms, added by one CTA that follows the rows'
+// kernels (it starts early and waits, so it adds little to them).  A ticket
+// that lets the last row's CTA do it would have to be zero beforehand, in
+// memory that outlives the call or by a launch before it.  A thread adds its
+// own terms in their order as an unevaluated pair (the rounding error of each float32 addition is exactly
 // (a - (s - v)) + (b - v) with s = a + b, v = s - a, and is kept apart), the
 // threads' sums go up a fixed tree in float64.  All-float64 additions at two
 // lanes a cycle took longer than the loads.
-__device__ __forceinline__ void add_terms(const LossArgs& a) {
+__global__ void __launch_bounds__(1024) loss_sum_kernel(const LossArgs a) {
   __shared__ double sums[32];
+  grid_dep_wait();
   float hi = 0.f, lo = 0.f;
 #pragma unroll 8
   for (int i = threadIdx.x; i < a.tokens; i += blockDim.x) {
@@ -165,19 +168,6 @@ __device__ __forceinline__ void add_terms(const LossArgs& a) {
   s = threadIdx.x < (blockDim.x >> 5) ? sums[threadIdx.x] : 0.0;
   s = warp_sum(s);
   if (threadIdx.x == 0) a.loss[0] = static_cast<float>(s);
-}
-
-// The last of `ctas` CTAs to finish adds them.
-__device__ __forceinline__ void finish_loss(const LossArgs& a, unsigned ctas) {
-  __shared__ unsigned last;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) == ctas - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  add_terms(a);
-  if (threadIdx.x == 0) *a.ticket = 0;
 }
 
 // CTAs of the register kernels that an SM holds, by registers: 42 a thread for
@@ -201,11 +191,12 @@ constexpr int policy_ctas() {
 // with; 16384 x 1000: 30 and 25.5).
 template <typename TZ, typename TG, int VE, int NV, bool LONG, int TPB, bool CLUSTER>
 __global__ void __launch_bounds__(TPB == 32 ? 256 : TPB, policy_ctas<VE, NV, TPB>())
-    policy_kernel(const LossArgs a, int slabs, int ticket, int64_t ahead) {
+    policy_kernel(const LossArgs a, int slabs, int64_t ahead) {
   constexpr int WPB = TPB / 32;
   __shared__ float2 pairs[(CLUSTER ? MAX_SLABS : 1) * WPB];
   if (CLUSTER) cluster_arrive();
   grid_dep_wait();
+  grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = TPB == 32 ? 0 : threadIdx.x >> 5;
   const int t = TPB == 32 ? lane : threadIdx.x;
   if (!CLUSTER) slabs = 1;
@@ -340,13 +331,6 @@ __global__ void __launch_bounds__(TPB == 32 ? 256 : TPB, policy_ctas<VE, NV, TPB
       }
     }
   }
-  if (ticket && rank == 0) finish_loss(a, a.tokens);
-}
-
-// The sum alone, where thousands of CTAs on one ticket would take longer.
-__global__ void __launch_bounds__(1024) loss_sum_kernel(const LossArgs a) {
-  grid_dep_wait();
-  add_terms(a);
 }
 
 // ---------------------------------------------------------------- long rows of many tokens
@@ -418,6 +402,7 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
   }
   cluster_sync();
   grid_dep_wait();
+  grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % slabs;
   const int64_t row0 = blockIdx.x / slabs, step = gridDim.x / slabs;
@@ -601,7 +586,6 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
     }
   }
   cluster_sync();                                            // no peer writes here any more
-  if (rank == 0) finish_loss(a, static_cast<unsigned>(step));
 }
 
 using namespace mxq_host;
@@ -610,15 +594,10 @@ bool valid_type(int t) { return t == MXQ_BF16 || t == MXQ_F32; }
 int type_size(int t) { return t == MXQ_F32 ? 4 : 2; }
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Up to this many CTAs share the ticket; more are followed by a kernel that
-// adds the terms (16384 tokens of 1000, bf16, on one ticket: 111 us, 37 without).
-constexpr int TICKET_MAX = 1024;
-
 template <typename TZ, typename TG, int VE, int NV, bool LONG, int TPB, bool CLUSTER>
 int launch_policy(const LossArgs& a, int slabs, cudaStream_t st) {
   const int64_t grid = TPB == 32 ? (static_cast<int64_t>(a.tokens) + 7) / 8 : static_cast<int64_t>(a.tokens) * slabs;
   if (grid > 0x7FFFFFFF) return MXQ_ERR_BAD_SHAPE;
-  const int ticket = TPB > 32 && a.tokens <= TICKET_MAX;
   auto kern = policy_kernel<TZ, TG, VE, NV, LONG, TPB, CLUSTER>;
   const dim3 g(static_cast<unsigned>(grid)), b(TPB == 32 ? 256 : TPB);
   // The rows that run at once; a quarter of them start within the next row's
@@ -626,10 +605,8 @@ int launch_policy(const LossArgs& a, int slabs, cudaStream_t st) {
   // a quarter 125).  Nothing is ahead while most rows start together.
   const int64_t live = static_cast<int64_t>(sm_count()) * policy_ctas<VE, NV, TPB>() * (TPB == 32 ? 8 : 1);
   const int64_t ahead = a.tokens >= 2 * live ? live / 4 : 0;
-  const int rc = CLUSTER ? launch_pdl_cluster(kern, g, b, 0, st, slabs, a, slabs, ticket, int64_t{0})
-                         : launch_pdl(kern, g, b, 0, st, a, 1, ticket, ahead);
-  if (rc || ticket) return rc;
-  return launch_pdl(loss_sum_kernel, dim3(1), dim3(1024), 0, st, a);
+  return CLUSTER ? launch_pdl_cluster(kern, g, b, 0, st, slabs, a, slabs, int64_t{0})
+                 : launch_pdl(kern, g, b, 0, st, a, 1, ahead);
 }
 
 // Clusters of `slabs` CTAs that run at once (asked once per device and size).
@@ -728,7 +705,7 @@ int dispatch_policy(const LossArgs& a, cudaStream_t st) {
 }
 
 template <typename TZ, typename TG>
-int policy(const LossArgs& a, cudaStream_t st) {
+int policy_rows(const LossArgs& a, cudaStream_t st) {
   constexpr int VE = sizeof(TZ) == 2 && sizeof(TG) == 2 ? 8 : 4;
   constexpr int RVE = 16 / static_cast<int>(sizeof(TZ));
   // whole words on both sides: every row of the gradient starts at the same
@@ -740,6 +717,12 @@ int policy(const LossArgs& a, cudaStream_t st) {
   if (same(RVE))
     if (const int slabs = ring_slabs<TZ>(a)) return launch_ring<TZ, TG>(a, slabs, st);
   return same(VE) ? dispatch_policy<TZ, TG, VE>(a, st) : dispatch_policy<TZ, TG, 1>(a, st);
+}
+
+template <typename TZ, typename TG>
+int policy(const LossArgs& a, cudaStream_t st) {
+  const int rc = policy_rows<TZ, TG>(a, st);
+  return rc ? rc : launch_pdl(loss_sum_kernel, dim3(1), dim3(std::min(1024, (a.tokens + 31) / 32 * 32)), 0, st, a);
 }
 
 }  // namespace
@@ -785,8 +768,7 @@ extern "C" int mxq_policy_loss(const void* logits, int64_t tokens, int64_t vocab
   a.lo = clip_low, a.hi = clip_high, a.beta = beta, a.scale = grad_scale;
   a.tokens = static_cast<int>(tokens), a.vocab = static_cast<int>(vocab);
   a.logp = logp, a.loss = loss;
-  a.ticket = static_cast<unsigned*>(workspace);
-  a.terms = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+  a.terms = static_cast<float*>(workspace);
   using bf16 = __nv_bfloat16;
   if (logits_type == MXQ_BF16)
     return grad && grad_type == MXQ_F32 ? policy<bf16, float>(a, st) : policy<bf16, bf16>(a, st);

@@ -412,9 +412,9 @@ int mxq_layer_norm_backward(const void* dy, int64_t ld_dy, int dy_type,
  * clip_low, clip_high >= 0.
  * loss     one float; logp float [tokens].
  * grad     NULL, or [tokens][ld_grad] of grad_type; must not overlap logits.
- * workspace  mxq_policy_loss_workspace_size bytes, 16-byte aligned,
- *          zero-filled before its first use (its first 256 bytes are left
- *          zero).  Calls that share a workspace must not run concurrently.
+ * workspace  mxq_policy_loss_workspace_size bytes, 16-byte aligned, any
+ *          contents.  A call is two launches, so calls that share a workspace
+ *          must not overlap, nor be made by two threads at once.
  * Sums in a fixed order; tokens == 0 gives loss 0. */
 int mxq_policy_loss_workspace_size(int64_t tokens, size_t* bytes);
 int mxq_policy_loss(const void* logits, int64_t tokens, int64_t vocab,
