@@ -131,7 +131,7 @@ __device__ __forceinline__ void token_loss(const LossArgs& a, const TokenIn& t, 
   const float ra = r * t.adv, ca = fminf(fmaxf(r, 1.f - a.lo), 1.f + a.hi) * t.adv;
   const float nan = __int_as_float(0x7FFFFFFF);
   l = ra <= ca ? -ra : (ca < ra ? -ca : nan);
-  slope = lp != lp ? nan : (ra <= ca ? -ra : 0.f);
+  slope = ra <= ca ? -ra : (ca < ra ? 0.f : nan);
   if (a.beta != 0.f) {
     const float d = t.ref_lp - lp;
     const float x = expm1f(d);

@@ -399,8 +399,9 @@ int mxq_layer_norm_backward(const void* dy, int64_t ld_dy, int dy_type,
  *        + beta (exp(d) - d - 1),  d = ref_logp - lp
  *   loss = sum over tokens of w l
  *   grad_v = grad_scale w dl/dlp ([v == a] - exp(z_v - lse))
- * where the first term's slope is -A r while r A <= the clipped product and 0
- * beyond, and the second's beta (1 - exp(d)).
+ * where the first term's slope is -A r while r A <= the clipped product, 0
+ * beyond and NaN where the two do not compare (a NaN log-probability, old_logp
+ * or advantage shows in loss and grad), and the second's beta (1 - exp(d)).
  * logits   [tokens][ld] of logits_type, only the first vocab of a row read.
  * targets  int64 (targets_64 == 1) or int32 (0) [tokens].
  * weights  float [tokens].  A token of weight 0 (a prompt token, padding) is
