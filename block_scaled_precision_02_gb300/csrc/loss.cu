@@ -127,16 +127,18 @@ __device__ __forceinline__ TokenIn token_in(const LossArgs& a, int64_t row) {
 
 // Loss term and its slope dl/dlp of one token.
 __device__ __forceinline__ void token_loss(const LossArgs& a, const TokenIn& t, float lp, float& l, float& slope) {
-  const float r = expf(lp - t.old_lp);
+  const float x = lp - t.old_lp;
+  // no advantage, no term: also where the ratio is finite but beyond float32
+  const float r = t.adv == 0.f && x < INFINITY ? 0.f : expf(x);
   const float ra = r * t.adv, ca = fminf(fmaxf(r, 1.f - a.lo), 1.f + a.hi) * t.adv;
   const float nan = __int_as_float(0x7FFFFFFF);
   l = ra <= ca ? -ra : (ca < ra ? -ca : nan);
   slope = ra <= ca ? -ra : (ca < ra ? 0.f : nan);
   if (a.beta != 0.f) {
     const float d = t.ref_lp - lp;
-    const float x = expm1f(d);
-    l += a.beta * (x - d);
-    slope -= a.beta * x;
+    const float e = expm1f(d);
+    l += a.beta * (e - d);
+    slope -= a.beta * e;
   }
 }
 

@@ -38,3 +38,21 @@ def test_undefined_ratio_shows_in_the_gradient(lib, T, V, dtype, which, beta):
     rest = torch.ones(T, dtype=torch.bool, device=dev)
     rest[bad] = False
     assert torch.equal(dz[rest], clean[2][rest])
+
+
+@pytest.mark.parametrize("T,V,dtype", SHAPES)
+def test_no_advantage_means_no_term_whatever_the_ratio(lib, T, V, dtype):
+    """Ratios beyond float32 (an old log-probability 100 to 300 below): 0 under
+    advantage 0, as in float64, and the clipped product under a positive one."""
+    z, a, old, adv, w, ref = batch(T, V, dtype, T + V + 1)
+    rows = torch.arange(0, T, 5, device=dev)
+    old[rows] = ref[rows] - 100 - 200 * torch.rand(len(rows), device=dev)
+    adv[rows[::2]] = 0
+    adv[rows[1::4]] = -0.0
+    r = reference(z[:60], a[:60], old[:60], adv[:60], w[:60])
+    loss, lp, dz = lib.policy_loss(z, a, old, adv, w)
+    assert loss.isfinite().all() and dz.isfinite().all() and (dz[rows] == 0).all()
+    check(lib.policy_loss(z[:60].contiguous(), a[:60], old[:60], adv[:60], w[:60]), r)
+    adv[rows] = 0                       # without an upper clip the clipped ratio is as large
+    loss, lp, dz = lib.policy_loss(z, a, old, adv, w, clip_high=float("inf"))
+    assert loss.isfinite().all() and (dz[rows] == 0).all()
