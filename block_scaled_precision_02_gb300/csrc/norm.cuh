@@ -36,10 +36,11 @@ struct NormArgs {
 };
 
 // 1 / sqrt(v): the hardware's estimate and one Newton step, within 2 ulp; at
-// v = 0 or an infinity the estimate is the result.
+// v = 0 or an infinity the estimate is the result.  v r is normal for every
+// v, v / 2 is not.
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float r = rsqrtf(v);
-  return v > 0.f && v < INFINITY ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
+  return v > 0.f && v < INFINITY ? r * fmaf(v * r, -0.5f * r, 1.5f) : r;
 }
 
 __device__ __forceinline__ float norm_value(float x, float mean, float rstd, float w, float b) {
