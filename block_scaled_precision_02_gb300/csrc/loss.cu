@@ -748,7 +748,7 @@ extern "C" int mxq_policy_loss(const void* logits, int64_t tokens, int64_t vocab
   if (!valid_type(logits_type) || (grad && !valid_type(grad_type))) return MXQ_ERR_BAD_ARG;
   if ((targets_64 != 0 && targets_64 != 1) || !loss) return MXQ_ERR_BAD_ARG;
   if (tokens < 0 || vocab < 1 || ld < vocab || (grad && ld_grad < vocab)) return MXQ_ERR_BAD_SHAPE;
-  if (tokens > 0x7FFFFFFFll / MAX_SLABS || vocab > 0x7FFFFF00ll) return MXQ_ERR_BAD_SHAPE;
+  if (tokens > 0x7FFFFFFFll / MAX_SLABS || vocab > kMaxCols) return MXQ_ERR_BAD_SHAPE;
   if (tokens && (!logits || !targets || !old_logp || !advantages || !weights || !logp)) return MXQ_ERR_BAD_ARG;
   if (tokens && beta != 0.f && !ref_logp) return MXQ_ERR_BAD_ARG;
   if (!(clip_low >= 0.f) || !(clip_high >= 0.f)) return MXQ_ERR_BAD_ARG;

@@ -328,7 +328,7 @@ inline int check_norm(const void* x, int64_t rows, int64_t cols, int64_t ld, int
                const void* b, int b_type, const float* mean, const float* rstd) {
   if (!valid_type(x_type) || (w && !valid_type(w_type)) || (b && !valid_type(b_type))) return MXQ_ERR_BAD_ARG;
   if (rows < 0 || cols < 1 || ld < cols) return MXQ_ERR_BAD_SHAPE;
-  if (rows > 0x7FFFFFF0ll || cols > 0x7FFFFFF0ll) return MXQ_ERR_BAD_SHAPE;
+  if (rows > 0x7FFFFFF0ll || cols > kMaxCols) return MXQ_ERR_BAD_SHAPE;
   if (rows && (!x || !mean || !rstd)) return MXQ_ERR_BAD_ARG;
   if (!aligned_to(x, type_size(x_type)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4)) return MXQ_ERR_MISALIGNED;
   if ((w && !aligned_to(w, type_size(w_type))) || (b && !aligned_to(b, type_size(b_type)))) return MXQ_ERR_MISALIGNED;

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
   const int kbr = a.cols / 32, kbc = a.rows / 32;        // scales of a row of the row and the column copy
   const int k0 = (c0 + lane * 16) / 32;
   const int64_t row_step = a.mma ? 16 : kbr;
-  uint8_t* const my_rows = a.s_row + (a.mma ? (k0 >> 2) * 512 + (k0 & 3) : k0) + warp * RW * row_step;
+  uint8_t* const my_rows = a.s_row + scale_at(0, k0, kbr, a.mma) + warp * RW * row_step;
   uint32_t col_scales[S / T];                            // this thread's columns, a byte per tile
   if (first < last) load(first);
   for (int c = threadIdx.x * 4; c < nc; c += T * 4) {

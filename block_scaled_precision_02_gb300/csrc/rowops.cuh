@@ -8,6 +8,10 @@
 
 namespace mxq {
 
+// The longest row.  Kernels count a row's elements in int and step past its
+// end, by 4096 at most, before they compare.
+constexpr int64_t kMaxCols = 0x7FFF0000;
+
 // VE consecutive elements of T in registers, as loaded (VE * sizeof(T) is 2,
 // 4, 8 or 16 bytes and the address is aligned to it); get() widens one.
 template <typename T, int VE>

@@ -348,7 +348,8 @@ int mxq_mm_fp8(const void* a, const void* b, int64_t batch, int64_t M,
  * rstd = 1 / sqrt(var + eps), y = (x - mean) * rstd * w + b, in float32,
  * rounded once to y's type (RNE).  The products' operands come from such rows.
  * x        [rows][ld] of x_type (MXQ_BF16 | MXQ_F32); only the first cols of a
- *          row are read.  rows >= 0, cols >= 1, ld >= cols, any sizes.
+ *          row are read.  rows >= 0, 1 <= cols <= 2^31 - 65536 (as in the
+ *          calls below), ld >= cols.
  * w, b     [cols] of w_type / b_type, or NULL (1 and 0).
  * y        [rows][cols] of y_type.
  * mean, rstd  float [rows], kept for the backward pass.
@@ -402,7 +403,8 @@ int mxq_layer_norm_backward(const void* dy, int64_t ld_dy, int dy_type,
  * where the first term's slope is -A r while r A <= the clipped product, 0
  * beyond and NaN where the two do not compare (a NaN log-probability, old_logp
  * or advantage shows in loss and grad), and the second's beta (1 - exp(d)).
- * logits   [tokens][ld] of logits_type, only the first vocab of a row read.
+ * logits   [tokens][ld] of logits_type, only the first vocab of a row read;
+ *          vocab <= 2^31 - 65536.
  * targets  int64 (targets_64 == 1) or int32 (0) [tokens].
  * weights  float [tokens].  A token of weight 0 (a prompt token, padding) is
  *          not looked at: its logits, target, old_logp, advantage and
