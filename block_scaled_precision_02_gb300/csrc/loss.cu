@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
       if (t == 0) mbar_arrive_expect_tx(smem_u32(&xbar[par]), slabs * RING_WARPS * 8);
       if (lane < slabs)
         st_async_f2(smem_u32(&pairs[par][rank * RING_WARPS + warp]), smem_u32(&xbar[par]), lane, wm, s);
-      if (alive) alive = mbar_wait_sleep(smem_u32(&xbar[par]), (live >> 1) & 1, status);
+      if (alive) alive = mbar_wait_sleep<true>(smem_u32(&xbar[par]), (live >> 1) & 1, status);
       ++live;
       float top = kLowest;
       for (int i = lane; i < slabs * RING_WARPS; i += 32) top = fmaxf(top, pairs[par][i].x);

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
     float mean, rstd;                                    // of row lr of this warp
     if constexpr (CLUSTER) {
       const int buf = (tile - first) & 1;
-      if (alive) alive = mbar_wait_sleep(smem_u32(&bar[buf]), ((tile - first) >> 1) & 1, status);
+      if (alive) alive = mbar_wait_sleep<true>(smem_u32(&bar[buf]), ((tile - first) >> 1) & 1, status);
       const float2 p = lk < slabs ? parts[buf][lk][warp * RW + lr] : make_float2(0.f, 0.f);
       mean = group_sum(p.x) * inv_c;
       const float d = lk < slabs ? p.x / n_k - mean : 0.f;

@@ -147,11 +147,16 @@ __device__ __forceinline__ void st_async_f2(uint32_t addr, uint32_t bar, uint32_
 }
 
 // Bounded wait for phases that take microseconds: the thread sleeps in the
-// barrier unit instead of polling.
+// barrier unit instead of polling.  PEERS: other CTAs of the cluster complete
+// the phase by stores of theirs, so the acquire is at cluster scope.
+template <bool PEERS = false>
 __device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, int* status) {
-  if (mbar_try_wait_sleep(bar, parity, 2000u)) return true;
+  const auto done = [&](uint32_t hint_ns) {
+    return PEERS ? mbar_try_wait_cl_sleep(bar, parity, hint_ns) : mbar_try_wait_sleep(bar, parity, hint_ns);
+  };
+  if (done(2000u)) return true;
   const unsigned long long t0 = globaltimer_ns();
-  while (!mbar_try_wait_sleep(bar, parity, 20000u))
+  while (!done(20000u))
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       record_timeout(status);
       return false;
