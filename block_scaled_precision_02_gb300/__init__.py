@@ -755,6 +755,17 @@ def _grad_types(ts, what: str):
     return array.array("q", [_TYPE[d] for d in dtypes]), contiguous
 
 
+def _check_writes(read, written, sizes, what: str) -> None:
+    """No address is written for two tensors, or for one and read for another
+    (empty tensors aside)."""
+    first, reader = {}, {p: k for k, (p, n) in enumerate(zip(read, sizes)) if n}
+    for k, (p, n) in enumerate(zip(written, sizes)):
+        if n and first.setdefault(p, k) != k:
+            raise ValueError(f"{what}[{k}] and {what}[{first[p]}] share memory")
+        if n and reader.get(p, k) != k and what == "out":
+            raise ValueError(f"{what}[{k}] and grads[{reader[p]}] share memory")
+
+
 def _grad_call(name: str, grads, out, *args) -> torch.Tensor:
     """Check the lists and run entry point ``name`` on them: one mxq_grad per
     tensor, written as four 64-bit words.  Attributes are fetched list by
@@ -780,14 +791,18 @@ def _grad_call(name: str, grads, out, *args) -> torch.Tensor:
                 if o.numel() != g.numel() or not (g.is_contiguous() and o.is_contiguous()) and (
                         o.shape != g.shape or o.stride() != g.stride()):
                     raise ValueError(f"out[{k}] must have the shape and strides of grads[{k}]")
+    read = list(map(torch.Tensor.data_ptr, grads))
+    written = read if out is None else list(map(torch.Tensor.data_ptr, outs))
+    if args and len(set(read + written)) < (n if out is None else 2 * n):
+        _check_writes(read, written, sizes, "grads" if out is None else "out")
     dev, index = grads[0].device, grads[0].get_device()
     for ts, what in ((grads, "grads"),) if out is None else ((grads, "grads"), (outs, "out")):
         if index < 0 or set(map(torch.Tensor.get_device, ts)) != {index}:
             for k, t in enumerate(ts):
                 _on_device(((t, f"{what}[{k}]"),), dev)
     words = array.array("q", bytes(32 * n))
-    words[0::4] = pointers = array.array("q", map(torch.Tensor.data_ptr, grads))
-    words[1::4] = pointers if out is None else array.array("q", map(torch.Tensor.data_ptr, outs))
+    words[0::4] = pointers = array.array("q", read)
+    words[1::4] = pointers if out is None else array.array("q", written)
     words[2::4] = sizes
     words[3::4] = array.array("q", [g | o << 32 for g, o in zip(types, out_types)])
     norm = torch.empty(1, dtype=torch.float32, device=dev)
@@ -808,7 +823,9 @@ def clip_grad_norm(grads, max_norm: float, out=None) -> torch.Tensor:
     global 2-norm, which is returned (1-element float32, nothing is read back
     to the host).  In place, or into the tensors of ``out`` (bf16 or float32,
     of as many elements each, e.g. stretches of an optimizer's float32 buffer;
-    a gradient that is not contiguous needs one of its own strides)."""
+    a gradient that is not contiguous needs one of its own strides).  What is
+    written must overlap neither another output nor another gradient: a
+    gradient that is in the list twice cannot be clipped in place."""
     if not max_norm >= 0:
         raise ValueError("max_norm must not be negative")
     return _grad_call("mxq_clip_grad_norm", grads, out, max_norm)

@@ -435,7 +435,8 @@ int mxq_policy_loss(const void* logits, int64_t tokens, int64_t vocab,
  * grads    host array (read during the call only), one entry per tensor of n
  *          elements in a row; n == 0 is allowed.  mxq_grad_norm reads g only;
  *          for mxq_clip_grad_norm out may be g itself (the same type) or
- *          another buffer that overlaps no tensor.
+ *          another buffer that overlaps no tensor and no other output; g that
+ *          is in the list twice cannot be its own output.
  * norm     one float.  Values whose squares overflow or vanish in float32
  *          are squared in float64; a NaN or infinite element shows in norm
  *          (NaN or inf), and the factor is then NaN or 0 as the formula says.
