@@ -526,7 +526,8 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
       const float wm = warp_max(m);
       s = warp_sum(s * ex2((m - wm) * kLog2e));
       const int par = live & 1;
-      if (t == 0) mbar_arrive_expect_tx(smem_u32(&xbar[par]), slabs * RING_WARPS * 8);
+      // (once a wait has given up, its phase may still be open: no second arrival)
+      if (t == 0 && alive) mbar_arrive_expect_tx(smem_u32(&xbar[par]), slabs * RING_WARPS * 8);
       if (lane < slabs)
         st_async_f2(smem_u32(&pairs[par][rank * RING_WARPS + warp]), smem_u32(&xbar[par]), lane, wm, s);
       if (alive) alive = mbar_wait_sleep<true>(smem_u32(&xbar[par]), (live >> 1) & 1, status);
@@ -587,7 +588,8 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
       }
     }
   }
-  cluster_sync();                                            // no peer writes here any more
+  cluster_sync();                                            // no peer writes here any more,
+  if (!alive) linger();                                      // unless a wait gave up
 }
 
 using namespace mxq_host;

@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
   // the slab's part of the statistics of the rows in registers, to every CTA
   const auto send_stats = [&](int tile) {
     const int buf = (tile - first) & 1;
-    if (threadIdx.x == 0) mbar_arrive_expect_tx(smem_u32(&bar[buf]), 256 * slabs);
+    // (once a wait has given up, its phase may still be open: no second arrival)
+    if (threadIdx.x == 0 && alive) mbar_arrive_expect_tx(smem_u32(&bar[buf]), 256 * slabs);
     float s[RW];
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
@@ -277,7 +278,10 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) norm_tile_kernel(const No
   }
   // peers may still be sending: they wait for this CTA's sums, it for theirs,
   // so nothing is on its way once every tile is merged -- unless a wait gave up
-  if constexpr (CLUSTER) cluster_sync();
+  if constexpr (CLUSTER) {
+    cluster_sync();
+    if (!alive) linger();
+  }
 }
 
 // ---------------------------------------------------------------- host

@@ -164,6 +164,14 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, i
   return true;
 }
 
+// After a wait for peers' stores has given up, and the cluster's last barrier:
+// what was sent to this CTA's shared memory lands within microseconds, and
+// the CTA stays for a hundred.
+__device__ __forceinline__ void linger() {
+  const unsigned long long t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 100000ull) __nanosleep(1000);
+}
+
 // Scale byte of an MX block whose largest magnitude has the bits `ab`, and the
 // multiplier 2^-e of its elements; a block that holds NaN or an infinity gets
 // 0xFF (and zero codes: `bad` of mx_codes).
