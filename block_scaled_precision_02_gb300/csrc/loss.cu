@@ -153,6 +153,7 @@ __device__ __forceinline__ void token_loss(const LossArgs& a, const TokenIn& t, 
 __global__ void __launch_bounds__(1024) loss_sum_kernel(const LossArgs a) {
   __shared__ double sums[32];
   grid_dep_wait();
+  grid_dep_launch();
   float hi = 0.f, lo = 0.f;
 #pragma unroll 8
   for (int i = threadIdx.x; i < a.tokens; i += blockDim.x) {
