@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const BwdArgs a, int G) 
 // to dx.  More (KEEP false): the slot is read again for dx and given
 // back after the next row's barrier, and the weights are read from shared
 // memory, because the column sums fill the registers.
+static_assert(BWD_THREADS <= 512, "half a warp adds the warps' sums of a row");
 template <typename TX, typename TD, int VE, int NV, bool FULL>
 __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const BwdArgs a, int G, int stages, int* status) {
   constexpr bool KEEP = VE * NV <= BWD_KEEP;
@@ -302,9 +303,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) norm_bwd_ring_kernel(const Bwd
       }
     }
     if (wpg > 1) {
-      const float* half = red[buf][lane >> 4] + g * wpg + (lane & 15);
-      v = (lane & 15) < wpg ? half[0] : 0.f;
-      if (wpg > 16) v += (lane & 15) + 16 < wpg ? half[16] : 0.f;
+      v = (lane & 15) < wpg ? red[buf][lane >> 4][g * wpg + (lane & 15)] : 0.f;
 #pragma unroll
       for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
       buf ^= 1;
