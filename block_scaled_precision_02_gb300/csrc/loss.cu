@@ -595,10 +595,6 @@ __global__ void __launch_bounds__(RING_TPB + 32, 2) policy_ring_kernel(const Los
 
 using namespace mxq_host;
 
-bool valid_type(int t) { return t == MXQ_BF16 || t == MXQ_F32; }
-int type_size(int t) { return t == MXQ_F32 ? 4 : 2; }
-bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 template <typename TZ, typename TG, int VE, int NV, bool LONG, int TPB, bool CLUSTER>
 int launch_policy(const LossArgs& a, int slabs, cudaStream_t st) {
   const int64_t grid = TPB == 32 ? (static_cast<int64_t>(a.tokens) + 7) / 8 : static_cast<int64_t>(a.tokens) * slabs;

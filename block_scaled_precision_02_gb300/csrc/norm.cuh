@@ -284,9 +284,6 @@ using namespace mxq_host;
 
 constexpr int kMaxRowElems = 32768;       // forward: one CTA's registers
 
-inline bool valid_type(int t) { return t == MXQ_BF16 || t == MXQ_F32; }
-inline int type_size(int t) { return t == MXQ_F32 ? 4 : 2; }
-inline bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
 template <typename TX, int OUT, int VE, int NV>

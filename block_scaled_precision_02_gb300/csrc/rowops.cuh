@@ -220,4 +220,9 @@ __device__ __forceinline__ int64_t scale_at(int64_t row, int64_t k, int64_t kb, 
   return ((row >> 7) * (kb >> 2) + (k >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (k & 3);
 }
 
+// ---------------------------------------------------------------- host: checks of arguments
+inline bool valid_type(int t) { return t == MXQ_BF16 || t == MXQ_F32; }
+inline int type_size(int t) { return t == MXQ_F32 ? 4 : 2; }
+inline bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
 }  // namespace mxq
