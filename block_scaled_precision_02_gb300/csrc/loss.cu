@@ -143,9 +143,10 @@ __device__ __forceinline__ void token_loss(const LossArgs& a, const TokenIn& t, 
 }
 
 // The loss: the tokens' terms, added by one CTA that follows the rows'
-// kernels (it starts early and waits, so it adds little to them).  A ticket
-// that lets the last row's CTA do it would have to be zero beforehand, in
-// memory that outlives the call or by a launch before it.  A thread adds its
+// kernels.  It starts early and waits for them: 5 x 32001 takes 4.9 us in a
+// graph, 6.4 with the sum in the last row's CTA and 10.2 with a fill of that
+// CTA's ticket before each call (a ticket kept at zero would have to outlive
+// the call).  A thread adds its
 // own terms in their order as an unevaluated pair (the rounding error of each float32 addition is exactly
 // (a - (s - v)) + (b - v) with s = a + b, v = s - a, and is kept apart), the
 // threads' sums go up a fixed tree in float64.  All-float64 additions at two
@@ -347,7 +348,8 @@ __global__ void __launch_bounds__(TPB == 32 ? 256 : TPB, policy_ctas<VE, NV, TPB
 // computes while the other waits.  Two exponentials per element instead of
 // one, but no data held in registers.  Eight warps to a CTA: with sixteen the
 // waits and branches of each chunk weigh twice as much (2048 x 131072 bf16, no
-// token masked: 229 us against 189, 84 % of the measured copy rate).
+// token masked: 229 us against 189 when that was chosen; 181 us since, 88 % of
+// the measured copy rate).
 constexpr int RING_CHUNK = 16384, RING_SLOTS = 6, RING_AHEAD = 2;
 constexpr int RING_TPB = 256, RING_WARPS = RING_TPB / 32;
 constexpr float kLowest = -3.402823466e38f;
@@ -647,9 +649,10 @@ int64_t row_words(const LossArgs& a) {
 // The ring kernel takes rows beyond the register kernels' (float32), or their
 // last step of 12288 to 16384 elements and on (bf16), when every CTA gets two
 // tokens or more, in the smallest cluster whose CTAs keep RING_AHEAD chunks of
-// the ring for the next token.  Here against in registers, us: bf16 16384 x
-// 12000 220 and 177, 8192 x 16384 121 and 131; float32 8192 x 12001 137 and 99,
-// 4096 x 16384 100 and 86.  0: not for it.
+// the ring for the next token.  Here against in registers, no token masked, us:
+// bf16 16384 x 12000 205 and 178, 8192 x 12296 110 and 120, 8192 x 16384 115 and
+// 131; float32 8192 x 12001 144 and 122 (bf16 gradient 132 and 101), 4096 x 16384
+// 100 and 87, 4096 x 16392 108 and 168.  0: not for it.
 template <typename TZ>
 int ring_slabs(const LossArgs& a) {
   if (a.vocab <= (sizeof(TZ) == 2 ? 12288 : 16384)) return 0;
