@@ -146,11 +146,11 @@ __device__ __forceinline__ void token_loss(const LossArgs& a, const TokenIn& t, 
 // kernels.  It starts early and waits for them: 5 x 32001 takes 4.9 us in a
 // graph, 6.4 with the sum in the last row's CTA and 10.2 with a fill of that
 // CTA's ticket before each call (a ticket kept at zero would have to outlive
-// the call).  A thread adds its
-// own terms in their order as an unevaluated pair (the rounding error of each float32 addition is exactly
-// (a - (s - v)) + (b - v) with s = a + b, v = s - a, and is kept apart), the
-// threads' sums go up a fixed tree in float64.  All-float64 additions at two
-// lanes a cycle took longer than the loads.
+// the call).  A thread adds its own terms in their order as an unevaluated pair
+// (the rounding error of each float32 addition is exactly (a - (s - v)) +
+// (b - v) with s = a + b, v = s - a, and is kept apart), the threads' sums go
+// up a fixed tree in float64.  All-float64 additions at two lanes a cycle took
+// longer than the loads.
 __global__ void __launch_bounds__(1024) loss_sum_kernel(const LossArgs a) {
   __shared__ double sums[32];
   grid_dep_wait();
