@@ -10,7 +10,10 @@ Entry points (same names as the C ABI):
   mx_gemm_mx_out, mm_fp8, sf_to_mma, last_device_status; plus ``quantize`` / ``quantize_dual`` with the
   argument order of AstrAI's fp8 adapter (astrai/extension/ops/fp8.py).
 Around the products of a training step: layer_norm, mx_layer_norm,
-  layer_norm_backward, policy_loss, grad_norm, clip_grad_norm.
+  layer_norm_backward, policy_loss, grad_norm, clip_grad_norm, dropout.
+Of a mixture-of-experts layer (experts.py): expert_sort, expert_gather,
+  mx_expert_gather, mx_expert_gemm, mx_expert_wgrad, expert_combine,
+  expert_combine_backward.
 """
 
 from __future__ import annotations
@@ -107,6 +110,16 @@ def load() -> ctypes.CDLL:
     L.mxq_grad_norm_workspace_size.argtypes = [i32, vp]
     L.mxq_grad_norm.argtypes = [vp, i32, vp, vp, ctypes.c_size_t, vp]
     L.mxq_clip_grad_norm.argtypes = [vp, i32, f32, vp, vp, ctypes.c_size_t, vp]
+    L.mxq_expert_rows.argtypes = [i64, i32, i32, vp]
+    L.mxq_expert_sort_workspace_size.argtypes = [i64, i32, vp]
+    L.mxq_expert_sort.argtypes = [vp, i32, i64, i32, i32, i64, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    L.mxq_expert_gather.argtypes = [vp, i64, i64, i64, i32, vp, i64, vp, i64, vp, vp]
+    L.mxq_expert_gather_mx.argtypes = [vp, i64, i64, i64, vp, i64, i64, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+    L.mxq_expert_gemm.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, i32, i32, vp, vp, i32, vp, i32, vp]
+    L.mxq_expert_wgrad.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, i32, i32, vp, vp, i32, vp]
+    L.mxq_expert_combine.argtypes = [vp, i64, i64, i64, i32, vp, i64, i64, vp, i32, vp, i32, vp]
+    L.mxq_expert_combine_backward.argtypes = [vp, i64, i32, vp, i64, i32, i64, i64, vp, vp, i64, i64, vp, i32, vp, vp, vp]
+    L.mxq_dropout.argtypes = [vp, i64, i64, i64, i32, vp, i64, ctypes.c_double, u64, u64, vp, vp, vp]
     L.mxq_sf_to_mma.argtypes = [vp, i64, i64, vp, vp]
     L.mxq_last_device_status.argtypes = [vp]
     L.mxq_strerror.argtypes = [i32]
@@ -118,7 +131,9 @@ def load() -> ctypes.CDLL:
                  "mxq_gemm_mx_out", "mxq_mm_fp8", "mxq_layer_norm", "mxq_layer_norm_mx",
                  "mxq_layer_norm_backward_workspace_size", "mxq_layer_norm_backward",
                  "mxq_policy_loss_workspace_size", "mxq_policy_loss", "mxq_grad_norm_workspace_size",
-                 "mxq_grad_norm", "mxq_clip_grad_norm", "mxq_sf_to_mma",
+                 "mxq_grad_norm", "mxq_clip_grad_norm", "mxq_expert_rows", "mxq_expert_sort_workspace_size",
+                 "mxq_expert_sort", "mxq_expert_gather", "mxq_expert_gather_mx", "mxq_expert_gemm", "mxq_expert_wgrad",
+                 "mxq_expert_combine", "mxq_expert_combine_backward", "mxq_dropout", "mxq_sf_to_mma",
                  "mxq_last_device_status", "mxq_version", "mxq_test_stall_next_launch"):
         getattr(L, name).restype = i32
     _lib = L
@@ -831,6 +846,40 @@ def clip_grad_norm(grads, max_norm: float, out=None) -> torch.Tensor:
     return _grad_call("mxq_clip_grad_norm", grads, out, max_norm)
 
 
+def dropout(x: torch.Tensor, p: float, seed: int, offset=0, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Dropout of ``x`` [rows][cols] (bf16 or float32, row stride may exceed
+    cols) with probability ``p`` in [0, 1), what is kept divided by 1 - p, plus
+    ``residual`` (x's shape and type) if given.  The mask is not stored: it
+    follows from ``seed``, ``offset`` and the element's index (mxq_dropout has
+    the formula), so the backward pass is dropout(dy, p, seed, offset), and the
+    residual's gradient is dy.
+
+    A call uses (rows * cols + 3) // 4 counters from ``offset`` on; calls under
+    one seed draw independently where their counters do not meet.  ``offset``
+    may be an int64 CUDA tensor of one element: a recorded graph that advances
+    it draws anew in every replay."""
+    xt, rows, cols, ld = _matrix(x, "x")
+    rp = ld_res = 0
+    if residual is not None:
+        rt, _, _, ld_res = _matrix(residual, "residual")
+        if rt != xt or residual.shape != x.shape:
+            raise ValueError("residual must have x's shape and type")
+        rp = residual.data_ptr()
+    if not 0.0 <= p < 1.0:
+        raise ValueError("p must lie in [0, 1)")
+    off_dev = None
+    op = 0
+    if isinstance(offset, torch.Tensor):
+        if offset.dtype != torch.int64 or offset.numel() != 1:
+            raise ValueError("offset must be an integer or an int64 tensor of one element")
+        off_dev, offset, op = offset, 0, offset.data_ptr()
+    dev = _same_device("x residual offset", x, residual, off_dev)
+    y = torch.empty(rows, cols, dtype=x.dtype, device=dev)
+    _launch("mxq_dropout", dev, x.data_ptr(), rows, cols, ld, xt, rp, ld_res, p, seed & (2**64 - 1),
+            offset & (2**64 - 1), op, y.data_ptr())
+    return y
+
+
 def sf_to_mma(s: torch.Tensor) -> torch.Tensor:
     """Canonical scales [rows][kb] -> the GEMM's 512-byte-chunk layout (flat)."""
     if not isinstance(s, torch.Tensor) or s.dim() != 2:
@@ -848,3 +897,7 @@ def last_device_status(device=None) -> int:
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(dev):
         return load().mxq_last_device_status(_stream(dev))
+
+
+from .experts import (ExpertPlan, expert_combine, expert_combine_backward, expert_gather, expert_sort,  # noqa: E402,F401
+                      mx_expert_gather, mx_expert_gemm, mx_expert_wgrad)

@@ -33,6 +33,12 @@ struct Vec {
       w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
   }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (BYTES == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (BYTES == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (BYTES == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
+    else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+  }
   __device__ __forceinline__ void fill(uint32_t word) {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i] = word;
@@ -67,6 +73,19 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VE]) {
     else
       *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]),
                                                 bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+  }
+}
+
+// VE consecutive elements, widened (8 of float32 as two 16-byte loads).
+template <typename T, int VE>
+__device__ __forceinline__ void load_elems(const T* p, float (&out)[VE]) {
+  constexpr int N = VE * static_cast<int>(sizeof(T)) > 16 ? VE / 2 : VE;
+#pragma unroll
+  for (int k = 0; k < VE; k += N) {
+    Vec<T, N> t;
+    t.load(p + k);
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[k + i] = t.get(i);
   }
 }
 

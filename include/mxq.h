@@ -98,7 +98,7 @@ extern "C" {
 #define MXQ_SF_CANONICAL 0
 #define MXQ_SF_MMA       1
 /* Element types of the training-step operators (layer norm, policy loss,
- * gradient clipping). */
+ * gradient clipping, experts, dropout). */
 #define MXQ_BF16 0
 #define MXQ_F32  1
 
@@ -456,6 +456,133 @@ int mxq_grad_norm(const mxq_grad* grads, int ntensors, float* norm,
 int mxq_clip_grad_norm(const mxq_grad* grads, int ntensors, float max_norm,
                        float* norm, void* workspace, size_t workspace_bytes,
                        void* stream);
+
+/* ---- tokens sorted by expert -----------------------------------------------------
+ * A routing gives every token `top` experts: slot s = token * top + j.  The
+ * plan gives every slot of a valid expert a row: the rows of an expert are one
+ * stretch that starts at a multiple of `align`, its slots in their order first,
+ * padding after them.
+ * experts  int32 (experts_64 == 0) or int64 (1) [slots]; a value outside
+ *          [0, num_experts) drops the slot (a full expert, a padding token).
+ * num_experts  1 .. 1024;  align  128 | 256 (the products' tiles).
+ * rows     what mxq_expert_rows gives: rows enough for any routing, a multiple
+ *          of align, known without reading the device.
+ * offsets  int32 [num_experts + 1]: first row of each stretch; the last entry
+ *          is the end of the last stretch (<= rows).
+ * counts   int32 [num_experts]: slots of each expert.
+ * slot_row int32 [slots]: the slot's row, -1 where it is dropped.
+ * row_slot int32 [rows]: the row's slot, -1 in padding and behind the last stretch.
+ * block_expert  int32 [rows / align]: expert of each block of align rows, -1
+ *          behind the last stretch.
+ * workspace  mxq_expert_sort_workspace_size bytes, 16-byte aligned, any contents.
+ * The order depends on the slots alone.  The calls below bound every index
+ * that they read from a plan: a wrong plan gives wrong numbers, no more. */
+int mxq_expert_rows(int64_t slots, int num_experts, int align, int64_t* rows);
+int mxq_expert_sort_workspace_size(int64_t slots, int num_experts, size_t* bytes);
+int mxq_expert_sort(const void* experts, int experts_64, int64_t slots,
+                    int num_experts, int align, int64_t rows,
+                    int32_t* offsets, int32_t* counts, int32_t* slot_row,
+                    int32_t* row_slot, int32_t* block_expert, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* ---- gather by expert --------------------------------------------------------------
+ * out[r] = x[row_slot[r] / top], 0 where row_slot[r] is -1: every row is
+ * written.  Its backward pass is mxq_expert_combine without weights.
+ * x        [tokens][ld] of x_type, the first cols of a row read; out
+ *          [rows][cols] of the same type, bit for bit (16-byte aligned rows of
+ *          a multiple of 16 bytes run faster).
+ * slot_row, row_slot, top, rows  of the plan (slots = tokens * top). */
+int mxq_expert_gather(const void* x, int64_t tokens, int64_t cols, int64_t ld,
+                      int x_type, const int32_t* slot_row, int64_t top,
+                      const int32_t* row_slot, int64_t rows, void* out,
+                      void* stream);
+
+/* ---- gather by expert straight to MX ([FAF]) ----------------------------------------
+ * Bit for bit what mxq_quantize (RNE, no Hadamard) writes for the gathered
+ * rows, which are not written themselves.
+ * x        bf16 [tokens][ld], 16-byte aligned, ld % 8 == 0; tokens >= 1 if rows.
+ * rows     a multiple of 128; cols a multiple of 32 (128 for MXQ_SF_MMA).
+ * fmt .. s_col  as mxq_quantize. */
+int mxq_expert_gather_mx(const void* x, int64_t tokens, int64_t cols, int64_t ld,
+                         const int32_t* row_slot, int64_t rows, int64_t top,
+                         int fmt, int orient, int scale_mode, int sf_layout,
+                         void* q_row, uint8_t* s_row, void* q_col,
+                         uint8_t* s_col, void* stream);
+
+/* ---- block-scaled products of all experts ([MX] section 1) --------------------------
+ * C[r][n] = sum_k A[r][k] B[e][n][k] for every row r of expert e's stretch
+ * (padding rows too), 0 behind the last stretch: every element is written.
+ * A, a_s   [rows][K] codes and MXQ_SF_MMA scales.
+ * B, b_s   b_along_k == 0: [experts * N][K], the experts' weights stacked;
+ *          1: [N][experts * K], the experts along the contraction: the column
+ *          copy that mxq_quantize makes of stacked weights, which the backward
+ *          pass multiplies with.
+ * formats, alignment as mxq_gemm_mixed; N, K multiples of 128 (K of 256 where
+ * both are E2M1).  align 256 with N % 256 == 0 runs on pairs of SMs.
+ * rows, experts, align, offsets, block_expert  of the plan; rows == 0 is MXQ_OK.
+ * c        [rows][N] bf16 or float32, 16-byte aligned. */
+int mxq_expert_gemm(const void* a_q, const uint8_t* a_s, int a_fmt,
+                    const void* b_q, const uint8_t* b_s, int b_fmt,
+                    int64_t rows, int64_t N, int64_t K, int experts, int align,
+                    const int32_t* offsets, const int32_t* block_expert,
+                    int b_along_k, void* c, int out_fp32, void* stream);
+
+/* ---- gradient of the experts' weights -------------------------------------------------
+ * C[e][n][k] = sum over the rows r of expert e's stretch of A[n][r] B[k][r]
+ * (0 for an expert without rows): A [N][rows] and B [K][rows] are column
+ * copies of the gradients and of the activations, whose padding rows are zero.
+ * formats, alignment as above (both E2M1: align == 256); rows == 0 gives zeros.
+ * c        [experts][N][K] bf16 or float32, 16-byte aligned. */
+int mxq_expert_wgrad(const void* a_q, const uint8_t* a_s, int a_fmt,
+                     const void* b_q, const uint8_t* b_s, int b_fmt,
+                     int64_t rows, int64_t N, int64_t K, int experts, int align,
+                     const int32_t* offsets, void* c, int out_fp32,
+                     void* stream);
+
+/* ---- back from the experts ------------------------------------------------------------
+ * y[t] = sum over j of w[t][j] rows_in[slot_row[t top + j]], added in float32 in
+ * the order of j, rounded once to y's type; dropped slots add nothing (their
+ * weights are not looked at), a token with none left gets 0.
+ * rows_in  [rows][ld] of type.   weights  [tokens][top] of w_type, or NULL (1).
+ * y        [tokens][cols] of y_type; must not overlap rows_in. */
+int mxq_expert_combine(const void* rows_in, int64_t rows, int64_t cols,
+                       int64_t ld, int type, const int32_t* slot_row,
+                       int64_t tokens, int64_t top, const void* weights,
+                       int w_type, void* y, int y_type, void* stream);
+
+/* Its gradients:
+ *   drows[slot_row[s]] = w[s] dy[t], rounded once, 0 where row_slot is -1
+ *   dweights[s] = sum over c of dy[t][c] rows_in[slot_row[s]][c] in float32, 0
+ *                 for a dropped slot
+ * dy       [tokens][ld_dy] of dy_type; drows [rows][cols] of type; must overlap
+ *          neither dy nor rows_in.  dweights float [tokens][top].
+ * Sums in a fixed order. */
+int mxq_expert_combine_backward(const void* dy, int64_t ld_dy, int dy_type,
+                                const void* rows_in, int64_t ld, int type,
+                                int64_t rows, int64_t cols,
+                                const int32_t* slot_row,
+                                const int32_t* row_slot, int64_t tokens,
+                                int64_t top, const void* weights, int w_type,
+                                void* drows, float* dweights, void* stream);
+
+/* ---- dropout ------------------------------------------------------------------------------
+ * y[i] = residual[i] + [u_i >= t] x[i] / (1 - p), t = p 2^32 to the nearest
+ * integer (2^32 - 1 at most), u_i word i & 3 of Philox-4x32-10(key = seed, counter
+ * = (c, c >> 32, 0, 0)), c = offset + (i >> 2), i = r cols + c the element's index:
+ * the draws of MXQ_SR4.  No mask is stored: the backward pass is the same call
+ * on dy without residual.  float32 arithmetic, one rounding; what is dropped is
+ * not looked at.
+ * x        [rows][ld] of type; residual NULL or [rows][ld_residual] of type;
+ *          y [rows][cols] of type, which may be x or residual where that has no
+ *          gaps between its rows, and overlaps neither otherwise.
+ * p        0 <= p < 1.
+ * offset_dev  NULL, or a device integer that is added to offset: a recorded
+ *          graph that advances it draws anew in every replay.
+ * A call uses the counters offset .. offset + (rows cols - 1) / 4. */
+int mxq_dropout(const void* x, int64_t rows, int64_t cols, int64_t ld, int type,
+                const void* residual, int64_t ld_residual, double p,
+                uint64_t seed, uint64_t offset, const int64_t* offset_dev,
+                void* y, void* stream);
 
 /* ---- scale layout conversion ([FAF]) -----------------------------------------
  * Canonical scales s [rows][kb] -> MMA layout (rows % 128 == 0,

@@ -1,0 +1,269 @@
+"""Tokens sorted by expert, gathered (plain and to MX), and combined again, with
+gradients, against plain 64-bit forms."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.expert_reference import plan_of, routing
+from tests.rounding import half_ulp
+
+pytestmark = pytest.mark.gpu
+
+dev = torch.device("cuda")
+BF, F32 = torch.bfloat16, torch.float32
+PATTERNS = ["even", "skewed", "one", "none", "dropped"]
+
+
+def make_plan(lib, rng, tokens, top, experts, pattern="even", align=128, dtype=torch.int32):
+    e = routing(rng, tokens, top, experts, pattern)
+    return lib.expert_sort(torch.from_numpy(e).to(dtype).to(dev), experts, align), plan_of(e, experts, align)
+
+
+def np64(t):
+    return t.double().cpu().numpy()
+
+
+# ------------------------------------------------------------------ sort
+@pytest.mark.parametrize("pattern", PATTERNS)
+@pytest.mark.parametrize("tokens,top,experts", [(1, 1, 1), (1, 8, 64), (3, 2, 7), (100, 3, 5), (515, 2, 16), (2048, 1, 1024),
+                                                (2049, 1, 2), (4097, 5, 33), (5000, 8, 1000), (300000, 1, 128)])
+def test_sort(lib, tokens, top, experts, pattern):
+    rng = np.random.default_rng(tokens + experts)
+    for align, dtype in ((128, torch.int32), (256, torch.int64)):
+        got, want = make_plan(lib, rng, tokens, top, experts, pattern, align, dtype)
+        for t, w, name in zip(got[:5], (want[0], want[1], want[2], want[3], want[4]), got._fields):
+            assert t.dtype == torch.int32 and np.array_equal(t.cpu().numpy(), w), name
+        assert got.rows == len(want[3]) and got[5:] == (tokens, top, experts, got.rows, align)
+
+
+def test_sort_of_values_beyond_32_bits(lib):
+    e = torch.tensor([[1, 1 + 2 ** 32], [2 ** 63 - 1, -(2 ** 63)], [2 ** 33, 0]], device=dev)
+    p = lib.expert_sort(e, 4)
+    assert p.slot_row.tolist() == [[128, -1], [-1, -1], [-1, 0]]
+    assert p.counts.tolist() == [1, 1, 0, 0] and p.offsets.tolist() == [0, 128, 256, 256, 256]
+
+
+def test_sort_of_no_tokens(lib):
+    p = lib.expert_sort(torch.empty(0, 2, dtype=torch.int32, device=dev), 5)
+    assert p.rows == 0 and p.offsets.tolist() == [0] * 6 and p.counts.tolist() == [0] * 5
+    assert lib.expert_gather(torch.empty(0, 64, device=dev), p).shape == (0, 64)
+    assert [None if t is None else t.numel() for t in lib.mx_expert_gather(torch.empty(0, 64, dtype=BF, device=dev), p)] == \
+        [0, 0, None, None]
+    assert lib.expert_combine(torch.empty(0, 64, device=dev), p).shape == (0, 64)
+    d, w = lib.expert_combine_backward(torch.empty(0, 64, device=dev), torch.empty(0, 64, device=dev), p,
+                                       torch.empty(0, 2, device=dev))
+    assert d.shape == (0, 64) and w.shape == (0, 2)
+
+
+# ------------------------------------------------------------------ gather
+@pytest.mark.parametrize("pattern", ["even", "dropped", "none"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tokens,top,experts,cols", [(1, 1, 1, 1), (1, 8, 64, 4096), (5, 2, 3, 7), (33, 3, 5, 1021),
+                                                     (130, 2, 4, 1024), (257, 1, 300, 520), (70, 4, 8, 5000)])
+def test_gather(lib, tokens, top, experts, cols, dtype, pattern):
+    rng = np.random.default_rng(cols)
+    p, want = make_plan(lib, rng, tokens, top, experts, pattern)
+    bits = torch.int16 if dtype == BF else torch.int32
+    info = torch.iinfo(bits)
+    # any bit patterns, NaN payloads among them
+    x = torch.from_numpy(rng.integers(info.min, info.max, size=(tokens, cols), dtype=np.int64)).to(bits).to(dev)
+    got = lib.expert_gather(x.view(dtype), p).view(bits).cpu().numpy()
+    row = want[3]
+    ref = np.where((row >= 0)[:, None], x.cpu().numpy()[np.maximum(row, 0) // top], 0)
+    assert np.array_equal(got, ref)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shift,pad", [(0, 8), (1, 0), (1, 3), (8, 1)])
+def test_gather_of_strided_rows(lib, dtype, shift, pad):
+    rng = np.random.default_rng(3)
+    p, want = make_plan(lib, rng, 40, 2, 6, "dropped")
+    store = torch.randn(40 * (512 + pad) + shift, device=dev).to(dtype)
+    x = store[shift:].view(40, 512 + pad)[:, :512]
+    got = lib.expert_gather(x, p)
+    assert torch.equal(got, lib.expert_gather(x.contiguous(), p))
+    row = want[3]
+    ref = np.where((row >= 0)[:, None], np64(x)[np.maximum(row, 0) // 2], 0)
+    assert np.array_equal(np64(got), ref)
+
+
+# ------------------------------------------------------------------ gather to MX
+def bf16_values(rng, tokens, cols, special=True):
+    x = rng.standard_normal((tokens, cols)) * np.exp2(rng.integers(-12, 12, size=(tokens, 1)))
+    x = torch.from_numpy(x).to(BF)
+    if special:
+        flat = x.view(-1)
+        n = flat.numel()
+        for v in (float("nan"), float("inf"), -float("inf"), -0.0, 0.0, 1e-40, 3e38):
+            flat[torch.from_numpy(rng.integers(0, n, size=max(1, n // 2000)))] = v
+    return x.to(dev)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2", "e2m1"])
+@pytest.mark.parametrize("orientation", ["row", "col", "dual"])
+@pytest.mark.parametrize("scale,layout", [("floor", "canonical"), ("ceil", "mma")])
+@pytest.mark.parametrize("tokens,top,experts,cols,align", [(1, 1, 1, 128, 128), (1, 8, 64, 256, 128), (300, 2, 5, 384, 256),
+                                                           (1000, 3, 16, 640, 128)])
+def test_gather_to_mx(lib, tokens, top, experts, cols, align, scale, layout, orientation, fmt):
+    """Byte for byte the quantizer's output (which the oracle pins) for the gathered rows."""
+    rng = np.random.default_rng(cols + tokens)
+    p, _ = make_plan(lib, rng, tokens, top, experts, "dropped" if tokens > 1 else "even", align)
+    x = bf16_values(rng, tokens, cols)
+    got = lib.mx_expert_gather(x, p, fmt, orientation, scale, layout)
+    want = lib.mx_quantize(lib.expert_gather(x, p), fmt, orientation, scale, sf_layout=layout)
+    for g, w, name in zip(got, want, ("q_row", "s_row", "q_col", "s_col")):
+        assert (g is None) == (w is None) and (g is None or torch.equal(g, w)), name
+
+
+@pytest.mark.parametrize("cols", [32, 96, 160, 224])
+def test_gather_to_mx_of_narrow_and_strided_rows(lib, cols):
+    """Columns that end inside a tile, in rows that are wider than what is read."""
+    rng = np.random.default_rng(cols)
+    p, _ = make_plan(lib, rng, 77, 2, 5, "dropped")
+    wide = bf16_values(rng, 77, cols + 40)
+    x = wide[:, 8:8 + cols]
+    got = lib.mx_expert_gather(x, p, "e4m3", "dual", "floor", "canonical")
+    want = lib.mx_quantize(lib.expert_gather(x, p), "e4m3", "dual", "floor")
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+# ------------------------------------------------------------------ combine
+def inputs(rng, p, cols, dtype, wtype, fill=0.0):
+    """Rows whose padding holds `fill`, and gate weights whose dropped slots hold NaN."""
+    rows = torch.randn(p.rows, cols, generator=torch.Generator().manual_seed(cols)).to(dtype).to(dev)
+    rows[p.row_slot < 0] = fill
+    w = torch.rand(p.tokens, p.top, generator=torch.Generator().manual_seed(1)).to(wtype).to(dev)
+    w[p.slot_row < 0] = float("nan")
+    return rows, w
+
+
+def combine64(rows, w, slot_row):
+    """(sum, sum of magnitudes) in float64."""
+    r = np64(rows)
+    live = slot_row >= 0
+    wv = np.where(live, 1.0 if w is None else np64(w), 0.0)
+    at = np.maximum(slot_row, 0)
+    y = np.zeros((slot_row.shape[0], r.shape[1]))
+    m = np.zeros_like(y)
+    for j in range(slot_row.shape[1]):
+        term = np.where(live[:, j, None], r[at[:, j]], 0.0) * wv[:, j, None]
+        y += term
+        m += np.abs(term)
+    return y, m
+
+
+SHAPES = [(1, 1, 1, 1), (1, 8, 64, 4096), (5, 2, 3, 7), (33, 3, 5, 1021), (130, 2, 4, 1024), (70, 4, 8, 5000), (64, 33, 40, 264)]
+
+
+@pytest.mark.parametrize("pattern", ["even", "dropped", "none", "one"])
+@pytest.mark.parametrize("dtype,out,wtype", [(BF, BF, F32), (BF, F32, BF), (F32, BF, F32), (F32, F32, F32), (BF, BF, None)])
+@pytest.mark.parametrize("tokens,top,experts,cols", SHAPES)
+def test_combine(lib, tokens, top, experts, cols, dtype, out, wtype, pattern):
+    rng = np.random.default_rng(cols)
+    p, want = make_plan(lib, rng, tokens, top, experts, pattern)
+    rows, w = inputs(rng, p, cols, dtype, wtype or F32, float("nan"))
+    w = None if wtype is None else w
+    y = lib.expert_combine(rows, p, w, out)
+    ref, mag = combine64(rows.nan_to_num(0.0), None if w is None else w.nan_to_num(0.0), want[2])
+    # top fused steps in float32, each off by half a step of a partial sum (at most mag), then one rounding
+    tol = top * 2.0 ** -24 * mag * (1 + 1e-5)
+    tol = tol + half_ulp(out, ref, tol)
+    assert y.dtype == out and np.all(np.abs(np64(y) - ref) <= tol)
+    assert np.all(np64(y)[(want[2] < 0).all(1)] == 0)
+
+
+def test_combine_of_strided_and_shifted_rows(lib):
+    rng = np.random.default_rng(5)
+    p, _ = make_plan(lib, rng, 50, 2, 4, "dropped")
+    for dtype in (BF, F32):
+        for shift, pad, cols in ((0, 16, 512), (1, 0, 512), (2, 6, 512), (1, 1, 511)):
+            store = torch.randn(p.rows * (cols + pad) + shift, device=dev).to(dtype)
+            rows = store[shift:].view(p.rows, cols + pad)[:, :cols]
+            w = torch.rand(50, 2, device=dev)
+            assert torch.equal(lib.expert_combine(rows, p, w), lib.expert_combine(rows.contiguous(), p, w))
+            dstore = torch.randn(50 * (cols + pad) + shift, device=dev).to(dtype)
+            dy = dstore[shift:].view(50, cols + pad)[:, :cols]
+            got = lib.expert_combine_backward(dy, rows, p, w)
+            want = lib.expert_combine_backward(dy.contiguous(), rows.contiguous(), p, w)
+            assert torch.equal(got[0], want[0])
+            ref = (np64(dy)[:, None] * np64(rows)[np.maximum(p.slot_row.cpu().numpy(), 0)])
+            live = p.slot_row.cpu().numpy() >= 0
+            tol = cols * 2.0 ** -24 * np.abs(ref).sum(2)
+            assert np.all(np.abs(np64(got[1]) - np.where(live, ref.sum(2), 0)) <= tol)
+
+
+# ------------------------------------------------------------------ combine, backward
+@pytest.mark.parametrize("pattern", ["even", "dropped", "none", "one"])
+@pytest.mark.parametrize("dtype,dytype,wtype", [(BF, BF, F32), (BF, F32, BF), (F32, BF, F32), (F32, F32, F32)])
+@pytest.mark.parametrize("tokens,top,experts,cols", SHAPES)
+def test_combine_backward(lib, tokens, top, experts, cols, dtype, dytype, wtype, pattern):
+    rng = np.random.default_rng(cols)
+    p, want = make_plan(lib, rng, tokens, top, experts, pattern)
+    rows, w = inputs(rng, p, cols, dtype, wtype, float("nan"))
+    dy = torch.randn(tokens, cols, generator=torch.Generator().manual_seed(2)).to(dytype).to(dev)
+    drows, dw = lib.expert_combine_backward(dy, rows, p, w)
+    assert drows.dtype == dtype and dw.dtype == F32
+    live, at = want[2] >= 0, np.maximum(want[2], 0)
+    ref = np.zeros((p.rows, cols))
+    wv = np.where(live, np64(w), 0.0)
+    for j in range(top):
+        ref[at[live[:, j], j]] = (np64(dy) * wv[:, j, None])[live[:, j]]
+    tol = 2.0 ** -24 * np.abs(ref)
+    assert np.all(np.abs(np64(drows) - ref) <= tol + half_ulp(dtype, ref, tol) * (ref != 0))
+    prod = np64(dy)[:, None] * np.where(live[:, :, None], np64(rows)[at], 0.0)
+    # a term passes cols / 256 sums of its thread at most (and 8 within a vector), 5 of its warp, 8 of the CTA; one product
+    steps = cols // 256 + 1 + 8 + 5 + 8 + 1
+    assert np.all(np.abs(np64(dw) - prod.sum(2)) <= steps * 2.0 ** -24 * np.abs(prod).sum(2))
+    assert np.all(np64(dw)[~live] == 0)
+    again = lib.expert_combine_backward(dy, rows, p, w)
+    assert torch.equal(again[0], drows) and torch.equal(again[1], dw)
+
+
+def test_gradients_against_differences(lib):
+    """The sum is linear in the rows and in the weights: a difference over a
+    step h is the gradient up to the float32 rounding of both sums, 4 steps of
+    half an ulp each of a token's magnitude."""
+    rng = np.random.default_rng(11)
+    p, want = make_plan(lib, rng, 20, 3, 4, "dropped")
+    rows, w = inputs(rng, p, 64, F32, F32)
+    w = w.nan_to_num(0.5)
+    g = torch.randn(20, 64, device=dev)
+    drows, dw = lib.expert_combine_backward(g, rows, p, w)
+    loss = lambda r, ww: (np64(lib.expert_combine(r, p, ww)) * np64(g)).sum()
+    _, mag = combine64(rows, w, want[2])
+    noise = 2 * 4 * 2.0 ** -24 * np.abs(np64(g) * (mag + 1)).sum()
+    for _ in range(10):
+        t, j = rng.integers(20), rng.integers(3)
+        h = torch.zeros_like(w)
+        h[t, j] = 0.25
+        assert abs((loss(rows, w + h) - loss(rows, w - h)) / 0.5 - float(dw[t, j])) <= 2 * noise
+        r, c = rng.integers(p.rows), rng.integers(64)
+        h = torch.zeros_like(rows)
+        h[r, c] = 0.25
+        assert abs((loss(rows + h, w) - loss(rows - h, w)) / 0.5 - float(drows[r, c])) <= 2 * noise
+    # the gather's gradient is the combine without weights
+    x = torch.randn(20, 64, device=dev)
+    G = torch.randn(p.rows, 64, device=dev)
+    dx = lib.expert_combine(G, p)
+    for _ in range(10):
+        t, c = rng.integers(20), rng.integers(64)
+        up, down = x.clone(), x.clone()
+        up[t, c], down[t, c] = 1.0, -1.0
+        d = (np64(lib.expert_gather(up, p) - lib.expert_gather(down, p)) * np64(G)).sum() / 2
+        assert abs(d - float(dx[t, c])) <= 3 * 2.0 ** -24 * 3 * np.abs(np64(G)).max()
+
+
+def test_a_wrong_plan_reads_and_writes_within_bounds(lib):
+    """Indices beyond the rows or tokens are passed over (a plan changed by hand)."""
+    rng = np.random.default_rng(6)
+    p, _ = make_plan(lib, rng, 16, 2, 4)
+    bad = p._replace(slot_row=torch.full_like(p.slot_row, 2 ** 31 - 1), row_slot=torch.full_like(p.row_slot, 2 ** 31 - 1))
+    rows = torch.randn(p.rows, 128, device=dev).to(BF)
+    assert not lib.expert_combine(rows, bad).any()
+    _, dw = lib.expert_combine_backward(rows[:16], rows, bad, torch.ones(16, 2, device=dev))
+    assert not dw.any()
+    lib.expert_gather(rows[:16], bad)
+    q = lib.mx_expert_gather(rows[:16], bad, "e4m3", "dual")
+    assert not q[0].any() and not q[2].any()
+    torch.cuda.synchronize()
