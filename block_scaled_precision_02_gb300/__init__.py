@@ -113,12 +113,13 @@ def load() -> ctypes.CDLL:
     L.mxq_expert_rows.argtypes = [i64, i32, i32, vp]
     L.mxq_expert_sort_workspace_size.argtypes = [i64, i32, vp]
     L.mxq_expert_sort.argtypes = [vp, i32, i64, i32, i32, i64, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
-    L.mxq_expert_gather.argtypes = [vp, i64, i64, i64, i32, vp, i64, vp, i64, vp, vp]
+    L.mxq_expert_gather.argtypes = [vp, i64, i64, i64, i32, vp, i64, vp, vp, i32, i64, vp, vp]
     L.mxq_expert_gather_mx.argtypes = [vp, i64, i64, i64, vp, i64, i64, i32, i32, i32, i32, vp, vp, vp, vp, vp]
     L.mxq_expert_gemm.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, i32, i32, vp, vp, i32, vp, i32, vp]
     L.mxq_expert_wgrad.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, i32, i32, vp, vp, i32, vp]
     L.mxq_expert_combine.argtypes = [vp, i64, i64, i64, i32, vp, i64, i64, vp, i32, vp, i32, vp]
-    L.mxq_expert_combine_backward.argtypes = [vp, i64, i32, vp, i64, i32, i64, i64, vp, vp, i64, i64, vp, i32, vp, vp, vp]
+    L.mxq_expert_combine_backward.argtypes = [vp, i64, i32, vp, i64, i32, i64, i64, vp, i64, i64, vp, vp, i32, vp, i32, vp,
+                                              vp, vp]
     L.mxq_dropout.argtypes = [vp, i64, i64, i64, i32, vp, i64, ctypes.c_double, u64, u64, vp, vp, vp]
     L.mxq_sf_to_mma.argtypes = [vp, i64, i64, vp, vp]
     L.mxq_last_device_status.argtypes = [vp]

@@ -9,6 +9,7 @@
 // The sort is a counting sort of small integers: latency and launches bound
 // it.  The others move rows and are bound by HBM.
 #include <algorithm>
+#include <atomic>
 
 #include "rowops.cuh"
 
@@ -21,8 +22,12 @@ constexpr int kMaxExperts = 1024;
 
 // ---------------------------------------------------------------- sort
 constexpr int SORT_WARPS = 16, SORT_T = 32 * SORT_WARPS;
-constexpr int SORT_SLOTS = 2048;          // slots of a CTA, until there are SORT_CTAS of them
-constexpr int SORT_CTAS = 128;
+constexpr int SORT_SLOTS = 2048;          // slots of a CTA, until there are SORT_CLUSTER or SORT_CTAS of them
+// Up to 65536 slots one cluster of CTAs sorts, which read each other's counts
+// from shared memory: a launch less on the host's path (8 us there) and on the
+// device.  Beyond, SORT_CTAS count first and place in a second launch.
+constexpr int SORT_CLUSTER = 8, SORT_CTAS = 128;
+constexpr int64_t CLUSTER_SLOTS = 65536;
 
 struct SortArgs {
   const void* experts;
@@ -30,7 +35,7 @@ struct SortArgs {
   int64_t rows;
   int e64, E, align;
   int32_t *offsets, *counts, *slot_row, *row_slot, *block_expert;
-  int32_t* part;                          // [CTAs][E] counts, where there are several CTAs
+  int32_t* part;                          // [CTAs][E] counts, where they come from a launch of their own
 };
 
 // The expert of a slot, or -1 where the slot is dropped.
@@ -84,12 +89,14 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int& total) {
 // Every CTA takes `per` slots, every warp of it an even stretch of them.  A
 // slot's row is the start of its expert's stretch, the slots of that expert in
 // earlier CTAs, in earlier warps of its CTA, and earlier in its warp: an order
-// that depends on nothing but the slots.
+// that depends on nothing but the slots.  CLUSTER: the grid is one cluster.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(SORT_T) expert_place_kernel(const SortArgs a) {
   extern __shared__ int sm[];
   int* const off = sm;                            // [E + 1] starts of the experts' stretches
   int* const cnt = off + a.E + 1;                 // [E] slots of each expert
-  int* const wcnt = cnt + a.E;                    // [SORT_WARPS][E]
+  int* const own = cnt + a.E;                     // [E] this CTA's
+  int* const wcnt = own + a.E;                    // [SORT_WARPS][E]
   __shared__ int warp_sums[SORT_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < SORT_WARPS * a.E; i += SORT_T) wcnt[i] = 0;
@@ -100,19 +107,33 @@ __global__ void __launch_bounds__(SORT_T) expert_place_kernel(const SortArgs a) 
   const int64_t each = (a.per + SORT_WARPS * 32 - 1) / (SORT_WARPS * 32) * 32;
   const int64_t wlo = min(hi, lo + warp * each), whi = min(hi, wlo + each);
   int* const mine = wcnt + warp * a.E;
+#pragma unroll 8
   for (int64_t s = wlo + lane; s < whi; s += 32) {
     const int e = expert_of(a, s);
     if (e >= 0) atomicAdd(&mine[e], 1);
   }
   __syncthreads();
 
+  if constexpr (CLUSTER) {
+    for (int e = threadIdx.x; e < a.E; e += SORT_T) {
+      int n = 0;
+#pragma unroll
+      for (int w = 0; w < SORT_WARPS; ++w) n += wcnt[w * a.E + e];
+      own[e] = n;
+    }
+    cluster_sync();
+  }
   // this CTA's counts by warp become the counts of earlier CTAs and warps
   for (int e = threadIdx.x; e < a.E; e += SORT_T) {
     int before = 0, all = 0;
     if (gridDim.x > 1) {
 #pragma unroll 8
       for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-        const int n = __ldcg(a.part + static_cast<int64_t>(b) * a.E + e);
+        int n;
+        if constexpr (CLUSTER)
+          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(n) : "r"(cluster_map(smem_u32(own + e), b)) : "memory");
+        else
+          n = __ldcg(a.part + static_cast<int64_t>(b) * a.E + e);
         if (b < static_cast<int>(blockIdx.x)) before += n;
         all += n;
       }
@@ -126,6 +147,7 @@ __global__ void __launch_bounds__(SORT_T) expert_place_kernel(const SortArgs a) 
     }
     cnt[e] = gridDim.x > 1 ? all : run;
   }
+  if constexpr (CLUSTER) cluster_arrive();        // this CTA has read its peers' counts
   __syncthreads();
   int base = 0;
   for (int e0 = 0; e0 < a.E; e0 += SORT_T) {
@@ -139,9 +161,11 @@ __global__ void __launch_bounds__(SORT_T) expert_place_kernel(const SortArgs a) 
   if (threadIdx.x == 0) off[a.E] = base;
   __syncthreads();
 
+  int next = wlo + lane < whi ? expert_of(a, wlo + lane) : -1;
   for (int64_t s0 = wlo; s0 < whi; s0 += 32) {
     const int64_t s = s0 + lane;
-    const int e = s < whi ? expert_of(a, s) : -1;
+    const int e = next;
+    next = s + 32 < whi ? expert_of(a, s + 32) : -1;     // on its way while this one is placed
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
     const int rank = __popc(same & ((1u << lane) - 1u));
     int first = 0;
@@ -179,9 +203,20 @@ __global__ void __launch_bounds__(SORT_T) expert_place_kernel(const SortArgs a) 
     for (int e = threadIdx.x; e <= a.E; e += SORT_T) a.offsets[e] = off[e];
     for (int e = threadIdx.x; e < a.E; e += SORT_T) a.counts[e] = cnt[e];
   }
+  if constexpr (CLUSTER) cluster_wait();          // its own counts stay until every peer has read them
 }
 
 // ---------------------------------------------------------------- rows
+// The kernels below stay on the GPU and walk over tokens (and, for zeros, over
+// blocks of rows); the plan's entries of the next step are read while the
+// current step's rows are on their way, so that one latency is seen per step
+// instead of two.
+//
+// A row is taken in vectors of VE elements, the width of 16 bytes of its type.
+// ANY: rows may start anywhere.  The vectors then lie on what is written: its
+// first elements up to a 16-byte boundary (`head`) and its last ones go
+// singly, and what is read is put together from the two aligned words that
+// hold it.
 constexpr int ROW_T = 256, ROW_WARPS = ROW_T / 32;
 constexpr int U = 4;                      // vectors of a lane in flight per row
 
@@ -190,12 +225,13 @@ struct RowArgs {
   const void* dy;                         // backward
   void* out;                              // rows; y; drows
   float* dw;
-  const int32_t *slot_row, *row_slot;
+  const int32_t *slot_row, *offsets, *counts;
   const void* w;                          // or nullptr: 1
   int w_f32;
   int64_t tokens, rows, cols, ld, ld_dy;
-  int top;
-  int64_t pieces;                         // stretches of 32 * U vectors to a row
+  int top, experts;
+  int lanes;                              // of a warp to a row: 4 .. 32
+  int pieces;                             // stretches of lanes * U vectors to a row
 };
 
 __device__ __forceinline__ float weight_of(const RowArgs& a, int64_t slot) {
@@ -203,52 +239,188 @@ __device__ __forceinline__ float weight_of(const RowArgs& a, int64_t slot) {
   return a.w_f32 ? static_cast<const float*>(a.w)[slot] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.w)[slot]);
 }
 
-// One warp takes one stretch of a token: it is read once and written to the
-// row of each of the token's slots.  Padding rows are warps of their own.
+// Row of a slot, or -1 where it has none.
+__device__ __forceinline__ int row_of(const RowArgs& a, int64_t slot) {
+  const int r = a.slot_row[slot];
+  return r < a.rows ? r : -1;
+}
+
+// VE elements from anywhere: the aligned 16-byte words that hold the first and
+// the last of them, shifted together.  Both words hold elements of the vector,
+// so they lie where the row does.
 template <typename T, int VE>
-__global__ void __launch_bounds__(ROW_T) gather_kernel(const RowArgs a) {
-  grid_dep_launch();
-  grid_dep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t item = blockIdx.x * static_cast<int64_t>(ROW_WARPS) + (threadIdx.x >> 5);
-  const int64_t row = item / a.pieces, c0 = (item - row * a.pieces) * (32 * U * VE) + lane * VE;
-  T* const out = static_cast<T*>(a.out);
-  Vec<T, VE> v[U];
-  if (row >= a.tokens) {
-    const int64_t r = row - a.tokens;
-    if (r >= a.rows || a.row_slot[r] >= 0) return;
-    v[0].fill(0);
+__device__ __forceinline__ void load_any(Vec<T, VE>& v, const T* p) {
+  static_assert(Vec<T, VE>::BYTES == 16 || Vec<T, VE>::BYTES == 8, "a vector of one or half a word");
+  constexpr int W = Vec<T, VE>::W;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const int shift = static_cast<int>(at & 15);
+  const uint4* const q = reinterpret_cast<const uint4*>(at - shift);
+  const uint4 lo = q[0], hi = q[shift + 4 * W > 16 ? 1 : 0];
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (shift & 8) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = c0 + u * 32 * VE;
-      if (c < a.cols) v[0].store(out + r * a.cols + c);
-    }
-    return;
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
   }
-  const T* const x = static_cast<const T*>(a.src) + row * a.ld;
+  if (shift & 4) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t c = c0 + u * 32 * VE;
-    if (c < a.cols) v[u].load(x + c);
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
   }
-  for (int j = 0; j < a.top; ++j) {
-    const int64_t r = a.slot_row[row * a.top + j];
-    if (r < 0 || r >= a.rows) continue;
+  const int bits = 8 * (shift & 3);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = c0 + u * 32 * VE;
-      if (c < a.cols) v[u].store(out + r * a.cols + c);
-    }
+  for (int i = 0; i < W; ++i) v.w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+}
+
+template <bool ANY, typename T, int VE>
+__device__ __forceinline__ void load_vec(Vec<T, VE>& v, const T* p) {
+  if constexpr (ANY) load_any<T, VE>(v, p);
+  else v.load(p);
+}
+
+// Elements before the first boundary of a vector of VE elements of T.
+template <typename T, int VE>
+__device__ __forceinline__ int head_of(const T* p, int64_t cols) {
+  constexpr int B = VE * static_cast<int>(sizeof(T)) > 16 ? 16 : VE * static_cast<int>(sizeof(T));
+  const int h = static_cast<int>((0 - reinterpret_cast<uintptr_t>(p)) & (B - 1)) / static_cast<int>(sizeof(T));
+  return static_cast<int>(min(static_cast<int64_t>(h), cols));
+}
+
+// Walks of a grid's warps over the tokens' stretches: a warp's lanes fall into
+// groups of a.lanes, each of which takes a stretch of a token of its own.  A
+// place is advanced without a division.
+struct Walk {
+  int64_t rounds;                         // steps of this warp
+  int64_t row0;                           // its first token (that of its first group)
+  int piece0, group, lane, per;           // per: groups of a warp
+  int64_t row_step;
+  int piece_step, pieces;
+  __device__ __forceinline__ Walk(const RowArgs& a) {
+    const int l = threadIdx.x & 31;
+    per = 32 / a.lanes;
+    group = l / a.lanes;
+    lane = l - group * a.lanes;
+    pieces = a.pieces;
+    const int64_t step = blockIdx.x * static_cast<int64_t>(ROW_WARPS) + (threadIdx.x >> 5);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * ROW_WARPS, steps = (a.tokens + per - 1) / per * pieces;
+    rounds = step < steps ? (steps - step + stride - 1) / stride : 0;
+    row0 = step / pieces * per;
+    piece0 = static_cast<int>(step % pieces);
+    row_step = stride / pieces * per;
+    piece_step = static_cast<int>(stride % pieces);
+  }
+};
+
+struct Place {
+  int64_t row;                            // of the warp's first group
+  int piece;
+  __device__ __forceinline__ explicit Place(const Walk& w) : row(w.row0), piece(w.piece0) {}
+  __device__ __forceinline__ void next(const Walk& w) {
+    row += w.row_step;
+    piece += w.piece_step;
+    if (piece >= w.pieces) piece -= w.pieces, row += w.per;
+  }
+};
+
+// Zeros to `n` rows from row r0 on, by CTA `part` of `parts`: one stretch of memory.
+template <typename T, int VE, bool ANY, int THREADS = ROW_T>
+__device__ __forceinline__ void zero_rows(const RowArgs& a, int64_t r0, int64_t n, int64_t part, int64_t parts) {
+  if (n <= 0) return;
+  T* const p = static_cast<T*>(a.out) + r0 * a.cols;
+  const int64_t len = n * a.cols;
+  const int head = ANY ? head_of<T, VE>(p, len) : 0;
+  const int64_t nv = (len - head) / VE;
+  Vec<T, VE> z;
+  z.fill(0);
+  for (int64_t i = part * THREADS + threadIdx.x; i < nv; i += parts * THREADS) z.store(p + head + i * VE);
+  if (ANY && part == 0) {
+    Vec<T, 1> o;
+    o.fill(0);
+    if (static_cast<int>(threadIdx.x) < head) o.store(p + threadIdx.x);
+    const int64_t c = head + nv * VE + threadIdx.x;
+    if (c < len) o.store(p + c);
   }
 }
 
+// Zeros to the rows that hold no slot: what is left of every expert's stretch
+// (the experts dealt out over the CTAs, several CTAs to one where there are
+// enough), and the rows behind the last.
+template <typename T, int VE, bool ANY, int THREADS = ROW_T>
+__device__ __forceinline__ void zero_padding(const RowArgs& a) {
+  const int teams = min(a.experts, static_cast<int>(gridDim.x)), parts = gridDim.x / teams;
+  const int team = blockIdx.x % teams, part = blockIdx.x / teams;
+  if (part < parts)
+    for (int e = team; e < a.experts; e += teams) {
+      const int64_t end = min(static_cast<int64_t>(max(a.offsets[e + 1], 0)), a.rows);
+      const int64_t from = min(max(static_cast<int64_t>(a.offsets[e]) + a.counts[e], int64_t(0)), end);
+      zero_rows<T, VE, ANY, THREADS>(a, from, end - from, part, parts);
+    }
+  const int64_t last = min(static_cast<int64_t>(max(a.offsets[a.experts], 0)), a.rows);
+  zero_rows<T, VE, ANY, THREADS>(a, last, a.rows - last, blockIdx.x, gridDim.x);
+}
+
+// A token's stretch is read once and written to the row of each of its slots.
+template <typename T, int VE, bool ANY>
+__global__ void __launch_bounds__(ROW_T) gather_kernel(const RowArgs a) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const Walk w(a);
+  T* const out = static_cast<T*>(a.out);
+  Place at(w);
+  for (int64_t n = 0; n < w.rounds; ++n, at.next(w)) {
+    const int64_t t = at.row + w.group, v0 = static_cast<int64_t>(at.piece) * a.lanes * U + w.lane;
+    if (t >= a.tokens) continue;
+    const T* const x = static_cast<const T*>(a.src) + t * a.ld;
+    if constexpr (!ANY) {
+      Vec<T, VE> v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t c = (v0 + u * a.lanes) * VE;
+        if (c < a.cols) v[u].load(x + c);
+      }
+      for (int j = 0; j < a.top; ++j) {
+        const int64_t r = row_of(a, t * a.top + j);
+        if (r < 0) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t c = (v0 + u * a.lanes) * VE;
+          if (c < a.cols) v[u].store(out + r * a.cols + c);
+        }
+      }
+    } else {
+      for (int j = 0; j < a.top; ++j) {
+        const int64_t r = row_of(a, t * a.top + j);
+        if (r < 0) continue;
+        T* const o = out + r * a.cols;
+        const int head = head_of<T, VE>(o, a.cols);
+        const int64_t nv = (a.cols - head) / VE;
+        Vec<T, VE> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (v0 + u * a.lanes < nv) load_any<T, VE>(v[u], x + head + (v0 + u * a.lanes) * VE);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (v0 + u * a.lanes < nv) v[u].store(o + head + (v0 + u * a.lanes) * VE);
+        if (v0 < a.lanes)                                // the row's first stretch: its single elements
+          for (int64_t i = w.lane; i < a.cols - nv * VE; i += a.lanes) {
+            const int64_t c = i < head ? i : i + nv * VE;
+            o[c] = x[c];
+          }
+      }
+    }
+  }
+  zero_padding<T, VE, ANY>(a);
+}
+
+// ---------------------------------------------------------------- combine
+// Few tokens, or rows that have no vectors: a warp takes a stretch of a token
+// and reads its slots' rows straight into registers.
 template <typename T, typename TY, int VE>
-__global__ void __launch_bounds__(ROW_T) combine_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(ROW_T) combine_direct_kernel(const RowArgs a) {
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t item = blockIdx.x * static_cast<int64_t>(ROW_WARPS) + (threadIdx.x >> 5);
-  const int64_t t = item / a.pieces, c0 = (item - t * a.pieces) * (32 * U * VE) + lane * VE;
+  const uint32_t item = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
+  const int64_t t = item / static_cast<uint32_t>(a.pieces);
+  const int64_t c0 = static_cast<int64_t>(item % static_cast<uint32_t>(a.pieces)) * (32 * U * VE) + lane * VE;
   if (t >= a.tokens) return;
   float acc[U][VE];
 #pragma unroll
@@ -257,9 +429,9 @@ __global__ void __launch_bounds__(ROW_T) combine_kernel(const RowArgs a) {
     for (int i = 0; i < VE; ++i) acc[u][i] = 0.f;
 #pragma unroll 2
   for (int j = 0; j < a.top; ++j) {
-    const int64_t slot = t * a.top + j, r = a.slot_row[slot];
-    if (r < 0 || r >= a.rows) continue;
-    const float w = weight_of(a, slot);
+    const int64_t slot = t * a.top + j, r = row_of(a, slot);
+    if (r < 0) continue;
+    const float g = weight_of(a, slot);
     const T* const src = static_cast<const T*>(a.src) + r * a.ld;
     Vec<T, VE> v[U];
 #pragma unroll
@@ -271,7 +443,7 @@ __global__ void __launch_bounds__(ROW_T) combine_kernel(const RowArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < VE; ++i) acc[u][i] = fmaf(w, v[u].get(i), acc[u][i]);
+      for (int i = 0; i < VE; ++i) acc[u][i] = fmaf(g, v[u].get(i), acc[u][i]);
   }
   TY* const y = static_cast<TY*>(a.out) + t * a.cols;
 #pragma unroll
@@ -281,71 +453,309 @@ __global__ void __launch_bounds__(ROW_T) combine_kernel(const RowArgs a) {
   }
 }
 
-// A CTA takes a token: dy's stretches stay in registers while the rows of its
-// slots pass (rows of more than a stretch per warp go round again).
-template <typename T, typename TY, int VE>
-__global__ void __launch_bounds__(ROW_T) combine_bwd_kernel(const RowArgs a) {
-  __shared__ float red[ROW_WARPS];
+// Many tokens.
+// A warp's work is one sequence of units: a stretch of the row of one slot, the
+// slots of a token in their order.  Every lane copies its own vectors of a unit
+// to shared memory S units ahead (asynchronously: registers would hold less
+// than half of what has to be in flight), and the unit's row number and weight
+// S units before that.
+constexpr int S = 4;
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+constexpr int combine_words(bool any) { return 32 * U + (any ? 1 : 0); }    // of a warp's unit
+constexpr int combine_smem(bool any) { return S * ROW_WARPS * combine_words(any) * 16 + 2 * S * ROW_T * 8; }
+
+template <typename T, typename TY, int VE, bool ANY>
+__global__ void __launch_bounds__(ROW_T, 2) combine_kernel(const RowArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int WORDS = combine_words(ANY);
+  uint2* const plan = reinterpret_cast<uint2*>(ring + S * ROW_WARPS * WORDS * 16) + threadIdx.x;    // [2 S][ROW_T]
+  const Walk w(a);
+  const int lane = threadIdx.x & 31;
+  uint8_t* const mine = ring + (threadIdx.x >> 5) * (WORDS * 16) + (ANY ? 0 : lane * 16);
+  const uint32_t to = smem_u32(mine) + (ANY ? lane * 16 : 0), plan_to = smem_u32(plan);
+  const T* const src = static_cast<const T*>(a.src);
+  const int vecs = a.lanes * U, cols = static_cast<int>(a.cols);
   grid_dep_launch();
   grid_dep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  T* const out = static_cast<T*>(a.out);
-  if (blockIdx.x >= a.tokens) {
-    // ROW_WARPS rows, a warp each: padding gets zeros
-    const int64_t r = (blockIdx.x - a.tokens) * static_cast<int64_t>(ROW_WARPS) + warp;
-    if (r >= a.rows || a.row_slot[r] >= 0) return;
-    Vec<T, VE> z;
-    z.fill(0);
-    for (int64_t c = lane * VE; c < a.cols; c += 32 * VE) z.store(out + r * a.cols + c);
-    return;
-  }
-  const int64_t t = blockIdx.x;
-  const TY* const dy = static_cast<const TY*>(a.dy) + t * a.ld_dy;
-  for (int j = 0; j < a.top; ++j) {
-    const int64_t slot = t * a.top + j, r = a.slot_row[slot];
-    const bool live = r >= 0 && r < a.rows;
-    float dot = 0.f;
-    if (live) {
-      const float w = weight_of(a, slot);
-      const T* const src = static_cast<const T*>(a.src) + r * a.ld;
-      for (int64_t c0 = threadIdx.x * VE; c0 < a.cols; c0 += ROW_T * VE * 2) {
-        Vec<T, VE> v[2];
-        float g[2][VE];
+  // a token's row of y: elements before its vectors, and how many vectors
+  const auto head_at = [&](int64_t t) { return ANY ? head_of<TY, VE>(static_cast<TY*>(a.out) + t * cols, cols) : 0; };
+
+  float acc[U][VE];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int64_t c = c0 + u * ROW_T * VE;
-          if (c < a.cols) {
-            v[u].load(src + c);
-            load_elems<TY, VE>(dy + c, g[u]);
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < VE; ++i) acc[u][i] = 0.f;
+  Place use(w), copy(w), look(w);
+  int use_j = 0, copy_j = 0, look_j = 0;
+  int64_t use_n = w.rounds, copy_n = w.rounds, look_n = w.rounds;     // steps left
+  int slot = 0, at = 0;                                  // of the ring (S), of the plan (2 S)
+  for (int n = -2 * S; use_n > 0; n += n < 0) {
+    cp_async_wait<S - 1>();
+    if constexpr (ANY) __syncwarp();                     // lanes read each other's words
+    int r = -1;
+    float g = 1.f;
+    Vec<T, VE> x[U];
+    if (n >= 0 && use.row + w.group < a.tokens) {
+      const uint2 q = plan[at * ROW_T];
+      r = static_cast<int>(q.x) < a.rows ? static_cast<int>(q.x) : -1;
+      if (a.w) {
+        const bool high = !a.w_f32 && (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(a.w) >> 1) +
+                                       static_cast<uint32_t>((use.row + w.group) * a.top + use_j)) & 1;
+        g = a.w_f32 ? __uint_as_float(q.y) : high ? bf16hi(q.y) : bf16lo(q.y);
+      }
+      if (r >= 0) {
+        uint8_t* const from = mine + slot * (ROW_WARPS * WORDS * 16);
+        if constexpr (!ANY) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const uint4 p = *reinterpret_cast<const uint4*>(from + u * 512);
+            x[u].w[0] = p.x, x[u].w[1] = p.y, x[u].w[2] = p.z, x[u].w[3] = p.w;
           }
-        }
+        } else {
+          const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src + r * a.ld + head_at(use.row)) & 15);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int64_t c = c0 + u * ROW_T * VE;
-          if (c < a.cols) {
-            float q[VE], d[VE];
-#pragma unroll
-            for (int i = 0; i < VE; ++i) {
-              q[i] = g[u][i] * v[u].get(i);
-              d[i] = g[u][i] * w;
-            }
-            dot += tree_sum(q);
-            store_vec<T, VE>(out + r * a.cols + c, d);
-          }
+          for (int u = 0; u < U; ++u) load_any<T, VE>(x[u], reinterpret_cast<const T*>(from + (u * 32 + lane) * 16 + shift));
         }
       }
     }
-    dot = warp_sum(dot);
-    if (lane == 0) red[warp] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float s = 0.f;
+    if constexpr (ANY) __syncwarp();
+    if (n >= -S && copy_n > 0) {
+      const int64_t t = copy.row + w.group;
+      if (t < a.tokens) {
+        const int cr = static_cast<int>(plan[(at >= S ? at - S : at + S) * ROW_T].x);
+        if (cr >= 0 && cr < a.rows) {
+          const uint32_t dst = to + slot * (ROW_WARPS * WORDS * 16);
+          const T* const row = src + cr * a.ld;
+          if constexpr (!ANY) {
+            const int c = (copy.piece * vecs + w.lane) * VE, step = a.lanes * VE;
 #pragma unroll
-      for (int k = 0; k < ROW_WARPS; ++k) s += red[k];
-      a.dw[slot] = live ? s : 0.f;
+            for (int u = 0; u < U; ++u)
+              if (c + u * step < cols) cp_async16(dst + u * 512, row + c + u * step);
+          } else {
+            // the aligned words that hold any of the stretch's elements
+            const int head = head_at(t);
+            const uintptr_t p = (reinterpret_cast<uintptr_t>(row + head + copy.piece * (32 * U * VE)) & ~uintptr_t(15)) + lane * 16;
+            const uintptr_t end = reinterpret_cast<uintptr_t>(row + head + (cols - head) / VE * VE);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              if (p + u * 512 < end) cp_async16(dst + u * 512, reinterpret_cast<const void*>(p + u * 512));
+            if (lane == 0 && p + U * 512 < end) cp_async16(dst + U * 512, reinterpret_cast<const void*>(p + U * 512));
+          }
+        }
+      }
+      if (++copy_j == a.top) copy_j = 0, --copy_n, copy.next(w);
     }
-    __syncthreads();
+    if (look_n > 0) {
+      const int64_t t = look.row + w.group;
+      if (t < a.tokens) {
+        const int64_t id = t * a.top + look_j;
+        cp_async4(plan_to + at * (ROW_T * 8), a.slot_row + id);
+        // a bf16 weight comes with its neighbour
+        if (a.w)
+          cp_async4(plan_to + at * (ROW_T * 8) + 4,
+                    reinterpret_cast<const void*>((reinterpret_cast<uintptr_t>(a.w) + (a.w_f32 ? 4 : 2) * id) & ~uintptr_t(3)));
+      }
+      if (++look_j == a.top) look_j = 0, --look_n, look.next(w);
+    }
+    cp_async_commit();
+    if (n >= -S) slot = slot + 1 == S ? 0 : slot + 1;
+    at = at + 1 == 2 * S ? 0 : at + 1;
+    if (n < 0) continue;
+    if (r >= 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) acc[u][i] = fmaf(g, x[u].get(i), acc[u][i]);
+    }
+    if (++use_j < a.top) continue;
+    const int64_t t = use.row + w.group;
+    if (t < a.tokens) {
+      const int head = head_at(t), nv = (cols - head) / VE;
+      const int v = use.piece * vecs + w.lane;
+      TY* const y = static_cast<TY*>(a.out) + t * cols + head + static_cast<int64_t>(v) * VE;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v + u * a.lanes < nv) store_vec<TY, VE>(y + u * a.lanes * VE, acc[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < VE; ++i) acc[u][i] = 0.f;
+    use_j = 0, --use_n;
+    use.next(w);
   }
+  cp_async_wait<0>();
+
+  if constexpr (ANY) {
+    // the single elements before and behind a row's vectors, 16 lanes to a token
+    const int64_t team = (blockIdx.x * static_cast<int64_t>(ROW_T) + threadIdx.x) >> 4, teams = static_cast<int64_t>(gridDim.x) * (ROW_T / 16);
+    const int l = threadIdx.x & 15;
+    for (int64_t t = team; t < a.tokens; t += teams) {
+      const int head = head_at(t), nv = (cols - head) / VE;
+      const int c = l < head ? l : l + nv * VE;
+      if (c >= cols) continue;
+      float sum[1] = {0.f};
+#pragma unroll 4
+      for (int j = 0; j < a.top; ++j) {
+        const int r = row_of(a, t * a.top + j);
+        if (r >= 0) {
+          float e[1];
+          load_elems<T, 1>(static_cast<const T*>(a.src) + r * a.ld + c, e);
+          sum[0] = fmaf(weight_of(a, t * a.top + j), e[0], sum[0]);
+        }
+      }
+      store_vec<TY, 1>(static_cast<TY*>(a.out) + t * cols + c, sum);
+    }
+  }
+}
+
+constexpr int BWD_T = 256, BWD_WARPS = BWD_T / 32;
+
+// G of a CTA's BWD_WARPS warps take a token; dy's NV vectors of a lane stay in registers while the rows of its slots pass, two at a time.
+// Longer rows go round in stretches, whose parts of the sums are added up.
+template <typename T, typename TY, int VE, int G, int NV, bool ANY>
+__global__ void __launch_bounds__(BWD_T, 4) combine_bwd_kernel(const RowArgs a) {
+  constexpr int TEAMS = BWD_WARPS / G;
+  __shared__ float red[2][TEAMS][2][G];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / G, part = warp % G;
+  const int idx = part * 32 + lane;                      // thread of the team
+  T* const out = static_cast<T*>(a.out);
+  int buf = 0;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
+  int r[2];
+  float g[2];
+  const auto fetch = [&](int64_t t, int j) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      r[k] = -1, g[k] = 0.f;
+      if (t < a.tokens && j + k < a.top) {
+        r[k] = row_of(a, t * a.top + j + k);
+        if (r[k] >= 0) g[k] = weight_of(a, t * a.top + j + k);
+      }
+    }
+  };
+  int64_t t = blockIdx.x * static_cast<int64_t>(TEAMS) + team;
+  fetch(t, 0);
+  for (; t < a.tokens; t += stride) {
+    const TY* const dy = static_cast<const TY*>(a.dy) + t * a.ld_dy;
+    float d[NV][VE];
+    const bool whole = !ANY && a.cols <= G * 32 * NV * VE;       // dy is read once
+    if (whole) {
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        const int64_t c = (static_cast<int64_t>(n) * G * 32 + idx) * VE;
+        if (c < a.cols) load_elems<TY, VE>(dy + c, d[n]);
+      }
+    }
+    for (int j = 0; j < a.top; j += 2) {
+      const int rr[2] = {r[0], r[1]};
+      const float gg[2] = {g[0], g[1]};
+      if (j + 2 < a.top) fetch(t, j + 2);
+      else fetch(t + stride, 0);
+      float dot[2] = {0.f, 0.f};
+      if (whole) {
+        Vec<T, VE> x[2][NV];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            const int64_t c = (static_cast<int64_t>(n) * G * 32 + idx) * VE;
+            if (rr[k] >= 0 && c < a.cols) x[k][n].load(static_cast<const T*>(a.src) + rr[k] * a.ld + c);
+          }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (rr[k] < 0) continue;
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            const int64_t c = (static_cast<int64_t>(n) * G * 32 + idx) * VE;
+            if (c < a.cols) {
+              float q[VE], o[VE];
+#pragma unroll
+              for (int i = 0; i < VE; ++i) q[i] = d[n][i] * x[k][n].get(i), o[i] = d[n][i] * gg[k];
+              dot[k] += tree_sum(q);
+              store_vec<T, VE>(out + rr[k] * a.cols + c, o);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (rr[k] < 0) continue;
+          const T* const x = static_cast<const T*>(a.src) + rr[k] * a.ld;
+          T* const o = out + rr[k] * a.cols;
+          const int head = ANY ? head_of<T, VE>(o, a.cols) : 0;
+          const int64_t nv = (a.cols - head) / VE;
+          for (int64_t v0 = idx; v0 < nv; v0 += G * 32 * NV) {
+            Vec<T, VE> xv[NV];
+            Vec<TY, (VE * sizeof(TY) > 16 ? VE / 2 : VE)> dv[NV][VE * sizeof(TY) > 16 ? 2 : 1];
+            constexpr int H = VE * sizeof(TY) > 16 ? VE / 2 : VE, P = VE / H;
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+              const int64_t v = v0 + n * G * 32, c = head + v * VE;
+              if (v < nv) {
+                load_vec<ANY>(xv[n], x + c);
+#pragma unroll
+                for (int h = 0; h < P; ++h) load_vec<ANY>(dv[n][h], dy + c + h * H);
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+              const int64_t v = v0 + n * G * 32, c = head + v * VE;
+              if (v < nv) {
+                float q[VE], p[VE];
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                  const float dd = dv[n][i / H].get(i % H);
+                  q[i] = dd * xv[n].get(i), p[i] = dd * gg[k];
+                }
+                dot[k] += tree_sum(q);
+                store_vec<T, VE>(o + c, p);
+              }
+            }
+          }
+          if constexpr (ANY) {
+            for (int64_t i = idx; i < a.cols - nv * VE; i += G * 32) {
+              const int64_t c = i < head ? i : i + nv * VE;
+              float e[1], f[1];
+              load_elems<T, 1>(x + c, e);
+              load_elems<TY, 1>(dy + c, f);
+              dot[k] = fmaf(e[0], f[0], dot[k]);
+              f[0] *= gg[k];
+              store_vec<T, 1>(o + c, f);
+            }
+          }
+        }
+      }
+      dot[0] = warp_sum(dot[0]);
+      dot[1] = warp_sum(dot[1]);
+      if constexpr (G == 1) {
+        if (lane < 2 && j + lane < a.top) a.dw[t * a.top + j + lane] = lane ? dot[1] : dot[0];
+      } else {
+        if (lane == 0) red[buf][team][0][part] = dot[0], red[buf][team][1][part] = dot[1];
+        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(G * 32) : "memory");
+        if (idx < 2 && j + idx < a.top) {
+          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < G; ++k) sum += red[buf][team][idx][k];
+          a.dw[t * a.top + j + idx] = sum;
+        }
+        buf ^= 1;                                        // the next sums go elsewhere: one barrier a round is enough
+      }
+    }
+  }
+  zero_padding<T, VE, ANY, BWD_T>(a);
 }
 
 // ---------------------------------------------------------------- host
@@ -353,42 +763,127 @@ bool plan_sizes(int64_t tokens, int64_t top, int64_t rows) {
   return tokens >= 0 && top >= 1 && rows >= 0 && top <= kMaxCols && tokens <= kMaxCols / top && rows <= kMaxCols;
 }
 
+// Rows that start at 16-byte boundaries and hold whole words.
 bool wide(const void* p, int64_t ld, int type, int64_t cols) {
   const int s = type_size(type);
   return aligned16(p) && (ld * s) % 16 == 0 && (cols * s) % 16 == 0;
 }
 
-int ctas(int64_t items, unsigned* grid) {
-  const int64_t n = (items + ROW_WARPS - 1) / ROW_WARPS;
-  if (n > 0x7FFFFFFF) return MXQ_ERR_BAD_SHAPE;
-  *grid = static_cast<unsigned>(n);
+// CTAs that stay on the GPU: as many as fit, or as there is work for.
+template <typename K>
+int stay(K kern, int64_t want, std::atomic<int>* known, unsigned* grid, int smem = 0, int threads = ROW_T) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ERR_CUDA;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (!n) {
+    if (smem && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return MXQ_ERR_CUDA;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess || n < 1) return MXQ_ERR_CUDA;
+    n *= sm_count();
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  *grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(want, n)));
   return MXQ_OK;
 }
 
-template <typename T, int VE>
+// Lanes of a row: the power of two that its vectors fill with U each, 4 .. 32.
+void set_lanes(RowArgs& a, int ve) {
+  a.lanes = 4;
+  while (a.lanes < 32 && a.lanes * U * ve < a.cols) a.lanes *= 2;
+  a.pieces = static_cast<int>((a.cols + a.lanes * U * ve - 1) / (a.lanes * U * ve));
+}
+
+int64_t walk_ctas(const RowArgs& a) {
+  const int per = 32 / a.lanes;
+  return ((a.tokens + per - 1) / per * a.pieces + ROW_WARPS - 1) / ROW_WARPS;
+}
+
+template <typename T, int VE, bool ANY>
 int run_gather(RowArgs a, cudaStream_t st) {
-  a.pieces = (a.cols + 32 * U * VE - 1) / (32 * U * VE);
+  static std::atomic<int> known[64];
+  set_lanes(a, VE);
   unsigned grid = 0;
-  if (const int rc = ctas((a.tokens + a.rows) * a.pieces, &grid)) return rc;
-  return grid ? launch_pdl(gather_kernel<T, VE>, dim3(grid), dim3(ROW_T), 0, st, a) : MXQ_OK;
+  const int64_t want = std::max<int64_t>(walk_ctas(a), (a.rows * a.cols + ROW_T * VE - 1) / (ROW_T * VE));
+  if (const int rc = stay(gather_kernel<T, VE, ANY>, want, known, &grid)) return rc;
+  return launch_pdl(gather_kernel<T, VE, ANY>, dim3(grid), dim3(ROW_T), 0, st, a);
+}
+
+template <typename T, typename TY, int VE, bool ANY>
+int run_combine_ring(RowArgs a, cudaStream_t st) {
+  static std::atomic<int> known[64];
+  set_lanes(a, VE);
+  if (ANY) a.lanes = 32, a.pieces = static_cast<int>((a.cols + 32 * U * VE - 1) / (32 * U * VE));      // a warp's words lie side by side
+  unsigned grid = 0;
+  constexpr int smem = combine_smem(ANY);
+  if (const int rc = stay(combine_kernel<T, TY, VE, ANY>, walk_ctas(a), known, &grid, smem)) return rc;
+  return launch_pdl(combine_kernel<T, TY, VE, ANY>, dim3(grid), dim3(ROW_T), smem, st, a);
 }
 
 template <typename T, typename TY, int VE>
-int run_combine(RowArgs a, cudaStream_t st) {
-  a.pieces = (a.cols + 32 * U * VE - 1) / (32 * U * VE);
-  unsigned grid = 0;
-  if (const int rc = ctas(a.tokens * a.pieces, &grid)) return rc;
-  return grid ? launch_pdl(combine_kernel<T, TY, VE>, dim3(grid), dim3(ROW_T), 0, st, a) : MXQ_OK;
+int run_combine_direct(RowArgs a, cudaStream_t st) {
+  a.pieces = static_cast<int>((a.cols + 32 * U * VE - 1) / (32 * U * VE));
+  const int64_t grid = (a.tokens * a.pieces + ROW_WARPS - 1) / ROW_WARPS;
+  return launch_pdl(combine_direct_kernel<T, TY, VE>, dim3(static_cast<unsigned>(grid)), dim3(ROW_T), 0, st, a);
 }
+
+// The ring pays from about 2^21 elements of y on, and for bf16 rows without a
+// common alignment from DIRECT_COLS columns on (their single elements go round
+// apart); float32 rows without one are read element by element at
+// the same rate.
+constexpr int64_t RING_ELEMS = 1 << 21, DIRECT_COLS = 512, DIRECT_ITEMS = 1ll << 31;
 
 template <typename T, typename TY, int VE>
-int run_backward(const RowArgs& a, cudaStream_t st) {
-  const int64_t grid = a.tokens + (a.rows + ROW_WARPS - 1) / ROW_WARPS;
-  if (grid > 0x7FFFFFFF) return MXQ_ERR_BAD_SHAPE;
-  return grid ? launch_pdl(combine_bwd_kernel<T, TY, VE>, dim3(static_cast<unsigned>(grid)), dim3(ROW_T), 0, st, a) : MXQ_OK;
+int run_combine(const RowArgs& a, bool vectors, cudaStream_t st) {
+  const bool many = a.tokens * a.cols >= RING_ELEMS;
+  if (vectors) return many ? run_combine_ring<T, TY, VE, false>(a, st) : run_combine_direct<T, TY, VE>(a, st);
+  const bool countable = a.tokens * ((a.cols + 32 * U - 1) / (32 * U)) < DIRECT_ITEMS;
+  if (countable && (sizeof(T) == 4 || !many || a.cols < DIRECT_COLS)) return run_combine_direct<T, TY, 1>(a, st);
+  return run_combine_ring<T, TY, VE, true>(a, st);
 }
 
-int64_t sort_ctas(int64_t slots) { return std::max<int64_t>(1, std::min<int64_t>(SORT_CTAS, (slots + SORT_SLOTS - 1) / SORT_SLOTS)); }
+template <typename T, typename TY, int VE, int G, int NV, bool ANY>
+int launch_backward(const RowArgs& a, cudaStream_t st) {
+  static std::atomic<int> known[64];
+  unsigned grid = 0;
+  const int64_t want = std::max<int64_t>((a.tokens * G + BWD_WARPS - 1) / BWD_WARPS,
+                                         (a.rows * a.cols + BWD_T * VE - 1) / (BWD_T * VE));
+  if (const int rc = stay(combine_bwd_kernel<T, TY, VE, G, NV, ANY>, want, known, &grid, 0, BWD_T)) return rc;
+  return launch_pdl(combine_bwd_kernel<T, TY, VE, G, NV, ANY>, dim3(grid), dim3(BWD_T), 0, st, a);
+}
+
+// As many warps to a token as its vectors fill, eight at most.
+template <typename T, typename TY, int VE>
+int run_backward(const RowArgs& a, bool vectors, cudaStream_t st) {
+  if (!vectors)
+    return a.cols <= 64 * VE ? launch_backward<T, TY, VE, 1, 1, true>(a, st) : launch_backward<T, TY, VE, 8, 2, true>(a, st);
+  if (a.cols <= 32 * VE) return launch_backward<T, TY, VE, 1, 1, false>(a, st);
+  if (a.cols <= 64 * VE) return launch_backward<T, TY, VE, 2, 1, false>(a, st);
+  if (a.cols <= 128 * VE) return launch_backward<T, TY, VE, 4, 1, false>(a, st);
+  if (a.cols <= 256 * VE) return launch_backward<T, TY, VE, 8, 1, false>(a, st);
+  return launch_backward<T, TY, VE, 8, 2, false>(a, st);
+}
+
+int64_t sort_ctas(int64_t slots) {
+  const int most = slots <= CLUSTER_SLOTS ? SORT_CLUSTER : SORT_CTAS;
+  return std::max<int64_t>(1, std::min<int64_t>(most, (slots + SORT_SLOTS - 1) / SORT_SLOTS));
+}
+
+constexpr int sort_smem(int experts) { return ((3 + SORT_WARPS) * experts + 1) * static_cast<int>(sizeof(int)); }
+
+template <bool CLUSTER>
+int run_place(const SortArgs& a, int64_t n, cudaStream_t st) {
+  static std::atomic<bool> set[64];
+  auto kern = expert_place_kernel<CLUSTER>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ERR_CUDA;
+  if (!set[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem(kMaxExperts)) != cudaSuccess)
+      return MXQ_ERR_CUDA;
+    set[dev].store(true, std::memory_order_relaxed);
+  }
+  const dim3 grid(static_cast<unsigned>(n));
+  if (CLUSTER) return launch_pdl_cluster(kern, grid, dim3(SORT_T), sort_smem(a.E), st, static_cast<int>(n), a);
+  return launch_pdl(kern, grid, dim3(SORT_T), sort_smem(a.E), st, a);
+}
 
 }  // namespace
 }  // namespace mxq
@@ -409,7 +904,7 @@ extern "C" int mxq_expert_rows(int64_t slots, int experts, int align, int64_t* r
 extern "C" int mxq_expert_sort_workspace_size(int64_t slots, int experts, size_t* bytes) {
   if (!bytes) return MXQ_ERR_BAD_ARG;
   if (slots < 0 || slots > kMaxCols || experts < 1 || experts > kMaxExperts) return MXQ_ERR_BAD_SHAPE;
-  *bytes = static_cast<size_t>(sort_ctas(slots)) * experts * sizeof(int32_t);
+  *bytes = slots <= CLUSTER_SLOTS ? 16 : static_cast<size_t>(sort_ctas(slots)) * experts * sizeof(int32_t);
   return MXQ_OK;
 }
 
@@ -432,39 +927,32 @@ extern "C" int mxq_expert_sort(const void* experts, int experts_64, int64_t slot
   SortArgs a{experts, slots, (slots + n - 1) / n, rows, experts_64, num_experts, align, offsets, counts, slot_row,
              row_slot, block_expert, static_cast<int32_t*>(workspace)};
   const auto st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(n));
-  if (n > 1)
-    if (const int rc = launch_pdl(expert_count_kernel, grid, dim3(SORT_T), num_experts * sizeof(int), st, a)) return rc;
-  const size_t smem = ((2 + SORT_WARPS) * num_experts + 1) * sizeof(int);
-  static bool set[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MXQ_ERR_CUDA;
-  if (!set[dev & 63]) {
-    if (cudaFuncSetAttribute(expert_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             ((2 + SORT_WARPS) * kMaxExperts + 1) * sizeof(int)) != cudaSuccess)
-      return MXQ_ERR_CUDA;
-    set[dev & 63] = true;
-  }
-  return launch_pdl(expert_place_kernel, grid, dim3(SORT_T), smem, st, a);
+  if (n == 1) return run_place<false>(a, n, st);
+  if (slots <= CLUSTER_SLOTS) return run_place<true>(a, n, st);
+  if (const int rc = launch_pdl(expert_count_kernel, dim3(static_cast<unsigned>(n)), dim3(SORT_T), num_experts * sizeof(int), st, a))
+    return rc;
+  return run_place<false>(a, n, st);
 }
 
 extern "C" int mxq_expert_gather(const void* x, int64_t tokens, int64_t cols, int64_t ld, int x_type,
-                                 const int32_t* slot_row, int64_t top, const int32_t* row_slot, int64_t rows, void* out,
-                                 void* stream) {
+                                 const int32_t* slot_row, int64_t top, const int32_t* offsets, const int32_t* counts,
+                                 int experts, int64_t rows, void* out, void* stream) {
   if (!valid_type(x_type)) return MXQ_ERR_BAD_ARG;
   if (!plan_sizes(tokens, top, rows) || cols < 1 || cols > kMaxCols || ld < cols) return MXQ_ERR_BAD_SHAPE;
-  if ((tokens && (!x || !slot_row)) || (rows && (!row_slot || !out))) return MXQ_ERR_BAD_ARG;
+  if (experts < 1 || experts > kMaxExperts) return MXQ_ERR_BAD_SHAPE;
+  if ((tokens && (!x || !slot_row)) || (rows && (!offsets || !counts || !out))) return MXQ_ERR_BAD_ARG;
   if (!aligned_to(x, type_size(x_type)) || !aligned_to(out, type_size(x_type)) || !aligned_to(slot_row, 4) ||
-      !aligned_to(row_slot, 4))
+      !aligned_to(offsets, 4) || !aligned_to(counts, 4))
     return MXQ_ERR_MISALIGNED;
   if (!device_ok()) return MXQ_ERR_UNSUPPORTED;
   RowArgs a{};
-  a.src = x, a.out = out, a.slot_row = slot_row, a.row_slot = row_slot;
+  a.src = x, a.out = out, a.slot_row = slot_row, a.offsets = offsets, a.counts = counts, a.experts = experts;
   a.tokens = tokens, a.rows = rows, a.cols = cols, a.ld = ld, a.top = static_cast<int>(top);
   const auto st = static_cast<cudaStream_t>(stream);
   const bool v = wide(x, ld, x_type, cols) && aligned16(out);
-  if (x_type == MXQ_F32) return v ? run_gather<float, 4>(a, st) : run_gather<float, 1>(a, st);
-  return v ? run_gather<__nv_bfloat16, 8>(a, st) : run_gather<__nv_bfloat16, 1>(a, st);
+  if (!rows) return MXQ_OK;
+  if (x_type == MXQ_F32) return v ? run_gather<float, 4, false>(a, st) : run_gather<float, 4, true>(a, st);
+  return v ? run_gather<__nv_bfloat16, 8, false>(a, st) : run_gather<__nv_bfloat16, 8, true>(a, st);
 }
 
 extern "C" int mxq_expert_combine(const void* rows_in, int64_t rows, int64_t cols, int64_t ld, int type,
@@ -482,40 +970,45 @@ extern "C" int mxq_expert_combine(const void* rows_in, int64_t rows, int64_t col
   a.tokens = tokens, a.rows = rows, a.cols = cols, a.ld = ld, a.top = static_cast<int>(top);
   const auto st = static_cast<cudaStream_t>(stream);
   const bool v = wide(rows_in, ld, type, cols) && aligned16(y);
+  if (!tokens) return MXQ_OK;
   using bf = __nv_bfloat16;
   if (type == MXQ_F32) {
-    if (y_type == MXQ_F32) return v ? run_combine<float, float, 4>(a, st) : run_combine<float, float, 1>(a, st);
-    return v ? run_combine<float, bf, 4>(a, st) : run_combine<float, bf, 1>(a, st);
+    if (y_type == MXQ_F32) return run_combine<float, float, 4>(a, v, st);
+    return run_combine<float, bf, 4>(a, v, st);
   }
-  if (y_type == MXQ_F32) return v ? run_combine<bf, float, 8>(a, st) : run_combine<bf, float, 1>(a, st);
-  return v ? run_combine<bf, bf, 8>(a, st) : run_combine<bf, bf, 1>(a, st);
+  if (y_type == MXQ_F32) return run_combine<bf, float, 8>(a, v, st);
+  return run_combine<bf, bf, 8>(a, v, st);
 }
 
 extern "C" int mxq_expert_combine_backward(const void* dy, int64_t ld_dy, int dy_type, const void* rows_in, int64_t ld,
                                            int type, int64_t rows, int64_t cols, const int32_t* slot_row,
-                                           const int32_t* row_slot, int64_t tokens, int64_t top, const void* weights,
-                                           int w_type, void* drows, float* dweights, void* stream) {
+                                           int64_t tokens, int64_t top, const int32_t* offsets, const int32_t* counts,
+                                           int experts, const void* weights, int w_type, void* drows, float* dweights,
+                                           void* stream) {
   if (!valid_type(type) || !valid_type(dy_type) || !valid_type(w_type)) return MXQ_ERR_BAD_ARG;
   if (!plan_sizes(tokens, top, rows) || cols < 1 || cols > kMaxCols || ld < cols || ld_dy < cols) return MXQ_ERR_BAD_SHAPE;
-  if ((rows && (!rows_in || !row_slot || !drows)) || (tokens && (!dy || !slot_row || !weights || !dweights)))
+  if (experts < 1 || experts > kMaxExperts) return MXQ_ERR_BAD_SHAPE;
+  if ((rows && (!rows_in || !offsets || !counts || !drows)) || (tokens && (!dy || !slot_row || !weights || !dweights)))
     return MXQ_ERR_BAD_ARG;
   if (!aligned_to(rows_in, type_size(type)) || !aligned_to(dy, type_size(dy_type)) || !aligned_to(drows, type_size(type)) ||
-      !aligned_to(slot_row, 4) || !aligned_to(row_slot, 4) || !aligned_to(weights, type_size(w_type)) ||
+      !aligned_to(slot_row, 4) || !aligned_to(offsets, 4) || !aligned_to(counts, 4) || !aligned_to(weights, type_size(w_type)) ||
       !aligned_to(dweights, 4))
     return MXQ_ERR_MISALIGNED;
   if (!device_ok()) return MXQ_ERR_UNSUPPORTED;
   RowArgs a{};
-  a.src = rows_in, a.dy = dy, a.out = drows, a.dw = dweights, a.slot_row = slot_row, a.row_slot = row_slot;
+  a.src = rows_in, a.dy = dy, a.out = drows, a.dw = dweights, a.slot_row = slot_row;
+  a.offsets = offsets, a.counts = counts, a.experts = experts;
   a.w = weights, a.w_f32 = w_type == MXQ_F32;
   a.tokens = tokens, a.rows = rows, a.cols = cols, a.ld = ld, a.ld_dy = ld_dy, a.top = static_cast<int>(top);
   const auto st = static_cast<cudaStream_t>(stream);
   // a vector is 16 bytes of the rows; dy's side of it is 8, 16 or 32
   const bool v = wide(rows_in, ld, type, cols) && aligned16(drows) && wide(dy, ld_dy, dy_type, cols);
+  if (!tokens && !rows) return MXQ_OK;
   using bf = __nv_bfloat16;
   if (type == MXQ_F32) {
-    if (dy_type == MXQ_F32) return v ? run_backward<float, float, 4>(a, st) : run_backward<float, float, 1>(a, st);
-    return v ? run_backward<float, bf, 4>(a, st) : run_backward<float, bf, 1>(a, st);
+    if (dy_type == MXQ_F32) return run_backward<float, float, 4>(a, v, st);
+    return run_backward<float, bf, 4>(a, v, st);
   }
-  if (dy_type == MXQ_F32) return v ? run_backward<bf, float, 8>(a, st) : run_backward<bf, float, 1>(a, st);
-  return v ? run_backward<bf, bf, 8>(a, st) : run_backward<bf, bf, 1>(a, st);
+  if (dy_type == MXQ_F32) return run_backward<bf, float, 8>(a, v, st);
+  return run_backward<bf, bf, 8>(a, v, st);
 }

@@ -34,9 +34,35 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// The larger magnitudes of two pairs of bf16, half by half (a NaN gives NaN);
+// the signs of the halves mean nothing.
+__device__ __forceinline__ uint32_t amax2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <int N>
+__device__ __forceinline__ uint32_t amax_words(const uint32_t (&w)[N]) {
+  uint32_t t[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) t[i] = w[i];
+#pragma unroll
+  for (int n = N / 2; n; n /= 2)
+#pragma unroll
+    for (int i = 0; i < n; ++i) t[i] = amax2(t[i], t[i + n]);
+  return t[0];
+}
+// The halves' magnitudes as float32 bits.
+__device__ __forceinline__ uint32_t mag_lo(uint32_t m) { return (m << 16) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t mag_hi(uint32_t m) { return m & 0x7FFF0000u; }
+
 // Codes of a block (32 bytes of FP8, 16 of packed E2M1).
 template <int FMT>
-__device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&q)[code_words<FMT, 32>()], int wide) {
+__device__ __forceinline__ void store_codes(uint8_t* p, uint32_t (&q)[code_words<FMT, 32>()], bool bad, int wide) {
+  if (bad) {                                 // rare
+#pragma unroll
+    for (int i = 0; i < code_words<FMT, 32>(); ++i) q[i] = 0u;
+  }
   if constexpr (FMT == MXQ_E2M1) {
     *reinterpret_cast<uint4*>(p) = make_uint4(q[0], q[1], q[2], q[3]);
   } else if (wide) {
@@ -49,75 +75,146 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&q)[code
   }
 }
 
-// One block of 32 values: codes to `dst`, scale byte returned.
+// A block of 32 neighbours in 16 words: codes to `dst`, scale byte returned.
 template <int FMT>
-__device__ __forceinline__ uint32_t encode(const float (&v)[32], int ceil_mode, uint8_t* dst, int wide) {
+__device__ __forceinline__ uint32_t encode_row(const uint32_t (&w)[16], int ceil_mode, uint8_t* dst, int wide) {
+  const uint32_t m = amax_words(w);
   float mult;
-  const uint32_t code = mx_scale<FMT>(amax32_tree([&](int j) { return fabsf(v[j]); }), ceil_mode, mult);
+  const uint32_t code = mx_scale<FMT>(max(mag_lo(m), mag_hi(m)), ceil_mode, mult);
   uint32_t q[code_words<FMT, 32>()];
-  mx_codes<FMT, 32>(v, mult, code == 0xFFu, q);
-  store_codes<FMT>(dst, q, wide);
+  if constexpr (FMT == MXQ_E2M1) {
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[2 * i] = bf16lo(w[i]), v[2 * i + 1] = bf16hi(w[i]);
+    mx_codes<FMT, 32>(v, mult, false, q);
+  } else {
+    const uint64_t mm = f32x2_splat(mult);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = fp8x4_rows<FMT>(w[2 * i], w[2 * i + 1], mm);
+  }
+  store_codes<FMT>(dst, q, code == 0xFFu, wide);
   return code;
 }
 
+// One of two neighbouring columns (the low or high halves of 32 words), of the
+// largest magnitude `ab`.
+template <int FMT, int HALF>
+__device__ __forceinline__ uint32_t encode_col(const uint32_t (&w)[32], uint32_t ab, int ceil_mode, uint8_t* dst, int wide) {
+  float mult;
+  const uint32_t code = mx_scale<FMT>(ab, ceil_mode, mult);
+  uint32_t q[code_words<FMT, 32>()];
+  if constexpr (FMT == MXQ_E2M1) {
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = HALF ? bf16hi(w[i]) : bf16lo(w[i]);
+    mx_codes<FMT, 32>(v, mult, false, q);
+  } else {
+    const uint64_t mm = f32x2_splat(mult);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = fp8x4_col<FMT, HALF>(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3], mm);
+  }
+  store_codes<FMT>(dst, q, code == 0xFFu, wide);
+  return code;
+}
+
+// A tile of padding: codes and scales of zeros are zeros.
 template <int FMT, int ORIENT>
-__global__ void __launch_bounds__(T) gather_mx_kernel(const GatherMx a) {
+__device__ __forceinline__ void zero_tile(const GatherMx& a, int64_t r0, int c0) {
+  constexpr int SH = FMT == MXQ_E2M1 ? 1 : 0;            // E2M1: half a byte to a code
+  const int cols = min(TILE, a.cols - c0);
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  if constexpr (ORIENT & MXQ_ROW) {
+    const int words = cols >> (4 + SH);                  // of a row
+    for (int i = threadIdx.x; i < TILE * words; i += T)
+      *reinterpret_cast<uint4*>(a.q_row + (((r0 + i / words) * a.cols + c0) >> SH) + i % words * 16) = z;
+    const int kb = a.cols / 32;
+    for (int i = threadIdx.x; i < TILE * (cols / 32); i += T)
+      a.s_row[scale_at(r0 + i % TILE, c0 / 32 + i / TILE, kb, a.mma)] = 0;
+  }
+  if constexpr (ORIENT & MXQ_COL) {
+    constexpr int WORDS = TILE >> (4 + SH);
+    for (int i = threadIdx.x; i < cols * WORDS; i += T)
+      *reinterpret_cast<uint4*>(a.q_col + (((c0 + i / WORDS) * a.rows + r0) >> SH) + i % WORDS * 16) = z;
+    for (int c = threadIdx.x; c < cols; c += T)
+      *reinterpret_cast<uint32_t*>(a.s_col + scale_at(c0 + c, r0 / 32, a.rows / 32, a.mma)) = 0u;
+  }
+}
+
+template <int FMT, int ORIENT>
+__global__ void __launch_bounds__(T, 3) gather_mx_kernel(const GatherMx a) {
   extern __shared__ __align__(16) uint8_t buf[];
+  __shared__ int token[2][TILE];                         // token of each row of a tile, -1: none
+  __shared__ uint32_t col_scales[TILE];
   grid_dep_launch();
   grid_dep_wait();
   const int tid = threadIdx.x;
-  const int ntiles = a.tiles_r * a.tiles_c;
+  const int ntiles = a.tiles_r * a.tiles_c, step = gridDim.x;
+  const int lc = (tid & 15) * 8, lr = tid >> 4;          // this thread's chunk of 16 bytes of rows lr, lr + 16, ...
 
-  // a row's 16 chunks of 16 bytes go to 16 neighbouring threads
+  const auto slot_of = [&](int tile) {
+    return tid < TILE && tile < ntiles ? a.row_slot[static_cast<int64_t>(tile / a.tiles_c) * TILE + tid] : -1;
+  };
+  // tokens of a tile's rows to place b; returns (after the barrier) whether it has any
+  const auto keep = [&](int slot, int b) {
+    const int t = slot < 0 ? -1 : slot / a.top;
+    if (tid < TILE) token[b][tid] = t < a.tokens ? t : -1;
+    return __syncthreads_or(t >= 0);
+  };
   const auto load = [&](int tile, int b) {
-    const int64_t r0 = static_cast<int64_t>(tile / a.tiles_c) * TILE;
-    const int c = (tile % a.tiles_c) * TILE + (tid & 15) * 8;
+    const int c = (tile % a.tiles_c) * TILE + lc;
+    const uint32_t dst = smem_u32(buf) + b * BUF + lr * PITCH + lc * 2;
 #pragma unroll
     for (int i = 0; i < TILE / 16; ++i) {
-      const int r = i * 16 + (tid >> 4);
-      const int slot = a.row_slot[r0 + r];
-      const int64_t token = slot / a.top;
-      const bool live = slot >= 0 && token < a.tokens && c < a.cols;
-      cp_async16(smem_u32(buf + b * BUF + r * PITCH + (tid & 15) * 16), live ? a.x + token * a.ld + c : a.x, live);
+      const int t = token[b][i * 16 + lr];
+      const bool live = t >= 0 && c < a.cols;
+      cp_async16(dst + i * 16 * PITCH, live ? a.x + t * a.ld + c : a.x, live);
     }
     cp_async_commit();
   };
 
-  int b = 0;
-  if (static_cast<int>(blockIdx.x) < ntiles) load(blockIdx.x, 0);
-  for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x, b ^= 1) {
-    const bool more = tile + static_cast<int>(gridDim.x) < ntiles;
-    if (more) {
-      load(tile + gridDim.x, b ^ 1);
-      cp_async_wait<1>();
-    } else {
-      cp_async_wait<0>();
-    }
+  int tile = blockIdx.x, b = 0;
+  bool live = keep(slot_of(tile), 0), live_next = keep(slot_of(tile + step), 1);
+  if (live) load(tile, 0);
+  else cp_async_commit();
+  for (; tile < ntiles; tile += step, b ^= 1) {
+    const int ahead = slot_of(tile + 2 * step);
+    if (live_next) load(tile + step, b ^ 1);
+    else cp_async_commit();
+    cp_async_wait<1>();
     __syncthreads();
     const uint8_t* const t = buf + b * BUF;
     const int64_t r0 = static_cast<int64_t>(tile / a.tiles_c) * TILE;
     const int c0 = (tile % a.tiles_c) * TILE;
+    if (!live) {
+      zero_tile<FMT, ORIENT>(a, r0, c0);
+      live = live_next, live_next = keep(ahead, b);
+      continue;
+    }
     if constexpr (ORIENT & MXQ_ROW) {
-      // a thread takes two neighbouring blocks of a row
-      const int r = tid >> 1, h = (tid & 1) * 2;
+      // a thread takes every other block of a row
+      const int r = tid >> 1, h = tid & 1;
       const int64_t row = r0 + r;
       const int kb = a.cols / 32;
+      uint32_t scales = 0;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int c = c0 + (h + k) * 32;
+        const int c = c0 + (h + 2 * k) * 32;
         if (c < a.cols) {
-          float v[32];
+          uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint4 w = *reinterpret_cast<const uint4*>(t + r * PITCH + (h + k) * 64 + i * 16);
-            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[8 * i + 2 * j] = bf16lo(q[j]), v[8 * i + 2 * j + 1] = bf16hi(q[j]);
+            const uint4 q = *reinterpret_cast<const uint4*>(t + r * PITCH + (h + 2 * k) * 64 + i * 16);
+            w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
           }
           const int64_t el = row * a.cols + c;
-          const uint32_t s = encode<FMT>(v, a.ceil_mode, a.q_row + (FMT == MXQ_E2M1 ? el / 2 : el), a.wide);
-          a.s_row[scale_at(row, c / 32, kb, a.mma)] = static_cast<uint8_t>(s);
+          const uint32_t s = encode_row<FMT>(w, a.ceil_mode, a.q_row + (FMT == MXQ_E2M1 ? el / 2 : el), a.wide);
+          if (!a.mma) a.s_row[row * kb + c / 32] = static_cast<uint8_t>(s);
+          scales |= s << (8 * (h + 2 * k));
         }
+      }
+      if (a.mma) {                                       // whole tiles: the four scales of a row as one word
+        scales |= __shfl_xor_sync(0xFFFFFFFFu, scales, 1);
+        if (!h) *reinterpret_cast<uint32_t*>(a.s_row + scale_at(row, c0 / 32, kb, 1)) = scales;
       }
     }
     if constexpr (ORIENT & MXQ_COL) {
@@ -128,20 +225,24 @@ __global__ void __launch_bounds__(T) gather_mx_kernel(const GatherMx a) {
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) w[i] = *reinterpret_cast<const uint32_t*>(t + (rb * 32 + i) * PITCH + cp * 4);
-        const int64_t row = r0 + rb * 32;
-        const int64_t kb = a.rows / 32;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float v[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = k ? bf16hi(w[i]) : bf16lo(w[i]);
-          const int64_t el = (c + k) * a.rows + row;
-          const uint32_t s = encode<FMT>(v, a.ceil_mode, a.q_col + (FMT == MXQ_E2M1 ? el / 2 : el), a.wide);
-          a.s_col[scale_at(c + k, row / 32, kb, a.mma)] = static_cast<uint8_t>(s);
-        }
+        const uint32_t m = amax_words(w);
+        const int64_t el = c * a.rows + r0 + rb * 32;
+        uint8_t* const dst = a.q_col + (FMT == MXQ_E2M1 ? el / 2 : el);
+        const int64_t next = FMT == MXQ_E2M1 ? a.rows / 2 : a.rows;
+        const uint32_t s0 = encode_col<FMT, 0>(w, mag_lo(m), a.ceil_mode, dst, a.wide);
+        const uint32_t s1 = encode_col<FMT, 1>(w, mag_hi(m), a.ceil_mode, dst + next, a.wide);
+        uint8_t* const sc = reinterpret_cast<uint8_t*>(col_scales + 2 * cp) + rb;
+        sc[0] = static_cast<uint8_t>(s0);
+        sc[4] = static_cast<uint8_t>(s1);
       }
     }
-    __syncthreads();
+    live = live_next, live_next = keep(ahead, b);
+    if constexpr (ORIENT & MXQ_COL) {
+      // a column's four scales side by side, in either layout (rows are whole tiles)
+      const int c = c0 + tid;
+      if (tid < TILE && c < a.cols)
+        *reinterpret_cast<uint32_t*>(a.s_col + scale_at(c, r0 / 32, a.rows / 32, a.mma)) = col_scales[tid];
+    }
   }
 }
 
@@ -192,6 +293,8 @@ extern "C" int mxq_expert_gather_mx(const void* x, int64_t tokens, int64_t cols,
   if ((orient & MXQ_COL) && (!q_col || !s_col)) return MXQ_ERR_BAD_ARG;
   if (!aligned16(x) || ld % 8 || !aligned_to(row_slot, 4)) return MXQ_ERR_MISALIGNED;
   if (((orient & MXQ_ROW) && !aligned16(q_row)) || ((orient & MXQ_COL) && !aligned16(q_col))) return MXQ_ERR_MISALIGNED;
+  if (((orient & MXQ_ROW) && sf_layout == MXQ_SF_MMA && !aligned16(s_row)) || ((orient & MXQ_COL) && !aligned16(s_col)))
+    return MXQ_ERR_MISALIGNED;
   if (!device_ok()) return MXQ_ERR_UNSUPPORTED;
   GatherMx a{};
   a.x = static_cast<const __nv_bfloat16*>(x);

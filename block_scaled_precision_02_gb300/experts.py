@@ -5,7 +5,7 @@ marshalling only, as in the package."""
 
 from __future__ import annotations
 
-from typing import NamedTuple, Optional
+from typing import Optional
 
 import torch
 
@@ -14,65 +14,78 @@ from . import (_FMT, _ORIENT, _PARAM, _SCALE, _SF, _TYPE, COL, E2M1, ROW, _byte_
 
 MAX_EXPERTS = 1024
 _LIMIT = 2 ** 31 - 2 ** 16
+_INDEX = {torch.int32: 0, torch.int64: 1}
 
 
-class ExpertPlan(NamedTuple):
-    """Where expert_sort puts every slot (slot s = token * top + j): int32
-    device tensors, with the sizes that the host knows."""
-    offsets: torch.Tensor        # [experts + 1] first row of each expert's stretch, and the end of the last
-    counts: torch.Tensor         # [experts] slots of each expert
-    slot_row: torch.Tensor       # [tokens][top] row of each slot, -1 where it is dropped
-    row_slot: torch.Tensor       # [rows] slot of each row, -1 in padding
-    block_expert: torch.Tensor   # [rows / align] expert of each block of rows, -1 behind the last stretch
-    tokens: int
-    top: int
-    experts: int
-    rows: int                    # rows of gathered tensors: enough for any routing of this size
-    align: int
+class ExpertPlan:
+    """Where expert_sort puts every slot (slot s = token * top + j).
+
+    tokens, top, experts, align   as given
+    rows          rows of gathered tensors: enough for any routing of this size
+    and int32 tensors, parts of one allocation:
+    offsets       [experts + 1] first row of each expert's stretch, and the end of the last
+    counts        [experts] slots of each expert
+    slot_row      [tokens][top] row of each slot, -1 where it is dropped
+    row_slot      [rows] slot of each row, -1 in padding and behind the last stretch
+    block_expert  [rows / align] expert of each block of rows, -1 behind the last stretch"""
+
+    __slots__ = ("_buffer", "_at", "_pointers", "tokens", "top", "experts", "rows", "align")
+
+    def __init__(self, tokens: int, top: int, experts: int, align: int, device):
+        slots = tokens * top
+        rows = (slots + min(experts, slots) * (align - 1)) // align * align
+        if rows > _LIMIT:
+            raise ValueError("too many slots")
+        at = [0]
+        for n in (experts + 1, experts, slots, rows, rows // align):
+            at.append(at[-1] + n)
+        at[-1] = (at[-1] + 3) // 4 * 4                   # the sort's workspace follows, at 16 bytes
+        work = _size("mxq_expert_sort_workspace_size", device, slots, experts)
+        self._buffer = torch.empty(at[-1] + (work + 3) // 4, dtype=torch.int32, device=device)
+        base = self._buffer.data_ptr()
+        self._at, self._pointers = at, [base + 4 * n for n in at]
+        self.tokens, self.top, self.experts, self.rows, self.align = tokens, top, experts, rows, align
+
+    def _part(self, k: int, n: int) -> torch.Tensor:
+        return self._buffer[self._at[k]:self._at[k] + n]
+
+    offsets = property(lambda self: self._part(0, self.experts + 1))
+    counts = property(lambda self: self._part(1, self.experts))
+    slot_row = property(lambda self: self._part(2, self.tokens * self.top).view(self.tokens, self.top))
+    row_slot = property(lambda self: self._part(3, self.rows))
+    block_expert = property(lambda self: self._part(4, self.rows // self.align))
 
 
-def expert_sort(experts: torch.Tensor, num_experts: int, align: int = 128) -> ExpertPlan:
+def expert_sort(experts: torch.Tensor, num_experts: int, align: Optional[int] = None) -> ExpertPlan:
     """Sort the slots of a routing ``experts`` [tokens][top] (int32 or int64) by
     expert.  An expert's slots keep their order; its rows start at a multiple
-    of ``align`` (128, or 256 for the products' larger tiles: worth it from about
-    256 slots an expert).  An index outside [0, num_experts) drops the slot."""
-    if not isinstance(experts, torch.Tensor) or experts.dtype not in (torch.int32, torch.int64):
+    of ``align``: 128, or 256 for the products' larger tiles (the default from
+    256 slots an expert on, where they outweigh the longer padding).  An index
+    outside [0, num_experts) drops the slot."""
+    if not isinstance(experts, torch.Tensor) or experts.dtype not in _INDEX:
         raise ValueError("experts must be an int32 or int64 tensor")
     if experts.dim() != 2 or experts.shape[1] < 1 or not experts.is_contiguous():
         raise ValueError("experts must be a contiguous [tokens][top] tensor")
     if not 1 <= num_experts <= MAX_EXPERTS:
         raise ValueError(f"num_experts must lie in 1 .. {MAX_EXPERTS}")
-    if align not in (128, 256):
-        raise ValueError("align must be 128 or 256")
     tokens, top = experts.shape
-    slots = tokens * top
-    rows = (slots + min(num_experts, slots) * (align - 1)) // align * align
-    if rows > _LIMIT:
+    if align is None:
+        align = 256 if tokens * top >= 256 * num_experts else 128
+    elif align not in (128, 256):
+        raise ValueError("align must be 128 or 256")
+    if tokens * top > _LIMIT:
         raise ValueError("too many slots")
     dev = _same_device("experts", experts)
-    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
-    counts = torch.empty(num_experts, dtype=torch.int32, device=dev)
-    slot_row = torch.empty(tokens, top, dtype=torch.int32, device=dev)
-    row_slot = torch.empty(rows, dtype=torch.int32, device=dev)
-    block_expert = torch.empty(rows // align, dtype=torch.int32, device=dev)
-    need = _size("mxq_expert_sort_workspace_size", dev, slots, num_experts)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch("mxq_expert_sort", dev, experts.data_ptr(), int(experts.dtype == torch.int64), slots, num_experts, align, rows,
-            offsets.data_ptr(), counts.data_ptr(), slot_row.data_ptr(), row_slot.data_ptr(), block_expert.data_ptr(),
-            ws.data_ptr(), need)
-    return ExpertPlan(offsets, counts, slot_row, row_slot, block_expert, tokens, top, num_experts, rows, align)
+    plan = ExpertPlan(tokens, top, num_experts, align, dev)
+    at = plan._pointers
+    _launch("mxq_expert_sort", dev, experts.data_ptr(), _INDEX[experts.dtype], tokens * top, num_experts, align, plan.rows,
+            *at, 4 * (plan._buffer.numel() - plan._at[-1]))
+    return plan
 
 
 def _plan(plan) -> ExpertPlan:
-    """A plan whose tensors hold what its sizes say (they reach kernels as pointers)."""
-    if not isinstance(plan, ExpertPlan):
+    if type(plan) is not ExpertPlan:
         raise ValueError("plan must be what expert_sort returned")
-    for t, n, name in ((plan.offsets, plan.experts + 1, "offsets"), (plan.slot_row, plan.tokens * plan.top, "slot_row"),
-                       (plan.row_slot, plan.rows, "row_slot"), (plan.block_expert, plan.rows // plan.align, "block_expert")):
-        if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"plan.{name} must be a contiguous int32 tensor of {n} elements")
-        if t.get_device() != plan.offsets.get_device():
-            raise ValueError(f"plan.{name} is on {t.device}, plan.offsets on {plan.offsets.device}")
     return plan
 
 
@@ -98,10 +111,11 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan) -> torch.Tensor:
     slots, zeros in padding.  Its backward pass is expert_combine(drows, plan)."""
     plan = _plan(plan)
     xt, cols, ld = _rows_of(x, "x", plan.tokens, "tokens")
-    dev = _same_device("x plan", x, plan.row_slot)
+    dev = _same_device("x plan", x, plan._buffer)
     out = torch.empty(plan.rows, cols, dtype=x.dtype, device=dev)
-    _launch("mxq_expert_gather", dev, x.data_ptr(), plan.tokens, cols, ld, xt, plan.slot_row.data_ptr(), plan.top,
-            plan.row_slot.data_ptr(), plan.rows, out.data_ptr())
+    at = plan._pointers
+    _launch("mxq_expert_gather", dev, x.data_ptr(), plan.tokens, cols, ld, xt, at[2], plan.top, at[0], at[1], plan.experts,
+            plan.rows, out.data_ptr())
     return out
 
 
@@ -117,7 +131,7 @@ def mx_expert_gather(x: torch.Tensor, plan: ExpertPlan, fmt="e4m3", orientation=
     _, cols, ld = _rows_of(x, "x", plan.tokens, "tokens")
     if x.dtype != torch.bfloat16:
         raise ValueError("x must be bf16 with a contiguous last dimension")
-    dev = _same_device("x plan", x, plan.row_slot)
+    dev = _same_device("x plan", x, plan._buffer)
     rows, qb = plan.rows, 2 if f == E2M1 else 1
     q_row = s_row = q_col = s_col = None
     rp = rs = cp = cs = 0
@@ -129,7 +143,7 @@ def mx_expert_gather(x: torch.Tensor, plan: ExpertPlan, fmt="e4m3", orientation=
         q_col = torch.empty(cols, rows // qb, dtype=torch.uint8, device=dev)
         s_col = torch.empty(cols, rows // 32, dtype=torch.uint8, device=dev)
         cp, cs = q_col.data_ptr(), s_col.data_ptr()
-    _launch("mxq_expert_gather_mx", dev, x.data_ptr(), plan.tokens, cols, ld, plan.row_slot.data_ptr(), rows, plan.top, f, o,
+    _launch("mxq_expert_gather_mx", dev, x.data_ptr(), plan.tokens, cols, ld, plan._pointers[3], rows, plan.top, f, o,
             sm, sf, rp, rs, cp, cs)
     return q_row, s_row, q_col, s_col
 
@@ -146,9 +160,9 @@ def expert_combine(rows: torch.Tensor, plan: ExpertPlan, weights: Optional[torch
     out_dtype = rows.dtype if out_dtype is None else out_dtype
     if out_dtype not in _TYPE:
         raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
-    dev = _same_device("rows plan weights", rows, plan.slot_row, weights)
+    dev = _same_device("rows plan weights", rows, plan._buffer, weights)
     y = torch.empty(plan.tokens, cols, dtype=out_dtype, device=dev)
-    _launch("mxq_expert_combine", dev, rows.data_ptr(), plan.rows, cols, ld, t, plan.slot_row.data_ptr(), plan.tokens,
+    _launch("mxq_expert_combine", dev, rows.data_ptr(), plan.rows, cols, ld, t, plan._pointers[2], plan.tokens,
             plan.top, w, wt, y.data_ptr(), _TYPE[out_dtype])
     return y
 
@@ -164,12 +178,12 @@ def expert_combine_backward(dy: torch.Tensor, rows: torch.Tensor, plan: ExpertPl
     if rcols != cols:
         raise ValueError(f"dy has {cols} columns, rows {rcols}")
     w, wt = _gate(weights, plan)
-    dev = _same_device("rows dy plan weights", rows, dy, plan.slot_row, weights)
+    dev = _same_device("rows dy plan weights", rows, dy, plan._buffer, weights)
     drows = torch.empty(plan.rows, cols, dtype=rows.dtype, device=dev)
     dw = torch.empty(plan.tokens, plan.top, dtype=torch.float32, device=dev)
+    at = plan._pointers
     _launch("mxq_expert_combine_backward", dev, dy.data_ptr(), ld_dy, dt, rows.data_ptr(), ld, t, plan.rows, cols,
-            plan.slot_row.data_ptr(), plan.row_slot.data_ptr(), plan.tokens, plan.top, w, wt, drows.data_ptr(),
-            dw.data_ptr())
+            at[2], plan.tokens, plan.top, at[0], at[1], plan.experts, w, wt, drows.data_ptr(), dw.data_ptr())
     return drows, dw
 
 
@@ -207,10 +221,10 @@ def mx_expert_gemm(a_q: torch.Tensor, a_s: torch.Tensor, b_q: torch.Tensor, b_s:
         raise ValueError(f"b_q holds {b_shape[0]} experts, the plan {plan.experts}")
     if b_shape[-1] != (plan.experts * K if along_k else K):
         raise ValueError(f"K differs: a_q holds {K}, b_q {b_shape[-1]}" + (f" for {plan.experts} experts" if along_k else ""))
-    dev = _same_device("a_q a_s b_q b_s plan", a_q, a_s, b_q, b_s, plan.offsets)
+    dev = _same_device("a_q a_s b_q b_s plan", a_q, a_s, b_q, b_s, plan._buffer)
     c = torch.empty(R, N, dtype=out_dtype, device=dev)
     _launch("mxq_expert_gemm", dev, a_q.data_ptr(), a_s.data_ptr(), f, b_q.data_ptr(), b_s.data_ptr(), fb, R, N, K,
-            plan.experts, plan.align, plan.offsets.data_ptr(), plan.block_expert.data_ptr(), int(along_k), c.data_ptr(),
+            plan.experts, plan.align, plan._pointers[0], plan._pointers[4], int(along_k), c.data_ptr(),
             int(out_dtype == torch.float32))
     return c
 
@@ -232,8 +246,8 @@ def mx_expert_wgrad(a_q: torch.Tensor, a_s: torch.Tensor, b_q: torch.Tensor, b_s
     for n, name in ((ra, "a_q"), (rb, "b_q")):
         if n != plan.rows:
             raise ValueError(f"{name} holds {n} rows, the plan {plan.rows}")
-    dev = _same_device("a_q a_s b_q b_s plan", a_q, a_s, b_q, b_s, plan.offsets)
+    dev = _same_device("a_q a_s b_q b_s plan", a_q, a_s, b_q, b_s, plan._buffer)
     c = torch.empty(plan.experts, N, K, dtype=out_dtype, device=dev)
     _launch("mxq_expert_wgrad", dev, a_q.data_ptr(), a_s.data_ptr(), f, b_q.data_ptr(), b_s.data_ptr(), fb, plan.rows, N, K,
-            plan.experts, plan.align, plan.offsets.data_ptr(), c.data_ptr(), int(out_dtype == torch.float32))
+            plan.experts, plan.align, plan._pointers[0], c.data_ptr(), int(out_dtype == torch.float32))
     return c

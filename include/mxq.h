@@ -486,23 +486,23 @@ int mxq_expert_sort(const void* experts, int experts_64, int64_t slots,
                     size_t workspace_bytes, void* stream);
 
 /* ---- gather by expert --------------------------------------------------------------
- * out[r] = x[row_slot[r] / top], 0 where row_slot[r] is -1: every row is
- * written.  Its backward pass is mxq_expert_combine without weights.
+ * out[slot_row[t top + j]] = x[t], 0 in the padding after each expert's counts[e]
+ * rows and behind the last stretch: every row is written.  Its backward pass is mxq_expert_combine without weights.
  * x        [tokens][ld] of x_type, the first cols of a row read; out
  *          [rows][cols] of the same type, bit for bit (16-byte aligned rows of
  *          a multiple of 16 bytes run faster).
- * slot_row, row_slot, top, rows  of the plan (slots = tokens * top). */
+ * slot_row, top, offsets, counts, experts, rows  of the plan (slots = tokens * top). */
 int mxq_expert_gather(const void* x, int64_t tokens, int64_t cols, int64_t ld,
                       int x_type, const int32_t* slot_row, int64_t top,
-                      const int32_t* row_slot, int64_t rows, void* out,
-                      void* stream);
+                      const int32_t* offsets, const int32_t* counts,
+                      int experts, int64_t rows, void* out, void* stream);
 
 /* ---- gather by expert straight to MX ([FAF]) ----------------------------------------
  * Bit for bit what mxq_quantize (RNE, no Hadamard) writes for the gathered
  * rows, which are not written themselves.
  * x        bf16 [tokens][ld], 16-byte aligned, ld % 8 == 0; tokens >= 1 if rows.
  * rows     a multiple of 128; cols a multiple of 32 (128 for MXQ_SF_MMA).
- * fmt .. s_col  as mxq_quantize. */
+ * fmt .. s_col  as mxq_quantize (outputs 16-byte aligned). */
 int mxq_expert_gather_mx(const void* x, int64_t tokens, int64_t cols, int64_t ld,
                          const int32_t* row_slot, int64_t rows, int64_t top,
                          int fmt, int orient, int scale_mode, int sf_layout,
@@ -551,7 +551,7 @@ int mxq_expert_combine(const void* rows_in, int64_t rows, int64_t cols,
                        int w_type, void* y, int y_type, void* stream);
 
 /* Its gradients:
- *   drows[slot_row[s]] = w[s] dy[t], rounded once, 0 where row_slot is -1
+ *   drows[slot_row[s]] = w[s] dy[t], rounded once, 0 in padding
  *   dweights[s] = sum over c of dy[t][c] rows_in[slot_row[s]][c] in float32, 0
  *                 for a dropped slot
  * dy       [tokens][ld_dy] of dy_type; drows [rows][cols] of type; must overlap
@@ -560,10 +560,11 @@ int mxq_expert_combine(const void* rows_in, int64_t rows, int64_t cols,
 int mxq_expert_combine_backward(const void* dy, int64_t ld_dy, int dy_type,
                                 const void* rows_in, int64_t ld, int type,
                                 int64_t rows, int64_t cols,
-                                const int32_t* slot_row,
-                                const int32_t* row_slot, int64_t tokens,
-                                int64_t top, const void* weights, int w_type,
-                                void* drows, float* dweights, void* stream);
+                                const int32_t* slot_row, int64_t tokens,
+                                int64_t top, const int32_t* offsets,
+                                const int32_t* counts, int experts,
+                                const void* weights, int w_type, void* drows,
+                                float* dweights, void* stream);
 
 /* ---- dropout ------------------------------------------------------------------------------
  * y[i] = residual[i] + [u_i >= t] x[i] / (1 - p), t = p 2^32 to the nearest

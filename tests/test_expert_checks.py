@@ -20,10 +20,13 @@ def z(*shape, dtype=F32):
 
 
 def plan(tokens=4, top=2, experts=3, align=128):
+    """A plan in host memory: only what a call checks before it needs a device."""
+    p = object.__new__(mxq.ExpertPlan)
     slots = tokens * top
-    rows = (slots + min(experts, slots) * (align - 1)) // align * align
-    return mxq.ExpertPlan(z(experts + 1, dtype=I32), z(experts, dtype=I32), z(tokens, top, dtype=I32), z(rows, dtype=I32),
-                          z(rows // align, dtype=I32), tokens, top, experts, rows, align)
+    p.tokens, p.top, p.experts, p.align = tokens, top, experts, align
+    p.rows = (slots + min(experts, slots) * (align - 1)) // align * align
+    p._at, p._buffer, p._pointers = [0] * 6, z(1, dtype=I32), [0] * 6
+    return p
 
 
 @pytest.fixture(scope="module")
@@ -51,14 +54,13 @@ def test_sort_checks():
 
 
 def test_plan_checks():
-    p = plan()
-    with pytest.raises(ValueError, match="what expert_sort returned"):
-        mxq.expert_gather(z(4, 8), tuple(p))
-    for bad in (p._replace(offsets=z(3, dtype=I32)), p._replace(row_slot=z(p.rows - 1, dtype=I32)),
-                p._replace(slot_row=z(4, 2)), p._replace(rows=p.rows + 128), p._replace(experts=4),
-                p._replace(block_expert=z(2 * (p.rows // 128), dtype=I32)[::2])):
-        with pytest.raises(ValueError, match="plan"):
-            mxq.expert_gather(z(4, 8), bad)
+    for bad in (None, (1, 2, 3), z(4)):
+        for call in (lambda: mxq.expert_gather(z(4, 8), bad), lambda: mxq.expert_combine(z(4, 8), bad),
+                     lambda: mxq.mx_expert_gather(z(4, 8), bad), lambda: mxq.expert_combine_backward(z(4, 8), z(4, 8), bad, z(4, 2)),
+                     lambda: mxq.mx_expert_gemm(z(4, 8), z(1), z(1), z(1), bad),
+                     lambda: mxq.mx_expert_wgrad(z(4, 8), z(1), z(1), z(1), bad)):
+            with pytest.raises(ValueError, match="what expert_sort returned"):
+                call()
 
 
 def test_row_calls_checks():
@@ -156,7 +158,7 @@ def test_c_sort(so):
     ok = [P, 0, 9, 8, 128, 1024, P, P, P, P, P, P, 1 << 20, None]
     assert so.mxq_expert_sort(*ok) == NO_DEVICE
     for at, bad, want in ((1, 2, BAD_ARG), (5, 1152, BAD_SHAPE), (0, None, BAD_ARG), (6, None, BAD_ARG), (9, None, BAD_ARG),
-                          (11, None, BAD_ARG), (12, 16, BAD_ARG), (0, 0x10002, MISALIGNED), (8, ODD, MISALIGNED),
+                          (11, None, BAD_ARG), (12, 8, BAD_ARG), (0, 0x10002, MISALIGNED), (8, ODD, MISALIGNED),
                           (11, 0x10008, MISALIGNED)):
         assert so.mxq_expert_sort(*[bad if i == at else v for i, v in enumerate(ok)]) == want, at
 
@@ -167,21 +169,22 @@ def test_c_rows(so):
         for at, bad, want in cases:
             assert fn(*[bad if i == at else v for i, v in enumerate(ok)]) == want, at
 
-    each(so.mxq_expert_gather, [P, 4, 8, 8, 1, P, 2, P, 384, P, None],
+    each(so.mxq_expert_gather, [P, 4, 8, 8, 1, P, 2, P, P, 3, 384, P, None],
          ((4, 2, BAD_ARG), (1, -1, BAD_SHAPE), (2, 0, BAD_SHAPE), (3, 7, BAD_SHAPE), (6, 0, BAD_SHAPE), (0, None, BAD_ARG),
-          (5, None, BAD_ARG), (7, None, BAD_ARG), (9, None, BAD_ARG), (0, 0x10002, MISALIGNED), (9, ODD, MISALIGNED),
-          (1, 2 ** 30, BAD_SHAPE)))
+          (5, None, BAD_ARG), (7, None, BAD_ARG), (8, None, BAD_ARG), (9, 0, BAD_SHAPE), (9, 1025, BAD_SHAPE), (11, None, BAD_ARG),
+          (0, 0x10002, MISALIGNED), (11, ODD, MISALIGNED), (7, ODD, MISALIGNED), (1, 2 ** 30, BAD_SHAPE)))
     each(so.mxq_expert_gather_mx, [P, 4, 128, 128, P, 384, 2, 0, 3, 0, 1, P, P, P, P, None],
          ((7, 3, BAD_ARG), (8, 0, BAD_ARG), (9, 2, BAD_ARG), (10, 2, BAD_ARG), (5, 32, BAD_SHAPE), (2, 160, BAD_SHAPE),
           (3, 64, BAD_SHAPE), (3, 132, MISALIGNED), (0, 0x10008, MISALIGNED), (11, 0x10008, MISALIGNED), (13, 0x10008, MISALIGNED),
-          (0, None, BAD_ARG), (4, None, BAD_ARG), (12, None, BAD_ARG), (14, None, BAD_ARG)))
+          (0, None, BAD_ARG), (4, None, BAD_ARG), (12, None, BAD_ARG), (14, None, BAD_ARG),
+          (12, 0x10008, MISALIGNED), (14, 0x10008, MISALIGNED)))
     each(so.mxq_expert_combine, [P, 384, 8, 8, 1, P, 4, 2, P, 1, P, 0, None],
          ((4, 2, BAD_ARG), (9, 2, BAD_ARG), (11, 2, BAD_ARG), (2, 0, BAD_SHAPE), (3, 7, BAD_SHAPE), (0, None, BAD_ARG),
           (5, None, BAD_ARG), (10, None, BAD_ARG), (8, 0x10002, MISALIGNED), (10, ODD, MISALIGNED)))
-    each(so.mxq_expert_combine_backward, [P, 8, 0, P, 8, 1, 384, 8, P, P, 4, 2, P, 1, P, P, None],
-         ((1, 7, BAD_SHAPE), (4, 7, BAD_SHAPE), (2, 2, BAD_ARG), (5, 2, BAD_ARG), (13, 2, BAD_ARG), (0, None, BAD_ARG),
-          (3, None, BAD_ARG), (8, None, BAD_ARG), (9, None, BAD_ARG), (12, None, BAD_ARG), (14, None, BAD_ARG),
-          (15, None, BAD_ARG), (0, ODD, MISALIGNED), (15, 0x10002, MISALIGNED)))
+    each(so.mxq_expert_combine_backward, [P, 8, 0, P, 8, 1, 384, 8, P, 4, 2, P, P, 3, P, 1, P, P, None],
+         ((1, 7, BAD_SHAPE), (4, 7, BAD_SHAPE), (2, 2, BAD_ARG), (5, 2, BAD_ARG), (15, 2, BAD_ARG), (0, None, BAD_ARG),
+          (3, None, BAD_ARG), (8, None, BAD_ARG), (11, None, BAD_ARG), (12, None, BAD_ARG), (13, 0, BAD_SHAPE), (14, None, BAD_ARG),
+          (16, None, BAD_ARG), (17, None, BAD_ARG), (0, ODD, MISALIGNED), (17, 0x10002, MISALIGNED)))
     each(so.mxq_dropout, [P, 4, 8, 8, 0, P, 8, 0.1, 1, 2, P, P, None],
          ((4, 2, BAD_ARG), (7, 1.0, BAD_ARG), (7, float("nan"), BAD_ARG), (1, -1, BAD_SHAPE), (2, 0, BAD_SHAPE), (3, 7, BAD_SHAPE),
           (6, 7, BAD_SHAPE), (0, None, BAD_ARG), (11, None, BAD_ARG), (0, ODD, MISALIGNED), (10, 0x10004, MISALIGNED)))

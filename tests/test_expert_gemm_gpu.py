@@ -153,11 +153,11 @@ def test_a_wrong_plan_stays_within_bounds(lib):
     aq, as_ = integer_operand(rng, p.rows, 128, "e4m3")
     bq, bs = integer_operand(rng, 4 * 128, 128, "e4m3")
     gq, gs = integer_operand(rng, 128, p.rows, "e4m3")
-    big = 2 ** 31 - 1
-    for off, block in ((torch.full_like(p.offsets, big), torch.full_like(p.block_expert, big)),
-                       (torch.full_like(p.offsets, -big), torch.full_like(p.block_expert, -big)),
-                       (p.offsets.flip(0).contiguous(), p.block_expert.flip(0).contiguous())):
-        bad = p._replace(offsets=off, block_expert=block)
-        lib.mx_expert_gemm(aq, as_, bq.view(4, 128, 128), bs, bad)
-        lib.mx_expert_wgrad(gq, gs, gq, gs, bad)
+    off, block, big = p.offsets.clone(), p.block_expert.clone(), 2 ** 31 - 1
+    for o, b in ((torch.full_like(off, big), torch.full_like(block, big)), (torch.full_like(off, -big), torch.full_like(block, -big)),
+                 (off.flip(0), block.flip(0)), (off, torch.full_like(block, 1))):
+        p.offsets.copy_(o)
+        p.block_expert.copy_(b)
+        lib.mx_expert_gemm(aq, as_, bq.view(4, 128, 128), bs, p)
+        lib.mx_expert_wgrad(gq, gs, gq, gs, p)
     assert lib.last_device_status() == 0

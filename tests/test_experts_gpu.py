@@ -27,14 +27,21 @@ def np64(t):
 # ------------------------------------------------------------------ sort
 @pytest.mark.parametrize("pattern", PATTERNS)
 @pytest.mark.parametrize("tokens,top,experts", [(1, 1, 1), (1, 8, 64), (3, 2, 7), (100, 3, 5), (515, 2, 16), (2048, 1, 1024),
-                                                (2049, 1, 2), (4097, 5, 33), (5000, 8, 1000), (300000, 1, 128)])
+                                                (2049, 1, 2), (4097, 5, 33), (5000, 8, 1000), (8192, 8, 64), (65537, 1, 20), (300000, 1, 128)])
 def test_sort(lib, tokens, top, experts, pattern):
     rng = np.random.default_rng(tokens + experts)
     for align, dtype in ((128, torch.int32), (256, torch.int64)):
         got, want = make_plan(lib, rng, tokens, top, experts, pattern, align, dtype)
-        for t, w, name in zip(got[:5], (want[0], want[1], want[2], want[3], want[4]), got._fields):
+        for name, w in zip(("offsets", "counts", "slot_row", "row_slot", "block_expert"), want):
+            t = getattr(got, name)
             assert t.dtype == torch.int32 and np.array_equal(t.cpu().numpy(), w), name
-        assert got.rows == len(want[3]) and got[5:] == (tokens, top, experts, got.rows, align)
+        assert (got.tokens, got.top, got.experts, got.rows, got.align) == (tokens, top, experts, len(want[3]), align)
+
+
+def test_alignment_by_default(lib):
+    """Longer blocks from 256 slots an expert on."""
+    for tokens, want in ((1, 128), (511, 128), (512, 256), (4000, 256)):
+        assert lib.expert_sort(torch.zeros(tokens, 1, dtype=torch.int32, device=dev), 2).align == want
 
 
 def test_sort_of_values_beyond_32_bits(lib):
@@ -258,12 +265,17 @@ def test_a_wrong_plan_reads_and_writes_within_bounds(lib):
     """Indices beyond the rows or tokens are passed over (a plan changed by hand)."""
     rng = np.random.default_rng(6)
     p, _ = make_plan(lib, rng, 16, 2, 4)
-    bad = p._replace(slot_row=torch.full_like(p.slot_row, 2 ** 31 - 1), row_slot=torch.full_like(p.row_slot, 2 ** 31 - 1))
+    p.slot_row.fill_(2 ** 31 - 1)
+    p.row_slot.fill_(2 ** 31 - 1)
+    for off, n in ((2 ** 31 - 1, 2 ** 31 - 1), (-(2 ** 31), -(2 ** 31)), (2 ** 31 - 1, -(2 ** 31)), (64, -65)):
+        p.offsets.fill_(off)
+        p.counts.fill_(n)
+        lib.expert_gather(torch.zeros(16, 129, device=dev), p)
     rows = torch.randn(p.rows, 128, device=dev).to(BF)
-    assert not lib.expert_combine(rows, bad).any()
-    _, dw = lib.expert_combine_backward(rows[:16], rows, bad, torch.ones(16, 2, device=dev))
+    assert not lib.expert_combine(rows, p).any()
+    _, dw = lib.expert_combine_backward(rows[:16], rows, p, torch.ones(16, 2, device=dev))
     assert not dw.any()
-    lib.expert_gather(rows[:16], bad)
-    q = lib.mx_expert_gather(rows[:16], bad, "e4m3", "dual")
+    lib.expert_gather(rows[:16], p)
+    q = lib.mx_expert_gather(rows[:16], p, "e4m3", "dual")
     assert not q[0].any() and not q[2].any()
     torch.cuda.synchronize()
