@@ -7,11 +7,12 @@
 //
 // A tile is 128 CTAS x BN of C.  CTAS == 2: a pair of CTAs on two SMs computes
 // 256 x 256 with tcgen05.mma.cta_group::2, each holding its 128 rows of A and
-// half of B.  CTAS == 1: 128 x 128, with two accumulators in tensor memory, so
-// that one drains while the other fills.
+// half of B.  CTAS == 1: 128 x 256, or 128 x 128 with two accumulators in tensor
+// memory, one of which drains while the other fills.
 // Roles (one CTA per SM, persistent over tiles), as in the plain products:
 // warp 0 loads by TMA into a ring of stages, warp 6 copies the stages' scales
-// to tensor memory, warp 1 issues the MMAs, warps 2-5 store.
+// to tensor memory, warp 1 issues the MMAs; warps 2-5, and 7-10 where a tile
+// has 256 columns, store 128 columns each.
 // Order of tiles: expert by expert, down the rows first, so that an expert's
 // weights stream through once while its rows stay in L2.
 #include <algorithm>
@@ -25,7 +26,6 @@ namespace egemm {
 using namespace gemm;
 
 constexpr int PRODUCT = 0, WGRAD = 1;
-constexpr int THREADS = 224;
 
 struct Params {
   const int32_t* offsets;         // [E + 1] first rows of the experts' stretches
@@ -40,27 +40,35 @@ struct Params {
   int out_fp32;
   int64_t ldc;
   void* c;
-  uint32_t a_type, b_type, tx_bytes;
+  uint32_t a_type, b_type;
+  uint32_t tx_bytes;              // of a stage (all CTAs of a pair)
   int* status;
 };
 
-template <int KIND, int CTAS>
+template <int KIND, int CTAS, int BN_>
 struct Cfg {
   static constexpr bool FP4 = KIND == KIND_MXF4;
   static constexpr int TM = 128 * CTAS;
-  static constexpr int BN = 128 * CTAS;
-  static constexpr int NACC = CTAS == 1 ? 2 : 1;
-  static constexpr int STAGES = 6;
-  static constexpr int NBUF = FP4 ? 1 : 2;               // FP4's scales take the second buffer's room
-  static constexpr int OUT = NBUF * STG_BYTES + 512;
+  static constexpr int BN = BN_;
+  static constexpr int NACC = BN == 128 ? 2 : 1;
+  // of four storing warps; FP4's pair has room for one staging buffer beside
+  // six stages (117 us against 125 with five and two groups)
+  static constexpr int GROUPS = BN == 128 || (CTAS == 2 && FP4) ? 1 : 2;
+  static constexpr int COLS = BN / GROUPS;               // of a group
+  static constexpr int THREADS = 224 + (GROUPS - 1) * 128;
+  // stages of the ring: what fits beside the staging
+  static constexpr int STAGES = CTAS == 1 && BN == 256 ? 4 : 6;
+  static constexpr int NBUF = BN == 128 ? 2 : 1;         // staging buffers of a group
+  static constexpr int OUT = GROUPS * NBUF * STG_BYTES;
+  static constexpr int B_ROWS = BN / CTAS;               // of this CTA
   static constexpr int A_BYTES = BM * BKB;
-  static constexpr int B_BYTES = 128 * BKB;              // this CTA's 128 rows of B
+  static constexpr int B_BYTES = B_ROWS * BKB;
   static constexpr int CHUNKS = FP4 ? 2 : 1;             // 512-byte scale chunks per 128 rows and step
   static constexpr int SFA_BYTES = 512 * CHUNKS;
-  static constexpr int SFB_BYTES = CTAS * SFA_BYTES;
+  static constexpr int SFB_BYTES = BN / 128 * SFA_BYTES;
   static constexpr int TX_CTA = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
   static constexpr int SFA_COLS = 4 * CHUNKS;
-  static constexpr int SF_COLS = SFA_COLS * (1 + CTAS);
+  static constexpr int SF_COLS = SFA_COLS * (1 + BN / 128);
   static constexpr int TMEM_COLS = 512;
   static_assert(NACC * BN + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
   static constexpr int SMEM = STAGES * TX_CTA + OUT + 256 + 1024;
@@ -129,17 +137,16 @@ __device__ __forceinline__ void sync_all() {
   else __syncthreads();
 }
 
-// This CTA's 128 x BN accumulator to C (rows cm .., columns n0 ..), through
-// NBUF swizzled staging buffers and TMA stores; the accumulator is released
-// once it is read.
-template <int BN, int NBUF, typename Release>
-__device__ __forceinline__ void store_acc(int out_fp32, uint32_t tmem, int q, int lane, bool leader, int& buf,
-                                          uint8_t* sOut, const CUtensorMap* map_c, int cm, int n0, Release release) {
-  const int row = q * 32 + lane;
-  const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+// 128 rows and COLS columns to C (rows cm .., columns n0 ..), by the four warps of
+// barrier `bar`, through NBUF swizzled staging buffers and TMA stores.  read(c, v)
+// gives this thread's row's columns 32 c .. 32 c + 63; release() follows the last
+// read, before the stores.
+template <int COLS, int NBUF, typename Read, typename Release>
+__device__ __forceinline__ void store_acc(int out_fp32, int row, bool leader, int bar, int& buf, uint8_t* sOut,
+                                          const CUtensorMap* map_c, int cm, int n0, Read read, Release release) {
   const auto put = [&](const uint32_t* w, int col) {     // 64 bytes of every row
     if (leader) bulk_wait_read_staging<NBUF>();
-    named_bar(1, 128);
+    named_bar(bar, 128);
     uint8_t* stg = sOut + buf * STG_BYTES;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -147,7 +154,7 @@ __device__ __forceinline__ void store_acc(int out_fp32, uint32_t tmem, int q, in
       *reinterpret_cast<uint4*>(stg + row * 64 + phys * 16) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     }
     fence_proxy_async_smem();
-    named_bar(1, 128);
+    named_bar(bar, 128);
     if (leader) {
       tma_store_2d(map_c, smem_u32(stg), col, cm);
       bulk_commit();
@@ -155,40 +162,44 @@ __device__ __forceinline__ void store_acc(int out_fp32, uint32_t tmem, int q, in
     buf ^= NBUF - 1;
   };
   if (!out_fp32) {
-    uint32_t pk[BN / 2];
+    uint32_t pk[COLS / 2];
 #pragma unroll
-    for (int c = 0; c < BN / 32; c += 2) {
-      uint32_t v[2][32];
-      tmem_ld32(lane_addr + c * 32, v[0]);
-      tmem_ld32(lane_addr + (c + 1) * 32, v[1]);
-      tmem_ld_wait();
+    for (int c = 0; c < COLS / 32; c += 2) {
+      uint32_t v[64];
+      read(c, v);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[h][2 * j]), __uint_as_float(v[h][2 * j + 1]));
-          pk[(c + h) * 16 + j] = *reinterpret_cast<const uint32_t*>(&b2);
-        }
+      for (int j = 0; j < 32; ++j) {
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+        pk[c * 16 + j] = *reinterpret_cast<const uint32_t*>(&b2);
+      }
     }
-    tc_fence_before();
-    __syncwarp();
     release();
 #pragma unroll
-    for (int c = 0; c < BN / 32; ++c) put(pk + c * 16, n0 + c * 32);
-    return;
-  }
-  for (int c0 = 0; c0 < BN; c0 += 32) {
-    uint32_t v[32];
-    tmem_ld32(lane_addr + c0, v);
-    tmem_ld_wait();
-    if (c0 + 32 == BN) {
-      tc_fence_before();
-      __syncwarp();
-      release();
+    for (int c = 0; c < COLS / 32; ++c) put(pk + c * 16, n0 + c * 32);
+  } else if constexpr (COLS <= 128) {
+    // all columns in registers first, too
+    uint32_t v[COLS];
+#pragma unroll
+    for (int c = 0; c < COLS / 32; c += 2) read(c, v + c * 32);
+    release();
+#pragma unroll
+    for (int c = 0; c < COLS / 16; ++c) put(v + c * 16, n0 + c * 16);
+  } else {
+    for (int c = 0; c < COLS / 32; c += 2) {
+      uint32_t v[64];
+      read(c, v);
+      if (c + 2 == COLS / 32) release();
+#pragma unroll
+      for (int h = 0; h < 4; ++h) put(v + h * 16, n0 + c * 32 + h * 16);
     }
-    put(v, n0 + c0);
-    put(v + 16, n0 + c0 + 16);
   }
+}
+
+// Columns 32 c .. 32 c + 63 of this thread's accumulator row.
+__device__ __forceinline__ void read_acc(uint32_t lane_addr, int c, uint32_t* v) {
+  tmem_ld32(lane_addr + c * 32, v);
+  tmem_ld32(lane_addr + c * 32 + 32, v + 32);
+  tmem_ld_wait();
 }
 
 // Zeros to this warp's 32 rows of a tile, row by row.
@@ -200,12 +211,12 @@ __device__ __forceinline__ void store_zeros(const Params& p, int q, int lane, in
     for (int b = lane * 16; b < BN * size; b += 512) *reinterpret_cast<uint4*>(row + b) = make_uint4(0, 0, 0, 0);
 }
 
-template <int KIND, int CTAS, int MODE>
-__global__ void __launch_bounds__(THREADS, 1)
+template <int KIND, int CTAS, int BN, int MODE>
+__global__ void __launch_bounds__(Cfg<KIND, CTAS, BN>::THREADS, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_sfa, const __grid_constant__ CUtensorMap map_sfb,
                    const __grid_constant__ CUtensorMap map_c, const Params p) {
-  using C = Cfg<KIND, CTAS>;
+  using C = Cfg<KIND, CTAS, BN>;
   using It = Items<MODE, C::TM, C::BN>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -224,7 +235,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   uint64_t* sf_drain = drain + 1;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sf_drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sf_drain + 1) + 1;
-  volatile int* epi_fail = reinterpret_cast<volatile int*>(sf_drain + 1) + 2;
+  volatile int* epi_fail = reinterpret_cast<volatile int*>(sf_drain + 1) + 2;     // [2], of the groups
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0u;
@@ -238,12 +249,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&acc_full[b]), 1);
-      mbar_init(smem_u32(&acc_empty[b]), 4 * CTAS);                // the storing warps of all CTAs
+      mbar_init(smem_u32(&acc_empty[b]), 4 * C::GROUPS * CTAS);    // the storing warps of all CTAs
     }
     mbar_init(smem_u32(drain), 1);
     mbar_init(smem_u32(sf_drain), 1);
     *abort_flag = 0;
-    *epi_fail = 0;
+    epi_fail[0] = epi_fail[1] = 0;
     fence_mbar_init();
     prefetch_tensormap(&map_a);
     prefetch_tensormap(&map_b);
@@ -270,7 +281,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       int u = 0;                                               // stage use counter
       for (int tile = team; tile < p.ntiles && !*abort_flag; tile += teams) {
         const Item it = items.at(tile);
-        const int ar = it.m0 + static_cast<int>(rank) * 128, br = it.br + static_cast<int>(rank) * 128;
+        const int ar = it.m0 + static_cast<int>(rank) * 128, br = it.br + static_cast<int>(rank) * C::B_ROWS;
         for (int k = 0; k < it.steps; ++k, ++u) {
           const int s = u % STAGES;
           if (!mbar_wait_suspend(smem_u32(&empty[s]), ((u / STAGES) & 1) ^ 1, p.status)) { *abort_flag = 1; break; }
@@ -281,7 +292,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
           // scale maps: one 512-byte chunk per row
           load_tile<CTAS>(smem_u32(sSFA + s * C::SFA_BYTES), &map_sfa, fb, 0, (ar / 128) * p.kb4a + (it.ak + k) * C::CHUNKS);
 #pragma unroll
-          for (int h = 0; h < CTAS; ++h)
+          for (int h = 0; h < BN / 128; ++h)
             load_tile<CTAS>(smem_u32(sSFB + s * C::SFB_BYTES + h * C::SFA_BYTES), &map_sfb, fb, 0,
                             (it.br / 128 + h) * p.kb4b + (it.bk + k) * C::CHUNKS);
         }
@@ -321,7 +332,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint32_t sfa = C::FP4 ? sfa_t + 4 * (kk >> 1) : sfa_t;
-            const uint32_t sfb = C::FP4 ? sfb_t + 4 * CTAS * (kk >> 1) : sfb_t;
+            const uint32_t sfb = C::FP4 ? sfb_t + 4 * (BN / 128) * (kk >> 1) : sfb_t;
             if constexpr (CTAS == 2) tc_mma_pair<KIND>(acc, ad + 2 * kk, bd + 2 * kk, idesc[kk], sfa, sfb, (k | kk) != 0);
             else tc_mma<KIND>(acc, ad + 2 * kk, bd + 2 * kk, idesc[kk], sfa, sfb, (k | kk) != 0);
           }
@@ -353,10 +364,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
           for (int c = 0; c < C::CHUNKS; ++c)
             cp_scales<CTAS>(sfa_t + 4 * c, sfa_desc0 + ((s * C::SFA_BYTES + c * 512) >> 4));
 #pragma unroll
-          for (int h = 0; h < CTAS; ++h)
+          for (int h = 0; h < BN / 128; ++h)
 #pragma unroll
             for (int c = 0; c < C::CHUNKS; ++c)
-              cp_scales<CTAS>(sfa_t + C::SFA_COLS + 4 * CTAS * c + 4 * h,
+              cp_scales<CTAS>(sfa_t + C::SFA_COLS + 4 * (BN / 128) * c + 4 * h,
                               sfb_desc0 + ((s * C::SFB_BYTES + h * C::SFA_BYTES + c * 512) >> 4));
           commit_self<CTAS>(smem_u32(&sf_full[s]));
           if (++s == STAGES) { s = 0; ph ^= 1; }
@@ -369,30 +380,38 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   } else {
     // ------------------------------------------------------------ stores (all CTAs)
     const int q = warp & 3;                                    // lane quarter of tensor memory
-    const bool leader = warp == 2 && lane == 0;
+    const int grp = warp >= 7 ? 1 : 0;                         // columns COLS grp ..
+    const bool leader = (warp == 2 || warp == 7) && lane == 0;
+    const int row = q * 32 + lane;
+    uint8_t* const staging = sOut + grp * C::NBUF * STG_BYTES;
     const It items(p);
     int t = 0, buf = 0;
     for (int tile = team; tile < p.ntiles; tile += teams) {
       const Item it = items.at(tile);
-      const int cm = it.cm + static_cast<int>(rank) * 128;
+      const int cm = it.cm + static_cast<int>(rank) * 128, n0 = it.n0 + grp * C::COLS;
       if (!it.steps) {
-        store_zeros<C::BN>(p, q, lane, cm, it.n0);
+        store_zeros<C::COLS>(p, q, lane, cm, n0);
         continue;
       }
       const int ab = C::NACC == 2 ? (t & 1) : 0;
       const uint32_t aph = C::NACC == 2 ? ((t >> 1) & 1) : (t & 1);
-      ++t;
-      // the four warps decide together, so none is left alone at a named barrier
-      if (!mbar_wait_suspend(smem_u32(&acc_full[ab]), aph, p.status)) *epi_fail = 1;
-      named_bar(1, 128);
-      if (*epi_fail) { *abort_flag = 1; break; }
-      tc_fence_after();
-      store_acc<C::BN, C::NBUF>(p.out_fp32, tmem + ab * C::BN, q, lane, leader, buf, sOut, &map_c, cm, it.n0, [&] {
+      const uint32_t lane_addr = tmem + ab * C::BN + grp * C::COLS + (static_cast<uint32_t>(q * 32) << 16);
+      const auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
         if (lane == 0) {
           if (rank == 0) mbar_arrive(smem_u32(&acc_empty[ab]));
           else mbar_arrive_remote(cluster_map(smem_u32(&acc_empty[ab]), 0));
         }
-      });
+      };
+      // a group's warps decide together, so none is left alone at a named barrier
+      if (!mbar_wait_suspend(smem_u32(&acc_full[ab]), aph, p.status)) epi_fail[grp] = 1;
+      ++t;
+      named_bar(1 + grp, 128);
+      if (epi_fail[grp]) { *abort_flag = 1; break; }
+      tc_fence_after();
+      store_acc<C::COLS, C::NBUF>(p.out_fp32, row, leader, 1 + grp, buf, staging, &map_c, cm, n0,
+                                  [&](int c, uint32_t* v) { read_acc(lane_addr, c, v); }, release);
     }
     if (leader) bulk_wait_all();
   }
@@ -433,7 +452,7 @@ struct Args {
 
 // Teams of CTAS CTAs that run at once (cached per device); 0 on an error.
 template <int CTAS, typename K>
-int resident(K kern, int smem, std::atomic<int>& known) {
+int resident(K kern, int smem, int threads, std::atomic<int>& known) {
   int n = known.load(std::memory_order_relaxed);
   if (n) return n;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
@@ -441,7 +460,7 @@ int resident(K kern, int smem, std::atomic<int>& known) {
   if (CTAS == 2) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (sm_count() / 2));
-    cfg.blockDim = dim3(mxq::egemm::THREADS);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -458,15 +477,15 @@ int resident(K kern, int smem, std::atomic<int>& known) {
   return n;
 }
 
-template <int KIND, int CTAS, int MODE>
+template <int KIND, int CTAS, int BN, int MODE>
 int launch(Args& g, cudaStream_t st) {
   using namespace mxq::gemm;
-  using Cf = mxq::egemm::Cfg<KIND, CTAS>;
+  using Cf = mxq::egemm::Cfg<KIND, CTAS, BN>;
   static std::atomic<int> known[64];
-  auto kern = mxq::egemm::expert_gemm_kernel<KIND, CTAS, MODE>;
+  auto kern = mxq::egemm::expert_gemm_kernel<KIND, CTAS, BN, MODE>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ERR_CUDA;
-  const int teams = resident<CTAS>(kern, Cf::SMEM, known[dev]);
+  const int teams = resident<CTAS>(kern, Cf::SMEM, Cf::THREADS, known[dev]);
   if (!teams) return MXQ_ERR_CUDA;
   const int per = Cf::FP4 ? 2 : 1;                       // codes of a byte
   const bool a_u4 = !Cf::FP4 && g.a_fmt == MXQ_E2M1, b_u4 = !Cf::FP4 && g.b_fmt == MXQ_E2M1;
@@ -477,7 +496,7 @@ int launch(Args& g, cudaStream_t st) {
   };
   const bool f32 = g.p.out_fp32;
   if (!encode_operand(&ma, g.a_q, a_u4, g.ka, g.ka / per, g.a_rows, 128) ||
-      !encode_operand(&mb, g.b_q, b_u4, g.kb, g.kb / per, g.b_rows, 128) || !scales(&msa, g.a_s, g.a_rows, g.ka) ||
+      !encode_operand(&mb, g.b_q, b_u4, g.kb, g.kb / per, g.b_rows, Cf::B_ROWS) || !scales(&msa, g.a_s, g.a_rows, g.ka) ||
       !scales(&msb, g.b_s, g.b_rows, g.kb) ||
       !encode_2d(&mc, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.c, g.c_cols, g.c_rows,
                  g.c_cols * (f32 ? 4 : 2), f32 ? 16 : 32, BM, CU_TENSOR_MAP_SWIZZLE_64B))
@@ -503,18 +522,33 @@ int launch(Args& g, cudaStream_t st) {
   if (!p.status) return MXQ_ERR_CUDA;
   const dim3 grid(CTAS * std::min(p.ntiles, teams));
   if constexpr (CTAS == 2)
-    return launch_pdl_cluster(kern, grid, dim3(mxq::egemm::THREADS), Cf::SMEM, st, 2, ma, mb, msa, msb, mc, p);
+    return launch_pdl_cluster(kern, grid, dim3(Cf::THREADS), Cf::SMEM, st, 2, ma, mb, msa, msb, mc, p);
   else
-    return launch_pdl(kern, grid, dim3(mxq::egemm::THREADS), Cf::SMEM, st, ma, mb, msa, msb, mc, p);
+    return launch_pdl(kern, grid, dim3(Cf::THREADS), Cf::SMEM, st, ma, mb, msa, msb, mc, p);
+}
+
+// Which tile.  Measured on 4096 x 4096 E4M3 weights of 16 experts unless said:
+//  * pairs, where both sides allow it and at least every second SM gets a tile
+//    (a training batch, align 256: 196 us, 221 on 128 x 256 tiles; one token: 16
+//    and 13 on 128 x 128), and for the weights' gradient from 1536 rows an expert
+//    on (2048 rows, 8 experts: 194 and 212; 256 rows of 2048 x 2048: 72 and 55);
+//  * 128 x 256, from two tiles an SM on (a training batch, align 128: 210 us, 266
+//    on 128 x 128; 512 tokens over 8 experts of 1024 x 1024: 7.6 and 6.0).
+template <int KIND, int MODE>
+int choose(Args& g, bool pair, cudaStream_t st) {
+  const int64_t sms = sm_count(), rows = MODE == PRODUCT ? g.c_rows : g.p.m_rows * static_cast<int64_t>(g.p.experts);
+  const int64_t blocks = rows / 128 * (g.c_cols / 128);           // 128 x 128 tiles
+  if (pair && 2 * (blocks / 4) >= sms && (MODE == PRODUCT || g.p.rows >= 1536ll * g.p.experts)) return launch<KIND, 2, 256, MODE>(g, st);
+  if (g.c_cols % 256 == 0 && blocks / 2 >= 2 * sms) return launch<KIND, 1, 256, MODE>(g, st);
+  return launch<KIND, 1, 128, MODE>(g, st);
 }
 
 template <int MODE>
 int run(Args& g, bool pair, void* stream) {
   using namespace mxq::gemm;
   const auto st = static_cast<cudaStream_t>(stream);
-  if (g.a_fmt == MXQ_E2M1 && g.b_fmt == MXQ_E2M1)
-    return pair ? launch<KIND_MXF4, 2, MODE>(g, st) : launch<KIND_MXF4, 1, MODE>(g, st);
-  return pair ? launch<KIND_MXF8, 2, MODE>(g, st) : launch<KIND_MXF8, 1, MODE>(g, st);
+  if (g.a_fmt == MXQ_E2M1 && g.b_fmt == MXQ_E2M1) return choose<KIND_MXF4, MODE>(g, pair, st);
+  return choose<KIND_MXF8, MODE>(g, pair, st);
 }
 
 // Checks that both calls share.
@@ -540,8 +574,8 @@ int check(const void* a_q, const uint8_t* a_s, int a_fmt, const void* b_q, const
 
 extern "C" int mxq_expert_gemm(const void* a_q, const uint8_t* a_s, int a_fmt, const void* b_q, const uint8_t* b_s,
                                int b_fmt, int64_t rows, int64_t N, int64_t K, int experts, int align,
-                               const int32_t* offsets, const int32_t* block_expert, int b_along_k, void* c, int out_fp32,
-                               void* stream) {
+                               const int32_t* offsets, const int32_t* block_expert, int b_along_k, void* c,
+                               int out_fp32, void* stream) {
   if (const int rc = check(a_q, a_s, a_fmt, b_q, b_s, b_fmt, rows, N, K, experts, align, offsets, c, out_fp32)) return rc;
   if (b_along_k != 0 && b_along_k != 1) return MXQ_ERR_BAD_ARG;
   const bool fp4 = a_fmt == MXQ_E2M1 && b_fmt == MXQ_E2M1;

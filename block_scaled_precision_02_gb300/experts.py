@@ -36,24 +36,38 @@ class ExpertPlan:
         rows = (slots + min(experts, slots) * (align - 1)) // align * align
         if rows > _LIMIT:
             raise ValueError("too many slots")
-        at = [0]
-        for n in (experts + 1, experts, slots, rows, rows // align):
-            at.append(at[-1] + n)
-        at[-1] = (at[-1] + 3) // 4 * 4                   # the sort's workspace follows, at 16 bytes
-        work = _size("mxq_expert_sort_workspace_size", device, slots, experts)
-        self._buffer = torch.empty(at[-1] + (work + 3) // 4, dtype=torch.int32, device=device)
-        base = self._buffer.data_ptr()
-        self._at, self._pointers = at, [base + 4 * n for n in at]
+        # where each tensor starts, then the sort's workspace (at 16 bytes), then the end
+        a1 = experts + 1
+        a2 = a1 + experts
+        a3 = a2 + slots
+        a4 = a3 + rows
+        a5 = (a4 + rows // align + 3) // 4 * 4
+        end = a5 + (_size("mxq_expert_sort_workspace_size", device, slots, experts) + 3) // 4
+        self._buffer = torch.empty(end, dtype=torch.int32, device=device)
+        p = self._buffer.data_ptr()
+        self._at = (0, a1, a2, a3, a4, a5, end)
+        self._pointers = (p, p + 4 * a1, p + 4 * a2, p + 4 * a3, p + 4 * a4, p + 4 * a5)
         self.tokens, self.top, self.experts, self.rows, self.align = tokens, top, experts, rows, align
 
-    def _part(self, k: int, n: int) -> torch.Tensor:
-        return self._buffer[self._at[k]:self._at[k] + n]
+    @property
+    def offsets(self):
+        return self._buffer.as_strided((self.experts + 1,), (1,), 0)
 
-    offsets = property(lambda self: self._part(0, self.experts + 1))
-    counts = property(lambda self: self._part(1, self.experts))
-    slot_row = property(lambda self: self._part(2, self.tokens * self.top).view(self.tokens, self.top))
-    row_slot = property(lambda self: self._part(3, self.rows))
-    block_expert = property(lambda self: self._part(4, self.rows // self.align))
+    @property
+    def counts(self):
+        return self._buffer.as_strided((self.experts,), (1,), self._at[1])
+
+    @property
+    def slot_row(self):
+        return self._buffer.as_strided((self.tokens, self.top), (self.top, 1), self._at[2])
+
+    @property
+    def row_slot(self):
+        return self._buffer.as_strided((self.rows,), (1,), self._at[3])
+
+    @property
+    def block_expert(self):
+        return self._buffer.as_strided((self.rows // self.align,), (1,), self._at[4])
 
 
 def expert_sort(experts: torch.Tensor, num_experts: int, align: Optional[int] = None) -> ExpertPlan:
@@ -77,9 +91,9 @@ def expert_sort(experts: torch.Tensor, num_experts: int, align: Optional[int] = 
         raise ValueError("too many slots")
     dev = _same_device("experts", experts)
     plan = ExpertPlan(tokens, top, num_experts, align, dev)
-    at = plan._pointers
+    at = plan._at
     _launch("mxq_expert_sort", dev, experts.data_ptr(), _INDEX[experts.dtype], tokens * top, num_experts, align, plan.rows,
-            *at, 4 * (plan._buffer.numel() - plan._at[-1]))
+            *plan._pointers, 4 * (at[6] - at[5]))
     return plan
 
 
@@ -223,8 +237,9 @@ def mx_expert_gemm(a_q: torch.Tensor, a_s: torch.Tensor, b_q: torch.Tensor, b_s:
         raise ValueError(f"K differs: a_q holds {K}, b_q {b_shape[-1]}" + (f" for {plan.experts} experts" if along_k else ""))
     dev = _same_device("a_q a_s b_q b_s plan", a_q, a_s, b_q, b_s, plan._buffer)
     c = torch.empty(R, N, dtype=out_dtype, device=dev)
+    at = plan._pointers
     _launch("mxq_expert_gemm", dev, a_q.data_ptr(), a_s.data_ptr(), f, b_q.data_ptr(), b_s.data_ptr(), fb, R, N, K,
-            plan.experts, plan.align, plan._pointers[0], plan._pointers[4], int(along_k), c.data_ptr(),
+            plan.experts, plan.align, at[0], at[4], int(along_k), c.data_ptr(),
             int(out_dtype == torch.float32))
     return c
 

@@ -511,7 +511,8 @@ int mxq_expert_gather_mx(const void* x, int64_t tokens, int64_t cols, int64_t ld
 
 /* ---- block-scaled products of all experts ([MX] section 1) --------------------------
  * C[r][n] = sum_k A[r][k] B[e][n][k] for every row r of expert e's stretch
- * (padding rows too), 0 behind the last stretch: every element is written.
+ * (padding, too: zeros where A's padding is, as the gathers leave it), 0 behind
+ * the last: every element is written.
  * A, a_s   [rows][K] codes and MXQ_SF_MMA scales.
  * B, b_s   b_along_k == 0: [experts * N][K], the experts' weights stacked;
  *          1: [N][experts * K], the experts along the contraction: the column

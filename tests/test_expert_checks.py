@@ -199,7 +199,7 @@ def test_c_products(so):
                           (9, 0, BAD_SHAPE), (9, 1025, BAD_SHAPE), (10, 64, BAD_ARG), (13, 2, BAD_ARG), (15, 2, BAD_ARG),
                           (0, None, BAD_ARG), (3, None, BAD_ARG), (11, None, BAD_ARG), (12, None, BAD_ARG), (14, None, BAD_ARG),
                           (0, 0x10008, MISALIGNED), (4, 0x10008, MISALIGNED), (14, 0x10008, MISALIGNED), (11, ODD, MISALIGNED),
-                          (7, 2 ** 30, BAD_SHAPE), (8, 2 ** 30, BAD_SHAPE)):
+                          (12, ODD, MISALIGNED), (7, 2 ** 30, BAD_SHAPE), (8, 2 ** 30, BAD_SHAPE)):
         assert so.mxq_expert_gemm(*[bad if i == at else v for i, v in enumerate(ok)]) == want, at
     fp4 = [P, P, 2, P, P, 2, 256, 128, 128, 3, 128, P, P, 0, P, 0, None]
     assert so.mxq_expert_gemm(*fp4) == BAD_SHAPE                     # both E2M1: K % 256

@@ -54,6 +54,27 @@ def test_products_exactly(lib, tokens, top, experts, pattern, align, n, fmt, b_f
     assert lib.last_device_status() == 0
 
 
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("fmt,b_fmt", PAIRS)
+@pytest.mark.parametrize("align,n,k", [(128, 128, 256), (128, 640, 2304), (256, 256, 2048)])
+@pytest.mark.parametrize("counts", [(1,), (0, 32), (31, 0, 1), (16, 1, 0, 8, 7), (33,), (0, 31, 2, 32), (129, 255, 64, 256, 1)])
+def test_products_of_few_tokens(lib, counts, align, n, k, fmt, b_fmt, out):
+    """Blocks with one token to a few, and what follows them: exact sums again,
+    zeros behind the tokens."""
+    experts = len(counts)
+    e = torch.repeat_interleave(torch.arange(experts), torch.tensor(counts))
+    p = lib.expert_sort(e[torch.randperm(len(e), generator=torch.Generator().manual_seed(4))].view(-1, 1).to(dev), experts, align)
+    rng = np.random.default_rng(n + k)
+    aq, as_ = integer_operand(rng, p.rows, k, fmt)
+    aq[p.row_slot < 0] = 0
+    bq, bs = integer_operand(rng, experts * n, k, b_fmt)
+    ref = products(decoded(aq, as_, fmt), decoded(bq, bs, b_fmt).reshape(experts, n, k), p.offsets.tolist(), p.rows)
+    for _ in range(2):
+        c = lib.mx_expert_gemm(aq, as_, bq.view(experts, n, -1), bs, p, fmt, b_fmt, out)
+        assert np.array_equal(c.double().cpu().numpy(), rounded(ref, out))
+    assert lib.last_device_status() == 0
+
+
 @pytest.mark.parametrize("fmt,b_fmt", PAIRS)
 @pytest.mark.parametrize("align,n", [(128, 128), (256, 256)])
 def test_products_with_experts_along_the_contraction(lib, align, n, fmt, b_fmt):
@@ -153,6 +174,9 @@ def test_a_wrong_plan_stays_within_bounds(lib):
     aq, as_ = integer_operand(rng, p.rows, 128, "e4m3")
     bq, bs = integer_operand(rng, 4 * 128, 128, "e4m3")
     gq, gs = integer_operand(rng, 128, p.rows, "e4m3")
+    few, _ = make_plan(lib, 16, 2, 4, "even", 128)
+    fq, fs = integer_operand(rng, few.rows, 1024, "e4m3")
+    wq, ws = integer_operand(rng, 4 * 128, 1024, "e4m3")
     off, block, big = p.offsets.clone(), p.block_expert.clone(), 2 ** 31 - 1
     for o, b in ((torch.full_like(off, big), torch.full_like(block, big)), (torch.full_like(off, -big), torch.full_like(block, -big)),
                  (off.flip(0), block.flip(0)), (off, torch.full_like(block, 1))):
@@ -160,4 +184,7 @@ def test_a_wrong_plan_stays_within_bounds(lib):
         p.block_expert.copy_(b)
         lib.mx_expert_gemm(aq, as_, bq.view(4, 128, 128), bs, p)
         lib.mx_expert_wgrad(gq, gs, gq, gs, p)
+        few.offsets.copy_(o)
+        few.block_expert.copy_(b[:few.rows // 128])
+        lib.mx_expert_gemm(fq, fs, wq.view(4, 128, 1024), ws, few)
     assert lib.last_device_status() == 0
