@@ -23,11 +23,12 @@ constexpr int kMaxExperts = 1024;
 // ---------------------------------------------------------------- sort
 constexpr int SORT_WARPS = 16, SORT_T = 32 * SORT_WARPS;
 constexpr int SORT_SLOTS = 2048;          // slots of a CTA, until there are SORT_CLUSTER or SORT_CTAS of them
-// Up to 65536 slots one cluster of CTAs sorts, which read each other's counts
-// from shared memory: a launch less on the host's path (8 us there) and on the
-// device.  Beyond, SORT_CTAS count first and place in a second launch.
+// Up to 32768 slots one cluster of CTAs sorts, which read each other's counts
+// from shared memory: a launch less, 8 us of the host's path (8192 tokens, 2 of
+// 16 experts: 6.1 us on the device either way).  Beyond, SORT_CTAS count first
+// and place in a second launch (8192 tokens, 8 of 64: 7.8 us against 15.8).
 constexpr int SORT_CLUSTER = 8, SORT_CTAS = 128;
-constexpr int64_t CLUSTER_SLOTS = 65536;
+constexpr int64_t CLUSTER_SLOTS = 32768;
 
 struct SortArgs {
   const void* experts;
@@ -822,22 +823,25 @@ template <typename T, typename TY, int VE>
 int run_combine_direct(RowArgs a, cudaStream_t st) {
   a.pieces = static_cast<int>((a.cols + 32 * U * VE - 1) / (32 * U * VE));
   const int64_t grid = (a.tokens * a.pieces + ROW_WARPS - 1) / ROW_WARPS;
+  if (grid > 0x0FFFFFFF) return MXQ_ERR_BAD_SHAPE;       // 2^31 warps, a terabyte of y
   return launch_pdl(combine_direct_kernel<T, TY, VE>, dim3(static_cast<unsigned>(grid)), dim3(ROW_T), 0, st, a);
 }
 
-// The ring pays from about 2^21 elements of y on, and for bf16 rows without a
-// common alignment from DIRECT_COLS columns on (their single elements go round
-// apart); float32 rows without one are read element by element at
-// the same rate.
-constexpr int64_t RING_ELEMS = 1 << 21, DIRECT_COLS = 512, DIRECT_ITEMS = 1ll << 31;
+// The ring pays from about 2^21 elements of y on (8192 x 4096 bf16: 32 us, read
+// directly 47; 515 x 2049 float32: 8.9 and 3.7).  Rows without a common alignment
+// take it as bf16 of DIRECT_COLS columns or more (8192 x 4095: 26 us, element by
+// element 49), as their single elements go round apart (16384 x 77, 4 slots: 40
+// and 6); float32 ones are read element by element as fast (5238 x 1023, 5
+// slots: 23 us, 31 in the ring).
+constexpr int64_t RING_ELEMS = 1 << 21, DIRECT_COLS = 512;
 
 template <typename T, typename TY, int VE>
 int run_combine(const RowArgs& a, bool vectors, cudaStream_t st) {
   const bool many = a.tokens * a.cols >= RING_ELEMS;
   if (vectors) return many ? run_combine_ring<T, TY, VE, false>(a, st) : run_combine_direct<T, TY, VE>(a, st);
-  const bool countable = a.tokens * ((a.cols + 32 * U - 1) / (32 * U)) < DIRECT_ITEMS;
-  if (countable && (sizeof(T) == 4 || !many || a.cols < DIRECT_COLS)) return run_combine_direct<T, TY, 1>(a, st);
-  return run_combine_ring<T, TY, VE, true>(a, st);
+  if constexpr (sizeof(T) == 2)
+    if (many && a.cols >= DIRECT_COLS) return run_combine_ring<T, TY, VE, true>(a, st);
+  return run_combine_direct<T, TY, 1>(a, st);
 }
 
 template <typename T, typename TY, int VE, int G, int NV, bool ANY>

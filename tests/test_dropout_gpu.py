@@ -45,6 +45,13 @@ def test_dropout(lib, rows, cols, p, dtype):
     check(lib, x, p, 2 ** 64 - 1, 0, res)
 
 
+@pytest.mark.parametrize("res", [False, True])
+def test_long_tensors(lib, res):
+    """Four vectors to a thread, and a last element that fills none."""
+    x = torch.randn(4099, 4101, device=dev).to(BF)
+    check(lib, x, 0.2, 99, 11, torch.randn_like(x) if res else None)
+
+
 @pytest.mark.parametrize("offset", [0, 2 ** 32 - 3, 2 ** 40 + 5, 2 ** 62 - 100])
 def test_counters_pass_32_bits(lib, offset):
     check(lib, torch.randn(9, 40, device=dev), 0.3, 5, offset)

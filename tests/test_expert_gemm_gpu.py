@@ -106,6 +106,46 @@ def test_weight_gradient_exactly(lib, tokens, top, experts, pattern, align, n, k
     assert lib.last_device_status() == 0
 
 
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("fmt,b_fmt", PAIRS)
+@pytest.mark.parametrize("align,n", [(128, 2048), (128, 2176), (256, 1024)])
+def test_products_of_many_tiles_exactly(lib, align, n, fmt, b_fmt, out):
+    """As many tiles as the wide tiles and the pairs take, an expert without rows among them."""
+    experts, K = 5, 512
+    e = np.minimum(routing(np.random.default_rng(2), 2500, 2, experts, "skewed") * 2, experts - 1)
+    e[e == 3] = 4
+    e[:30] = -1
+    p = lib.expert_sort(torch.from_numpy(e).int().to(dev), experts, align)
+    rng = np.random.default_rng(n)
+    aq, as_ = integer_operand(rng, p.rows, K, fmt)
+    bq, bs = integer_operand(rng, experts * n, K, b_fmt)
+    ref = products(decoded(aq, as_, fmt), decoded(bq, bs, b_fmt).reshape(experts, n, K), p.offsets.tolist(), p.rows)
+    for _ in range(2):
+        c = lib.mx_expert_gemm(aq, as_, bq.view(experts, n, -1), bs, p, fmt, b_fmt, out)
+        assert np.array_equal(c.double().cpu().numpy(), rounded(ref, out))
+    assert lib.last_device_status() == 0
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("fmt,b_fmt", PAIRS)
+@pytest.mark.parametrize("tokens,experts,n,k", [(700, 5, 1024, 2048), (1600, 2, 1536, 1792), (500, 6, 1152, 896)])
+def test_weight_gradient_of_many_tiles_exactly(lib, tokens, experts, n, k, fmt, b_fmt, out):
+    """Wide tiles, pairs (from 1536 rows an expert on) and small tiles, an expert without rows among them."""
+    e = routing(np.random.default_rng(3), tokens, 2, experts, "even")
+    if experts > 2:
+        e[e == 1] = 0
+    p = lib.expert_sort(torch.from_numpy(e).int().to(dev), experts, 256)
+    rng = np.random.default_rng(n + k)
+    aq, as_ = integer_operand(rng, n, p.rows, fmt)
+    bq, bs = integer_operand(rng, k, p.rows, b_fmt)
+    a, b, o = decoded(aq, as_, fmt), decoded(bq, bs, b_fmt), p.offsets.tolist()
+    ref = np.stack([a[:, o[i]:o[i + 1]] @ b[:, o[i]:o[i + 1]].T for i in range(experts)])
+    for _ in range(2):
+        c = lib.mx_expert_wgrad(aq, as_, bq, bs, p, fmt, b_fmt, out)
+        assert np.array_equal(c.double().cpu().numpy(), rounded(ref, out))
+    assert lib.last_device_status() == 0
+
+
 @pytest.mark.parametrize("align,n,k", [(128, 384, 1024), (256, 1024, 1152)])
 def test_many_tiles_of_general_values(lib, align, n, k):
     """More tiles than teams (rings and accumulators go round), general values, within the products' gate of 2e-3."""

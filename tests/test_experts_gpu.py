@@ -27,7 +27,7 @@ def np64(t):
 # ------------------------------------------------------------------ sort
 @pytest.mark.parametrize("pattern", PATTERNS)
 @pytest.mark.parametrize("tokens,top,experts", [(1, 1, 1), (1, 8, 64), (3, 2, 7), (100, 3, 5), (515, 2, 16), (2048, 1, 1024),
-                                                (2049, 1, 2), (4097, 5, 33), (5000, 8, 1000), (8192, 8, 64), (65537, 1, 20), (300000, 1, 128)])
+                                                (2049, 1, 2), (4097, 5, 33), (5000, 8, 1000), (8192, 4, 64), (8192, 8, 64), (32769, 1, 20), (300000, 1, 128)])
 def test_sort(lib, tokens, top, experts, pattern):
     rng = np.random.default_rng(tokens + experts)
     for align, dtype in ((128, torch.int32), (256, torch.int64)):
@@ -180,6 +180,32 @@ def test_combine(lib, tokens, top, experts, cols, dtype, out, wtype, pattern):
     assert np.all(np64(y)[(want[2] < 0).all(1)] == 0)
 
 
+@pytest.mark.parametrize("pattern", ["even", "dropped"])
+@pytest.mark.parametrize("dtype,out,wtype", [(BF, BF, F32), (BF, F32, BF), (F32, BF, BF), (F32, F32, None)])
+@pytest.mark.parametrize("tokens,top,experts,cols", [(2100, 2, 7, 1024), (2200, 3, 5, 1021), (4099, 1, 3, 515), (70000, 2, 64, 32),
+                                                     (30011, 5, 9, 77), (513, 2, 4, 4104), (9001, 2, 4, 264)])
+def test_combine_of_many_tokens(lib, tokens, top, experts, cols, dtype, out, wtype, pattern):
+    """Sizes of the ring of asynchronous copies, every lane group and alignment of it."""
+    rng = np.random.default_rng(cols)
+    p, want = make_plan(lib, rng, tokens, top, experts, pattern)
+    rows, w = inputs(rng, p, cols, dtype, wtype or F32, float("nan"))
+    if wtype == BF:                                  # weights that start inside a 4-byte word
+        store = torch.empty(w.numel() + 1, dtype=BF, device=dev)
+        store[1:] = w.view(-1)
+        w = store[1:].view(w.shape)
+    w = None if wtype is None else w
+    y = lib.expert_combine(rows, p, w, out)
+    ref, mag = combine64(rows.nan_to_num(0.0), None if w is None else w.nan_to_num(0.0), want[2])
+    tol = top * 2.0 ** -24 * mag * (1 + 1e-5)
+    tol = tol + half_ulp(out, ref, tol)
+    assert np.all(np.abs(np64(y) - ref) <= tol)
+    if cols % 8 and dtype == BF:                     # rows that start elsewhere in their words
+        store = torch.empty(p.rows * (cols + 3) + 5, dtype=BF, device=dev)
+        shifted = store[5:].view(p.rows, cols + 3)[:, :cols]
+        shifted.copy_(rows)
+        assert torch.equal(lib.expert_combine(shifted, p, w, out), y)
+
+
 def test_combine_of_strided_and_shifted_rows(lib):
     rng = np.random.default_rng(5)
     p, _ = make_plan(lib, rng, 50, 2, 4, "dropped")
@@ -259,6 +285,39 @@ def test_gradients_against_differences(lib):
         up[t, c], down[t, c] = 1.0, -1.0
         d = (np64(lib.expert_gather(up, p) - lib.expert_gather(down, p)) * np64(G)).sum() / 2
         assert abs(d - float(dx[t, c])) <= 3 * 2.0 ** -24 * 3 * np.abs(np64(G)).max()
+
+
+def test_offsets_that_pass_32_bits(lib):
+    """Tensors of more than 2^31 elements: the last rows and columns are where they belong."""
+    tokens, cols = 300000, 8192
+    e = torch.arange(tokens, device=dev, dtype=torch.int32).view(-1, 1) % 3
+    p = lib.expert_sort(e, 3)
+    x = torch.empty(tokens, cols, dtype=BF, device=dev)
+    x.copy_((torch.arange(tokens, device=dev) % 251)[:, None])
+    x[:, -1] = 2.0
+    rows = lib.expert_gather(x, p)
+    at = p.slot_row.view(-1).long()
+    assert torch.equal(rows[at[-5000:]], x[-5000:]) and torch.equal(rows[at[:100]], x[:100]) and not rows[-1].any()
+    q, s, qT, sT = lib.mx_expert_gather(x, p, "e4m3", "dual", sf_layout="mma")
+    lo = int(p.offsets[2]) + 128 * 700               # a stretch of the last expert
+    part = lib.mx_quantize(rows[lo:lo + 256].contiguous(), "e4m3", "dual", sf_layout="canonical")
+    assert torch.equal(q[lo:lo + 256], part[0]) and torch.equal(qT[:, lo:lo + 256], part[2])
+    assert p.rows * cols > 2 ** 31
+    del q, s, qT, sT, part
+    w = torch.full((tokens, 1), 0.5, device=dev)
+    y = lib.expert_combine(rows, p, w)
+    assert torch.equal(y[-5000:], x[-5000:] * 0.5)
+    del y
+    d, dw = lib.expert_combine_backward(x, rows, p, w)
+    assert torch.equal(d[at[-5000:]], x[-5000:] * 0.5) and not d[-1].any()
+    # a row's products are whole numbers: (cols - 1) v^2 + 4 up to 2^29, off by half a step of each partial sum
+    v = (torch.arange(tokens, device=dev) % 251).double()
+    want = (cols - 1) * v * v + 4
+    assert bool(((dw.view(-1).double() - want).abs() <= 64 * 2.0 ** -24 * want).all())
+    del d, rows
+    drop = lib.dropout(x, 0.5, 7, residual=x)
+    tail = lib.dropout(x[-1000:].contiguous(), 0.5, 7, (tokens - 1000) * cols // 4, residual=x[-1000:].contiguous())
+    assert torch.equal(drop[-1000:], tail)
 
 
 def test_a_wrong_plan_reads_and_writes_within_bounds(lib):
