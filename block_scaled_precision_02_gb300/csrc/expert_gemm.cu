@@ -55,7 +55,8 @@ struct Cfg {
   // six stages (117 us against 125 with five and two groups)
   static constexpr int GROUPS = BN == 128 || (CTAS == 2 && FP4) ? 1 : 2;
   static constexpr int COLS = BN / GROUPS;               // of a group
-  static constexpr int THREADS = 224 + (GROUPS - 1) * 128;
+  static constexpr int STORE_WARPS = 4 * GROUPS;
+  static constexpr int THREADS = 32 * (4 + STORE_WARPS);
   // stages of the ring: what fits beside the staging
   static constexpr int STAGES = CTAS == 1 && BN == 256 ? 4 : 6;
   static constexpr int NBUF = BN == 128 ? 2 : 1;         // staging buffers of a group
@@ -219,6 +220,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   using C = Cfg<KIND, CTAS, BN>;
   using It = Items<MODE, C::TM, C::BN>;
   constexpr int STAGES = C::STAGES;
+  constexpr int WARP_B = C::THREADS / 32 - 1;                      // the second producer
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -274,9 +276,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   const uint32_t tmem = *tmem_slot;
   const uint32_t tmem_sf = tmem + C::NACC * C::BN;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer (all CTAs)
+  if (warp == 0 || warp == WARP_B) {
+    // ------------------------------------------------------------ producers (all CTAs)
+    // one thread for A and its scales, one for B and its: issuing is what a
+    // step's loads cost
     if (lane == 0) {
+      const bool a_side = warp == 0;
       const It items(p);
       int u = 0;                                               // stage use counter
       for (int tile = team; tile < p.ntiles && !*abort_flag; tile += teams) {
@@ -286,15 +291,18 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
           const int s = u % STAGES;
           if (!mbar_wait_suspend(smem_u32(&empty[s]), ((u / STAGES) & 1) ^ 1, p.status)) { *abort_flag = 1; break; }
           const uint32_t fb = CTAS == 2 ? cluster_map(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), p.tx_bytes);
-          load_tile<CTAS>(smem_u32(sA + s * C::A_BYTES), &map_a, fb, (it.ak + k) * BKB, ar);
-          load_tile<CTAS>(smem_u32(sB + s * C::B_BYTES), &map_b, fb, (it.bk + k) * BKB, br);
           // scale maps: one 512-byte chunk per row
-          load_tile<CTAS>(smem_u32(sSFA + s * C::SFA_BYTES), &map_sfa, fb, 0, (ar / 128) * p.kb4a + (it.ak + k) * C::CHUNKS);
+          if (a_side) {
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), p.tx_bytes);
+            load_tile<CTAS>(smem_u32(sA + s * C::A_BYTES), &map_a, fb, (it.ak + k) * BKB, ar);
+            load_tile<CTAS>(smem_u32(sSFA + s * C::SFA_BYTES), &map_sfa, fb, 0, (ar / 128) * p.kb4a + (it.ak + k) * C::CHUNKS);
+          } else {
+            load_tile<CTAS>(smem_u32(sB + s * C::B_BYTES), &map_b, fb, (it.bk + k) * BKB, br);
 #pragma unroll
-          for (int h = 0; h < BN / 128; ++h)
-            load_tile<CTAS>(smem_u32(sSFB + s * C::SFB_BYTES + h * C::SFA_BYTES), &map_sfb, fb, 0,
-                            (it.br / 128 + h) * p.kb4b + (it.bk + k) * C::CHUNKS);
+            for (int h = 0; h < BN / 128; ++h)
+              load_tile<CTAS>(smem_u32(sSFB + s * C::SFB_BYTES + h * C::SFA_BYTES), &map_sfb, fb, 0,
+                              (it.br / 128 + h) * p.kb4b + (it.bk + k) * C::CHUNKS);
+          }
         }
       }
       // no copy of any CTA is still landing when the kernel ends (the other
