@@ -363,6 +363,7 @@ template <typename T, int VE, bool ANY>
 __global__ void __launch_bounds__(ROW_T) gather_kernel(const RowArgs a) {
   grid_dep_launch();
   grid_dep_wait();
+  zero_padding<T, VE, ANY>(a);                           // nothing waits for these stores
   const Walk w(a);
   T* const out = static_cast<T*>(a.out);
   Place at(w);
@@ -408,7 +409,6 @@ __global__ void __launch_bounds__(ROW_T) gather_kernel(const RowArgs a) {
       }
     }
   }
-  zero_padding<T, VE, ANY>(a);
 }
 
 // ---------------------------------------------------------------- combine
@@ -759,6 +759,118 @@ __global__ void __launch_bounds__(BWD_T, 4) combine_bwd_kernel(const RowArgs a) 
   zero_padding<T, VE, ANY, BWD_T>(a);
 }
 
+// Many tokens of aligned rows, dy of the rows' type: the ring of combine.  G warps
+// take a token, whose units are dy and then the rows of its slots; dy's vectors
+// stay in registers.  Sums of up to DOTS slots meet in shared memory.
+constexpr int DOTS = 8;
+constexpr int bwd_ring_smem() { return S * ROW_T * U * 16 + 2 * S * ROW_T * 8; }
+
+template <typename T, int VE, int G>
+__global__ void __launch_bounds__(ROW_T, 2) combine_bwd_ring_kernel(const RowArgs a) {
+  constexpr int TEAMS = ROW_WARPS / G;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float red[2][TEAMS][DOTS][G];
+  uint8_t* const mine = ring + (threadIdx.x >> 5) * (U * 512) + (threadIdx.x & 31) * 16;
+  uint2* const plan = reinterpret_cast<uint2*>(ring + S * ROW_T * U * 16) + threadIdx.x;          // [2 S][ROW_T]
+  const uint32_t to = smem_u32(mine), plan_to = smem_u32(plan);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / G, part = warp % G;
+  const int idx = part * 32 + lane, cols = static_cast<int>(a.cols);
+  const int c0 = idx * VE;
+  constexpr int STEP = G * 32 * VE;
+  const T* const src = static_cast<const T*>(a.src);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
+  grid_dep_launch();
+  grid_dep_wait();
+
+  // units of a token: -1 is dy, then its slots
+  int64_t use_t = blockIdx.x * static_cast<int64_t>(TEAMS) + team, copy_t = use_t, look_t = use_t;
+  int use_j = -1, copy_j = -1, look_j = -1;
+  int slot = 0, at = 0, buf = 0;
+  Vec<T, VE> d[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) d[u].fill(0);
+  for (int n = -2 * S; use_t < a.tokens; n += n < 0) {
+    cp_async_wait<S - 1>();
+    int r = -1;
+    float g = 0.f;
+    Vec<T, VE> x[U];
+    if (n >= 0) {
+      const uint8_t* const from = mine + slot * (ROW_T * U * 16);
+      if (use_j < 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) d[u].load(reinterpret_cast<const T*>(from + u * 512));
+      } else {
+        const uint2 q = plan[at * ROW_T];
+        r = static_cast<int>(q.x) < a.rows ? static_cast<int>(q.x) : -1;
+        const bool high = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(a.w) >> 1) + static_cast<uint32_t>(use_t * a.top + use_j)) & 1;
+        g = a.w_f32 ? __uint_as_float(q.y) : high ? bf16hi(q.y) : bf16lo(q.y);
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u].load(reinterpret_cast<const T*>(from + u * 512));
+      }
+    }
+    if (n >= -S && copy_t < a.tokens) {
+      const uint32_t dst = to + slot * (ROW_T * U * 16);
+      const int cr = copy_j < 0 ? 0 : static_cast<int>(plan[(at >= S ? at - S : at + S) * ROW_T].x);
+      if (cr >= 0 && cr < max(a.rows, int64_t(1))) {
+        const T* const row = copy_j < 0 ? static_cast<const T*>(a.dy) + copy_t * a.ld_dy : src + cr * a.ld;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (c0 + u * STEP < cols) cp_async16(dst + u * 512, row + c0 + u * STEP);
+      }
+      if (++copy_j == a.top) copy_j = -1, copy_t += stride;
+    }
+    if (look_t < a.tokens) {
+      if (look_j >= 0) {
+        const int64_t id = look_t * a.top + look_j;
+        cp_async4(plan_to + at * (ROW_T * 8), a.slot_row + id);
+        cp_async4(plan_to + at * (ROW_T * 8) + 4,
+                  reinterpret_cast<const void*>((reinterpret_cast<uintptr_t>(a.w) + (a.w_f32 ? 4 : 2) * id) & ~uintptr_t(3)));
+      }
+      if (++look_j == a.top) look_j = -1, look_t += stride;
+    }
+    cp_async_commit();
+    if (n >= -S) slot = slot + 1 == S ? 0 : slot + 1;
+    at = at + 1 == 2 * S ? 0 : at + 1;
+    if (n < 0) continue;
+    if (use_j >= 0) {
+      float dot = 0.f;
+      if (r >= 0) {
+        T* const o = static_cast<T*>(a.out) + static_cast<int64_t>(r) * cols + c0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (c0 + u * STEP < cols) {
+            float q[VE], w[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i) q[i] = d[u].get(i) * x[u].get(i), w[i] = d[u].get(i) * g;
+            dot += tree_sum(q);
+            store_vec<T, VE>(o + u * STEP, w);
+          }
+      }
+      dot = warp_sum(dot);
+      const int64_t id = use_t * a.top + use_j;
+      if constexpr (G == 1) {
+        if (lane == 0) a.dw[id] = dot;
+      } else {
+        const int k = use_j & (DOTS - 1);
+        if (lane == 0) red[buf][team][k][part] = dot;
+        if (k == DOTS - 1 || use_j == a.top - 1) {
+          asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(G * 32) : "memory");
+          if (idx <= k) {
+            float sum = 0.f;
+#pragma unroll
+            for (int p = 0; p < G; ++p) sum += red[buf][team][idx][p];
+            a.dw[id - k + idx] = sum;
+          }
+          buf ^= 1;
+        }
+      }
+    }
+    if (++use_j == a.top) use_j = -1, use_t += stride;
+  }
+  cp_async_wait<0>();
+  zero_padding<T, VE, false>(a);
+}
+
 // ---------------------------------------------------------------- host
 bool plan_sizes(int64_t tokens, int64_t top, int64_t rows) {
   return tokens >= 0 && top >= 1 && rows >= 0 && top <= kMaxCols && tokens <= kMaxCols / top && rows <= kMaxCols;
@@ -854,11 +966,31 @@ int launch_backward(const RowArgs& a, cudaStream_t st) {
   return launch_pdl(combine_bwd_kernel<T, TY, VE, G, NV, ANY>, dim3(grid), dim3(BWD_T), 0, st, a);
 }
 
+// Elements of dy from which the ring pays (16384 x 1024 bf16, 4 slots: 51 us, 63
+// read directly; 8192 x 4096, one slot: 33 and 48; 600 x 4096: 7.6 and 6.5).
+constexpr int64_t BWD_RING = 1 << 22;
+
+template <typename T, int VE, int G>
+int launch_backward_ring(const RowArgs& a, cudaStream_t st) {
+  static std::atomic<int> known[64];
+  unsigned grid = 0;
+  if (const int rc = stay(combine_bwd_ring_kernel<T, VE, G>, (a.tokens * G + ROW_WARPS - 1) / ROW_WARPS, known, &grid, bwd_ring_smem()))
+    return rc;
+  return launch_pdl(combine_bwd_ring_kernel<T, VE, G>, dim3(grid), dim3(ROW_T), bwd_ring_smem(), st, a);
+}
+
 // As many warps to a token as its vectors fill, eight at most.
 template <typename T, typename TY, int VE>
 int run_backward(const RowArgs& a, bool vectors, cudaStream_t st) {
   if (!vectors)
     return a.cols <= 64 * VE ? launch_backward<T, TY, VE, 1, 1, true>(a, st) : launch_backward<T, TY, VE, 8, 2, true>(a, st);
+  if constexpr (sizeof(T) == sizeof(TY))
+    if (a.tokens * a.cols >= BWD_RING && a.cols > 64 * VE && a.cols <= 1024 * VE) {
+      if (a.cols <= 128 * VE) return launch_backward_ring<T, VE, 1>(a, st);
+      if (a.cols <= 256 * VE) return launch_backward_ring<T, VE, 2>(a, st);
+      if (a.cols <= 512 * VE) return launch_backward_ring<T, VE, 4>(a, st);
+      return launch_backward_ring<T, VE, 8>(a, st);
+    }
   if (a.cols <= 32 * VE) return launch_backward<T, TY, VE, 1, 1, false>(a, st);
   if (a.cols <= 64 * VE) return launch_backward<T, TY, VE, 2, 1, false>(a, st);
   if (a.cols <= 128 * VE) return launch_backward<T, TY, VE, 4, 1, false>(a, st);

@@ -253,6 +253,39 @@ def test_combine_backward(lib, tokens, top, experts, cols, dtype, dytype, wtype,
     assert torch.equal(again[0], drows) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("pattern", ["even", "dropped"])
+@pytest.mark.parametrize("dtype,wtype", [(BF, F32), (BF, BF), (F32, BF), (F32, F32)])
+@pytest.mark.parametrize("tokens,top,experts,cols", [(4100, 2, 7, 1024), (4700, 1, 5, 904), (2100, 9, 30, 2048), (1100, 3, 4, 4096),
+                                                     (1030, 2, 4, 4104), (520, 17, 20, 8192), (520, 2, 3, 8200), (8200, 8, 11, 520)])
+def test_combine_backward_of_many_tokens(lib, tokens, top, experts, cols, dtype, wtype, pattern):
+    """Sizes of the ring of asynchronous copies, and the first ones beyond it."""
+    rng = np.random.default_rng(cols)
+    p, want = make_plan(lib, rng, tokens, top, experts, pattern)
+    rows, w = inputs(rng, p, cols, dtype, wtype, float("nan"))
+    if wtype == BF:                                  # weights that start inside a 4-byte word
+        store = torch.empty(w.numel() + 1, dtype=BF, device=dev)
+        store[1:] = w.view(-1)
+        w = store[1:].view(w.shape)
+    dy = torch.randn(tokens, cols, generator=torch.Generator().manual_seed(2)).to(dtype).to(dev)
+    drows, dw = lib.expert_combine_backward(dy, rows, p, w)
+    # float64 on the GPU, slot by slot
+    slot = torch.from_numpy(want[2]).to(dev)
+    ref = torch.zeros(p.rows, cols, dtype=torch.float64, device=dev)
+    steps = cols // 256 + 1 + 8 + 5 + 8 + 1
+    for j in range(top):
+        live = slot[:, j] >= 0
+        at, d = slot[live, j], dy[live].double()
+        ref[at] = d * w[live, j].double()[:, None]
+        prod = d * rows[at].double()
+        assert bool(((dw[live, j].double() - prod.sum(1)).abs() <= steps * 2.0 ** -24 * prod.abs().sum(1)).all())
+        assert not bool(dw[~live, j].any())
+    half = 2.0 ** -9 if dtype == BF else 2.0 ** -24
+    # one rounding of the product to float32 and one to the rows' type, each at most half a step of the value's binade
+    assert bool(((drows.double() - ref).abs() <= ref.abs() * (2 * half + 2.0 ** -23) + 2.0 ** -130).all())
+    again = lib.expert_combine_backward(dy, rows, p, w)
+    assert torch.equal(again[0], drows) and torch.equal(again[1], dw)
+
+
 def test_gradients_against_differences(lib):
     """The sum is linear in the rows and in the weights: a difference over a
     step h is the gradient up to the float32 rounding of both sums, 4 steps of
