@@ -342,7 +342,7 @@ def gemm_part(args, mxq, X, q, outs, timed, bf16, peak_src, gemm_rows):
                           "roofline": {"bound": "tensor", "achieved": round(tf, 1), "peak": round(pk, 1),
                                        "unit": "TFLOP/s", "frac": round(tf / pk, 4),
                                        "peak_source": f"bf16 burst x {RATIO['e4m3']} ({peak_src})",
-                                       "traffic": traffic_for("mx_gemm_pair_kernel", source_sha("gemm.cu"), name)}})
+                                       "traffic": traffic_for("mx_gemm_pair_kernel", source_sha("gemm.cu", "gemm.cuh"), name)}})
     # MXFP8 activations times MXFP4 weights (the weights quantized to E2M1 by
     # our quantizer; the E2M1 codes are widened on their way into shared memory)
     w4q, w4s, _, _ = q(W, "e2m1", "floor", "row")
@@ -406,7 +406,7 @@ def extra_gemm_row(args, fn, timed, name, M, N, K, bf16, peak_src, gemm_rows):
                       "roofline": {"bound": "tensor", "achieved": round(tf, 1), "peak": round(pk, 1),
                                    "unit": "TFLOP/s", "frac": round(tf / pk, 4),
                                    "peak_source": f"bf16 burst x {RATIO['e4m3']} ({peak_src})",
-                                   "traffic": traffic_for("mx_gemm_pair_kernel", source_sha("gemm.cu"), name)}})
+                                   "traffic": traffic_for("mx_gemm_pair_kernel", source_sha("gemm.cu", "gemm.cuh"), name)}})
     return args.steps
 
 
@@ -440,7 +440,7 @@ def fp4_part(args, mxq, X, q, timed, bf16, peak_src, gemm_rows):
                       "roofline": {"bound": "tensor", "achieved": round(tf5, 1), "peak": round(pk5, 1),
                                    "unit": "TFLOP/s", "frac": round(tf5 / pk5, 4),
                                    "peak_source": f"bf16 burst x {RATIO['e2m1']} ({peak_src})",
-                                   "traffic": traffic_for("mx_gemm_pair_kernel", source_sha("gemm.cu"),
+                                   "traffic": traffic_for("mx_gemm_pair_kernel", source_sha("gemm.cu", "gemm.cuh"),
                                                           "mxfp4_4096x4096x14336")}})
     # the same product written as MX E2M1 codes + scales (MMA layout: the
     # next MXFP4 product's A operand) straight from the accumulator
