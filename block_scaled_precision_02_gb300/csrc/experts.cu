@@ -808,8 +808,8 @@ __global__ void __launch_bounds__(ROW_T, 2) combine_bwd_ring_kernel(const RowArg
     }
     if (n >= -S && copy_t < a.tokens) {
       const uint32_t dst = to + slot * (ROW_T * U * 16);
-      const int cr = copy_j < 0 ? 0 : static_cast<int>(plan[(at >= S ? at - S : at + S) * ROW_T].x);
-      if (cr >= 0 && cr < max(a.rows, int64_t(1))) {
+      const int cr = copy_j < 0 ? -1 : static_cast<int>(plan[(at >= S ? at - S : at + S) * ROW_T].x);
+      if (copy_j < 0 || (cr >= 0 && cr < a.rows)) {
         const T* const row = copy_j < 0 ? static_cast<const T*>(a.dy) + copy_t * a.ld_dy : src + cr * a.ld;
 #pragma unroll
         for (int u = 0; u < U; ++u)

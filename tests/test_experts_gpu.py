@@ -27,7 +27,7 @@ def np64(t):
 # ------------------------------------------------------------------ sort
 @pytest.mark.parametrize("pattern", PATTERNS)
 @pytest.mark.parametrize("tokens,top,experts", [(1, 1, 1), (1, 8, 64), (3, 2, 7), (100, 3, 5), (515, 2, 16), (2048, 1, 1024),
-                                                (2049, 1, 2), (4097, 5, 33), (5000, 8, 1000), (8192, 4, 64), (8192, 8, 64), (32769, 1, 20), (300000, 1, 128)])
+                                                (2049, 1, 2), (3000, 2, 9), (5000, 2, 12), (12289, 1, 40), (4097, 5, 33), (5000, 8, 1000), (8192, 4, 64), (8192, 8, 64), (32769, 1, 20), (300000, 1, 128)])
 def test_sort(lib, tokens, top, experts, pattern):
     rng = np.random.default_rng(tokens + experts)
     for align, dtype in ((128, torch.int32), (256, torch.int64)):
@@ -370,4 +370,21 @@ def test_a_wrong_plan_reads_and_writes_within_bounds(lib):
     lib.expert_gather(rows[:16], p)
     q = lib.mx_expert_gather(rows[:16], p, "e4m3", "dual")
     assert not q[0].any() and not q[2].any()
-    torch.cuda.synchronize()
+    # the rings, and a plan of no rows at all
+    p, _ = make_plan(lib, rng, 4200, 1, 4)
+    rows = torch.randn(p.rows, 1024, device=dev).to(BF)
+    for r in (2 ** 31 - 1, -(2 ** 31), p.rows):
+        p.slot_row.fill_(r)
+        assert not lib.expert_combine(rows, p, torch.ones(4200, 1, device=dev)).any()
+        assert not lib.expert_combine(rows[:, 1:], p, torch.ones(4200, 1, device=dev)).any()
+        d, dw = lib.expert_combine_backward(rows[:4200], rows, p, torch.ones(4200, 1, device=dev))
+        assert not dw.any()
+    p.slot_row.zero_()
+    dw, w, zero = torch.ones(4200, 1, device=dev), torch.ones(4200, 1, device=dev), torch.zeros(8, dtype=torch.int32, device=dev)
+    y = torch.ones(4200, 1024, dtype=BF, device=dev)
+    stream = torch.cuda.current_stream().cuda_stream
+    at = p.slot_row.data_ptr()
+    assert lib.load().mxq_expert_combine_backward(rows.data_ptr(), 1024, 0, None, 1024, 0, 0, 1024, at, 4200, 1, zero.data_ptr(),
+                                                  zero.data_ptr(), 4, w.data_ptr(), 1, None, dw.data_ptr(), stream) == 0
+    assert lib.load().mxq_expert_combine(None, 0, 1024, 1024, 0, at, 4200, 1, w.data_ptr(), 1, y.data_ptr(), 0, stream) == 0
+    assert not dw.any() and not y.any()
