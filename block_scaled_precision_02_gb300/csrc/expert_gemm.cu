@@ -17,6 +17,9 @@
 // tensor pipe active 81 % of the time; a plain product of 16384 such rows 617),
 // the gradient of 4096 x 4096 187 us; with few tokens the weights' bytes (64 tokens, 16
 // experts of 4096 x 4096: 51 us, 86 % of the copy rate).
+// Columns are a multiple of 128: the last of wider tiles can reach beyond C.  Its
+// loads then bring the next expert's weights or zeros, and what they give is not
+// stored.
 // Order of tiles: expert by expert, down the rows first, so that an expert's
 // weights stream through once while its rows stay in L2.
 #include <algorithm>
@@ -148,7 +151,8 @@ __device__ __forceinline__ void sync_all() {
 // read, before the stores.
 template <int COLS, int NBUF, typename Read, typename Release>
 __device__ __forceinline__ void store_acc(int out_fp32, int row, bool leader, int bar, int& buf, uint8_t* sOut,
-                                          const CUtensorMap* map_c, int cm, int n0, Read read, Release release) {
+                                          const CUtensorMap* map_c, int cm, int n0, int cols, Read read,
+                                          Release release) {
   const auto put = [&](const uint32_t* w, int col) {     // 64 bytes of every row
     if (leader) bulk_wait_read_staging<NBUF>();
     named_bar(bar, 128);
@@ -160,7 +164,7 @@ __device__ __forceinline__ void store_acc(int out_fp32, int row, bool leader, in
     }
     fence_proxy_async_smem();
     named_bar(bar, 128);
-    if (leader) {
+    if (leader && col < cols) {                          // (a last tile can reach beyond C)
       tma_store_2d(map_c, smem_u32(stg), col, cm);
       bulk_commit();
     }
@@ -210,10 +214,10 @@ __device__ __forceinline__ void read_acc(uint32_t lane_addr, int c, uint32_t* v)
 // Zeros to this warp's 32 rows of a tile, row by row.
 template <int BN>
 __device__ __forceinline__ void store_zeros(const Params& p, int q, int lane, int cm, int n0) {
-  const int size = p.out_fp32 ? 4 : 2;
+  const int size = p.out_fp32 ? 4 : 2, bytes = static_cast<int>(min(static_cast<int64_t>(BN), p.ldc - n0)) * size;
   uint8_t* row = static_cast<uint8_t*>(p.c) + (static_cast<int64_t>(cm + q * 32) * p.ldc + n0) * size;
   for (int r = 0; r < 32; ++r, row += p.ldc * size)
-    for (int b = lane * 16; b < BN * size; b += 512) *reinterpret_cast<uint4*>(row + b) = make_uint4(0, 0, 0, 0);
+    for (int b = lane * 16; b < bytes; b += 512) *reinterpret_cast<uint4*>(row + b) = make_uint4(0, 0, 0, 0);
 }
 
 template <int KIND, int CTAS, int BN, int MODE>
@@ -422,7 +426,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       named_bar(1 + grp, 128);
       if (epi_fail[grp]) { *abort_flag = 1; break; }
       tc_fence_after();
-      store_acc<C::COLS, C::NBUF>(p.out_fp32, row, leader, 1 + grp, buf, staging, &map_c, cm, n0,
+      store_acc<C::COLS, C::NBUF>(p.out_fp32, row, leader, 1 + grp, buf, staging, &map_c, cm, n0, static_cast<int>(p.ldc),
                                   [&](int c, uint32_t* v) { read_acc(lane_addr, c, v); }, release);
     }
     if (leader) bulk_wait_all();
@@ -516,7 +520,7 @@ int launch(Args& g, cudaStream_t st) {
   Params& p = g.p;
   const int64_t m_rows = MODE == PRODUCT ? g.c_rows : p.m_rows;
   p.tiles_m = static_cast<int>(m_rows / Cf::TM);
-  p.tiles_n = static_cast<int>(g.c_cols / Cf::BN);
+  p.tiles_n = static_cast<int>((g.c_cols + Cf::BN - 1) / Cf::BN);
   const int64_t ntiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * (MODE == WGRAD ? p.experts : 1);
   if (ntiles > 0x7FFF0000) return MXQ_ERR_BAD_SHAPE;
   p.ntiles = static_cast<int>(ntiles);
@@ -545,13 +549,20 @@ int launch(Args& g, cudaStream_t st) {
 //    and 13 on 128 x 128), and for the weights' gradient from 1536 rows an expert
 //    on (2048 rows, 8 experts: 194 and 212; 256 rows of 2048 x 2048: 72 and 55);
 //  * 128 x 256, from two tiles an SM on (8192 tokens of 2, align 128: 210 us, 266
-//    on 128 x 128; 512 tokens over 8 experts of 1024 x 1024: 7.6 and 6.0).
+//    on 128 x 128; 512 tokens over 8 experts of 1024 x 1024: 7.6 and 6.0);
+//  * both for an odd multiple of 128 columns only where half a tile's waste is
+//    small: pairs from 640 on (6127 tokens of 2, 5 experts: 23.3 us against 24.4; 384
+//    columns 19.4 and 16.6; the gradient of 2816 x 6272: 161 and 224), 128 x 256
+//    from 896 on (28.0 and 29.5; 1664: 44.5 and 49.7), for gradients from 2048 on
+//    (4224 x 3200: 25.1 and 26.2; 1024 x 1152: 26.7 and 23.1).
 template <int KIND, int MODE>
 int choose(Args& g, bool pair, cudaStream_t st) {
   const int64_t sms = sm_count(), rows = MODE == PRODUCT ? g.c_rows : g.p.m_rows * static_cast<int64_t>(g.p.experts);
-  const int64_t blocks = rows / 128 * (g.c_cols / 128);           // 128 x 128 tiles
-  if (pair && 2 * (blocks / 4) >= sms && (MODE == PRODUCT || g.p.rows >= 1536ll * g.p.experts)) return launch<KIND, 2, 256, MODE>(g, st);
-  if (g.c_cols % 256 == 0 && blocks / 2 >= 2 * sms) return launch<KIND, 1, 256, MODE>(g, st);
+  const int64_t wide = (g.c_cols + 255) / 256;                    // columns of 256-wide tiles
+  const bool even = g.c_cols % 256 == 0;
+  if (pair && (even || g.c_cols >= 640) && 2 * (rows / 256 * wide) >= sms && (MODE == PRODUCT || g.p.rows >= 1536ll * g.p.experts))
+    return launch<KIND, 2, 256, MODE>(g, st);
+  if ((even || g.c_cols >= (MODE == PRODUCT ? 896 : 2048)) && rows / 128 * wide >= 2 * sms) return launch<KIND, 1, 256, MODE>(g, st);
   return launch<KIND, 1, 128, MODE>(g, st);
 }
 
@@ -606,7 +617,7 @@ extern "C" int mxq_expert_gemm(const void* a_q, const uint8_t* a_s, int a_fmt, c
   g.p.b_rows = b_along_k ? 0 : static_cast<int>(N);
   g.p.b_steps = b_along_k;
   g.p.out_fp32 = out_fp32;
-  return run<PRODUCT>(g, align == 256 && N % 256 == 0, stream);
+  return run<PRODUCT>(g, align == 256, stream);
 }
 
 extern "C" int mxq_expert_wgrad(const void* a_q, const uint8_t* a_s, int a_fmt, const void* b_q, const uint8_t* b_s,
@@ -628,5 +639,5 @@ extern "C" int mxq_expert_wgrad(const void* a_q, const uint8_t* a_s, int a_fmt, 
   g.p.experts = experts, g.p.align = align, g.p.rows = static_cast<int>(rows);
   g.p.m_rows = static_cast<int>(N);
   g.p.out_fp32 = out_fp32;
-  return run<WGRAD>(g, N % 256 == 0 && K % 256 == 0, stream);
+  return run<WGRAD>(g, N % 256 == 0, stream);
 }

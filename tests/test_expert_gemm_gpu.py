@@ -108,9 +108,10 @@ def test_weight_gradient_exactly(lib, tokens, top, experts, pattern, align, n, k
 
 @pytest.mark.parametrize("out", [BF, F32])
 @pytest.mark.parametrize("fmt,b_fmt", PAIRS)
-@pytest.mark.parametrize("align,n", [(128, 2048), (128, 2176), (256, 1024)])
+@pytest.mark.parametrize("align,n", [(128, 2048), (128, 2176), (256, 1024), (256, 1152)])
 def test_products_of_many_tiles_exactly(lib, align, n, fmt, b_fmt, out):
-    """As many tiles as the wide tiles and the pairs take, an expert without rows among them."""
+    """As many tiles as the wide tiles and the pairs take (of odd multiples of 128
+    columns, too: the last tile reaches beyond C), an expert without rows among them."""
     experts, K = 5, 512
     e = np.minimum(routing(np.random.default_rng(2), 2500, 2, experts, "skewed") * 2, experts - 1)
     e[e == 3] = 4
@@ -128,7 +129,8 @@ def test_products_of_many_tiles_exactly(lib, align, n, fmt, b_fmt, out):
 
 @pytest.mark.parametrize("out", [BF, F32])
 @pytest.mark.parametrize("fmt,b_fmt", PAIRS)
-@pytest.mark.parametrize("tokens,experts,n,k", [(700, 5, 1024, 2048), (1600, 2, 1536, 1792), (500, 6, 1152, 896)])
+@pytest.mark.parametrize("tokens,experts,n,k", [(700, 5, 1024, 2048), (700, 5, 1024, 2176), (1600, 2, 1536, 1792),
+                                                  (1600, 2, 1536, 1920), (500, 6, 1152, 896)])
 def test_weight_gradient_of_many_tiles_exactly(lib, tokens, experts, n, k, fmt, b_fmt, out):
     """Wide tiles, pairs (from 1536 rows an expert on) and small tiles, an expert without rows among them."""
     e = routing(np.random.default_rng(3), tokens, 2, experts, "even")
