@@ -234,6 +234,7 @@ struct RowArgs {
   int w_f32;
   int64_t tokens, rows, cols, ld, ld_dy;
   int top, experts;
+  int dy_rows;                            // backward: "tokens" that share a row of dy (1; top where slots go apart)
   int lanes;                              // of a warp to a row: 4 .. 32
   int pieces;                             // stretches of lanes * U vectors to a row
 };
@@ -648,7 +649,7 @@ __global__ void __launch_bounds__(BWD_T, 4) combine_bwd_kernel(const RowArgs a) 
   int64_t t = blockIdx.x * static_cast<int64_t>(TEAMS) + team;
   fetch(t, 0);
   for (; t < a.tokens; t += stride) {
-    const TY* const dy = static_cast<const TY*>(a.dy) + t * a.ld_dy;
+    const TY* const dy = static_cast<const TY*>(a.dy) + (a.dy_rows > 1 ? t / a.dy_rows : t) * a.ld_dy;
     float d[NV][VE];
     const bool whole = !ANY && a.cols <= G * 32 * NV * VE;       // dy is read once
     if (whole) {
@@ -954,10 +955,18 @@ int run_combine(const RowArgs& a, bool vectors, cudaStream_t st) {
   return run_combine_direct<T, TY, 1>(a, st);
 }
 
+// Warps of tokens per SM up to which each slot is a team's own work, which reads its
+// token's dy again: so few tokens leave most of the GPU idle and a token's slots wait
+// for one another (18 tokens of 6 slots, 2241 columns: 4.3 us, 9.6 with a team to a
+// token; 300 of 2, 4096: 4.7 and 5.2; 600 of 2: 7.1 and 5.4).
+constexpr int APART = 16;
+
 template <typename T, typename TY, int VE, int G, int NV, bool ANY>
-int launch_backward(const RowArgs& a, cudaStream_t st) {
+int launch_backward(RowArgs a, cudaStream_t st) {
   static std::atomic<int> known[64];
   unsigned grid = 0;
+  a.dy_rows = 1;
+  if (a.top > 1 && a.tokens * G < APART * sm_count()) a.dy_rows = a.top, a.tokens *= a.top, a.top = 1;
   const int64_t want = std::max<int64_t>((a.tokens * G + BWD_WARPS - 1) / BWD_WARPS,
                                          (a.rows * a.cols + BWD_T * VE - 1) / (BWD_T * VE));
   if (const int rc = stay(combine_bwd_kernel<T, TY, VE, G, NV, ANY>, want, known, &grid, 0, BWD_T)) return rc;
