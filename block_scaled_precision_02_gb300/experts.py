@@ -27,7 +27,10 @@ class ExpertPlan:
     counts        [experts] slots of each expert
     slot_row      [tokens][top] row of each slot, -1 where it is dropped
     row_slot      [rows] slot of each row, -1 in padding and behind the last stretch
-    block_expert  [rows / align] expert of each block of rows, -1 behind the last stretch"""
+    block_expert  [rows / align] expert of each block of rows, -1 behind the last stretch
+
+    A plan is neither copied nor pickled (its addresses are those of its own
+    allocation): sort again, or keep the tensors."""
 
     __slots__ = ("_buffer", "_at", "_pointers", "tokens", "top", "experts", "rows", "align")
 
@@ -48,6 +51,9 @@ class ExpertPlan:
         self._at = (0, a1, a2, a3, a4, a5, end)
         self._pointers = (p, p + 4 * a1, p + 4 * a2, p + 4 * a3, p + 4 * a4, p + 4 * a5)
         self.tokens, self.top, self.experts, self.rows, self.align = tokens, top, experts, rows, align
+
+    def __reduce_ex__(self, protocol):
+        raise TypeError("a plan cannot be copied or pickled: it holds its allocation's addresses")
 
     @property
     def offsets(self):

@@ -2,8 +2,10 @@
 launch.  CPU only: the binding's checks raise, and the C entry points return
 their status."""
 
+import copy
 import ctypes
 import os
+import pickle
 
 import pytest
 import torch
@@ -209,3 +211,11 @@ def test_c_products(so):
     assert so.mxq_expert_wgrad(*[2 if i in (2, 5) else v for i, v in enumerate(wg)]) == BAD_SHAPE      # both E2M1: align 256
     assert so.mxq_expert_wgrad(*[None if i == 12 else v for i, v in enumerate(wg)]) == BAD_ARG
     assert so.mxq_expert_wgrad(*[200 if i == 6 else v for i, v in enumerate(wg)]) == BAD_SHAPE
+
+
+def test_plan_is_not_copied():
+    # a copy's addresses would be the original's, whose memory may be gone
+    p = plan()
+    for call in (copy.copy, copy.deepcopy, pickle.dumps):
+        with pytest.raises(TypeError, match="copied or pickled"):
+            call(p)
