@@ -958,15 +958,17 @@ int run_combine(const RowArgs& a, bool vectors, cudaStream_t st) {
 // Warps of tokens per SM up to which each slot is a team's own work, which reads its
 // token's dy again: so few tokens leave most of the GPU idle and a token's slots wait
 // for one another (18 tokens of 6 slots, 2241 columns: 4.3 us, 9.6 with a team to a
-// token; 300 of 2, 4096: 4.7 and 5.2; 600 of 2: 7.1 and 5.4).
-constexpr int APART = 16;
+// token).  Aligned rows, 4096 bf16 columns: 250 tokens of 2 slots 4.7 and 5.2, of 8
+// slots 11.1 and 10.3; 325 of 2: 5.8 and 5.4.  Others cost more instructions: 325 of 4
+// slots, 1021 float32 columns 7.1 and 7.9; 400 8.0 and 8.0; 475 8.6 and 8.0.
+constexpr int apart(bool any) { return any ? 20 : 12; }
 
 template <typename T, typename TY, int VE, int G, int NV, bool ANY>
 int launch_backward(RowArgs a, cudaStream_t st) {
   static std::atomic<int> known[64];
   unsigned grid = 0;
   a.dy_rows = 1;
-  if (a.top > 1 && a.tokens * G < APART * sm_count()) a.dy_rows = a.top, a.tokens *= a.top, a.top = 1;
+  if (a.top > 1 && a.tokens * G < apart(ANY) * sm_count()) a.dy_rows = a.top, a.tokens *= a.top, a.top = 1;
   const int64_t want = std::max<int64_t>((a.tokens * G + BWD_WARPS - 1) / BWD_WARPS,
                                          (a.rows * a.cols + BWD_T * VE - 1) / (BWD_T * VE));
   if (const int rc = stay(combine_bwd_kernel<T, TY, VE, G, NV, ANY>, want, known, &grid, 0, BWD_T)) return rc;
