@@ -286,6 +286,38 @@ def test_combine_backward_of_many_tokens(lib, tokens, top, experts, cols, dtype,
     assert torch.equal(again[0], drows) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("cols", [512, 4096, 509, 2049])
+@pytest.mark.parametrize("dtype,dytype", [(BF, F32), (F32, BF)])
+def test_combine_backward_of_few_tokens(lib, cols, dtype, dytype):
+    """A few tokens and, among thousands of them, the same ones: what each gets is
+    the same, but for the order of a sum where rows lie differently."""
+    many, few, top, E = 4200, 37, 5, 6
+    g = torch.Generator(device=dev).manual_seed(cols)
+    experts = torch.randint(-1, E, (many, top), generator=g, device=dev)
+    rows_of = torch.randn(many * top, cols, generator=g, device=dev).to(dtype)       # by slot
+    dy = torch.randn(many, cols + 3, generator=g, device=dev).to(dytype)[:, :cols]
+    w = torch.rand(many, top, generator=g, device=dev)
+    got = []
+    for T in (few, many):
+        plan = lib.expert_sort(experts[:T].contiguous(), E, 128)
+        live = plan.slot_row >= 0
+        at = plan.slot_row[live].long()
+        rows = torch.zeros(plan.rows, cols, dtype=dtype, device=dev)
+        rows[at] = rows_of[: T * top].view(T, top, cols)[live]
+        drows, dw = lib.expert_combine_backward(dy[:T], rows, plan, w[:T].contiguous())
+        pad = torch.ones(plan.rows, dtype=torch.bool, device=dev)
+        pad[at] = False
+        assert not drows[pad].any() and not dw[~live].any()
+        mine = live.clone()
+        mine[few:] = False
+        got.append((drows[plan.slot_row[mine].long()], dw[:few]))
+    (da, wa), (db, wb) = got
+    assert torch.equal(da, db)
+    # a sum of n products in any order: n half steps of the sum of magnitudes, twice
+    mag = (dy[:few, None, :].double() * rows_of[: few * top].view(few, top, cols).double()).abs().sum(2)
+    assert ((wa - wb).abs().double() <= 2 * cols * 2.0 ** -24 * mag).all()
+
+
 def test_gradients_against_differences(lib):
     """The sum is linear in the rows and in the weights: a difference over a
     step h is the gradient up to the float32 rounding of both sums, 4 steps of
