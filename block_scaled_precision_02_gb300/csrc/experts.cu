@@ -620,11 +620,13 @@ constexpr int BWD_T = 256, BWD_WARPS = BWD_T / 32;
 // Few tokens, rows without a common alignment, longer ones than the ring takes, dy
 // of another type: G of a CTA's BWD_WARPS warps take a token; dy's NV vectors of a
 // lane stay in registers while the rows of its slots pass, two at a time.  Longer
-// rows go round in stretches, whose parts of the sums are added up.  Four CTAs an
-// SM, although some forms then spill: what counts is rows in flight (8192 x 4096:
-// 65 us, at three CTAs 71, at two of 512 threads 77).
+// rows, and those without alignment, go round in stretches, whose parts of the sums
+// are added up.  Four CTAs an SM, although some forms then spill: what counts is rows
+// in flight (8192 x 4096: 65 us, at three CTAs 71, at two of 512 threads 77).  Without
+// alignment and G = 8 six (3047 x 14335, 4 slots: 152 us, at four 173), else four
+// (1021 bf16 columns: 18.4 us, at five 20.1).
 template <typename T, typename TY, int VE, int G, int NV, bool ANY>
-__global__ void __launch_bounds__(BWD_T, 4) combine_bwd_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(BWD_T, ANY && G == 8 ? 6 : 4) combine_bwd_kernel(const RowArgs a) {
   constexpr int TEAMS = BWD_WARPS / G;
   __shared__ float red[2][TEAMS][2][G];
   grid_dep_launch();
@@ -956,12 +958,13 @@ int run_combine(const RowArgs& a, bool vectors, cudaStream_t st) {
 }
 
 // Warps of tokens per SM up to which each slot is a team's own work, which reads its
-// token's dy again: so few tokens leave most of the GPU idle and a token's slots wait
-// for one another (18 tokens of 6 slots, 2241 columns: 4.3 us, 9.6 with a team to a
-// token).  Aligned rows, 4096 bf16 columns: 250 tokens of 2 slots 4.7 and 5.2, of 8
-// slots 11.1 and 10.3; 325 of 2: 5.8 and 5.4.  Others cost more instructions: 325 of 4
-// slots, 1021 float32 columns 7.1 and 7.9; 400 8.0 and 8.0; 475 8.6 and 8.0.
-constexpr int apart(bool any) { return any ? 20 : 12; }
+// token's dy again: so few tokens leave part of the GPU idle and a token's slots wait
+// for one another.  Aligned rows, 4096 bf16 columns: 250 tokens of 2 slots 4.7 us and
+// 5.2 with a team to a token, of 8 slots 11.1 and 10.3; 325 of 2: 5.8 and 5.4.  Others
+// cost more instructions, and win until 32 warps fill an SM: 1021 bf16 columns, 4
+// slots, 1216 tokens 6.2 and 14.7, 3648 (24 warps) 16.7 and 19.2, 4864 21.7 and 20.5;
+// 2049 float32, 456 tokens 10.0 and 12.0, 608 13.4 and 13.9.
+constexpr int apart(bool any) { return any ? 28 : 12; }
 
 template <typename T, typename TY, int VE, int G, int NV, bool ANY>
 int launch_backward(RowArgs a, cudaStream_t st) {
@@ -988,11 +991,19 @@ int launch_backward_ring(const RowArgs& a, cudaStream_t st) {
   return launch_pdl(combine_bwd_ring_kernel<T, VE, G>, dim3(grid), dim3(ROW_T), bwd_ring_smem(), st, a);
 }
 
-// As many warps to a token as its vectors fill, eight at most.
+// As many warps to a token as its vectors fill, eight at most.  Rows without
+// alignment pay for every vector in instructions and take fewer warps, one vector a
+// lane: 3047 tokens of 4 slots, 501 float32 columns (125 vectors) 17.0 us with one
+// warp, 18.6 with two; 695 (174) 24.8 with two, 27.6 with four; 1021 (255) 29.7 with four,
+// 32.8 with two, 36.4 with eight; 2049 (512) 47.9 with eight, 52.7 with four.
 template <typename T, typename TY, int VE>
 int run_backward(const RowArgs& a, bool vectors, cudaStream_t st) {
-  if (!vectors)
-    return a.cols <= 64 * VE ? launch_backward<T, TY, VE, 1, 1, true>(a, st) : launch_backward<T, TY, VE, 8, 2, true>(a, st);
+  if (!vectors) {
+    if (a.cols <= 128 * VE) return launch_backward<T, TY, VE, 1, 1, true>(a, st);
+    if (a.cols <= 192 * VE) return launch_backward<T, TY, VE, 2, 1, true>(a, st);
+    if (a.cols <= 384 * VE) return launch_backward<T, TY, VE, 4, 1, true>(a, st);
+    return launch_backward<T, TY, VE, 8, 1, true>(a, st);
+  }
   if constexpr (sizeof(T) == sizeof(TY))
     if (a.tokens * a.cols >= BWD_RING && a.cols > 64 * VE && a.cols <= 1024 * VE) {
       if (a.cols <= 128 * VE) return launch_backward_ring<T, VE, 1>(a, st);
