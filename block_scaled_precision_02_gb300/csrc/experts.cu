@@ -234,7 +234,7 @@ struct RowArgs {
   int w_f32;
   int64_t tokens, rows, cols, ld, ld_dy;
   int top, experts;
-  int dy_rows;                            // backward: "tokens" that share a row of dy (1; top where slots go apart)
+  int shared;                             // "tokens" that share a row of x or dy: top where slots go apart, else 1
   int lanes;                              // of a warp to a row: 4 .. 32
   int pieces;                             // stretches of lanes * U vectors to a row
 };
@@ -362,8 +362,8 @@ __device__ __forceinline__ void zero_padding(const RowArgs& a) {
   zero_rows<T, VE, ANY, THREADS>(a, last, a.rows - last, blockIdx.x, gridDim.x);
 }
 
-// A token's stretch is read once and written to the row of each of its slots
-// (read once a row instead, tokens of several experts would come twice from HBM).
+// A token's stretch is read once and written to the row of each of its slots (read
+// once a row instead, many tokens of several experts would come twice from HBM).
 template <typename T, int VE, bool ANY>
 __global__ void __launch_bounds__(ROW_T) gather_kernel(const RowArgs a) {
   grid_dep_launch();
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(ROW_T) gather_kernel(const RowArgs a) {
   for (int64_t n = 0; n < w.rounds; ++n, at.next(w)) {
     const int64_t t = at.row + w.group, v0 = static_cast<int64_t>(at.piece) * a.lanes * U + w.lane;
     if (t >= a.tokens) continue;
-    const T* const x = static_cast<const T*>(a.src) + t * a.ld;
+    const T* const x = static_cast<const T*>(a.src) + (a.shared > 1 ? t / a.shared : t) * a.ld;
     if constexpr (!ANY) {
       Vec<T, VE> v[U];
 #pragma unroll
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(BWD_T, ANY && G == 8 ? 6 : 4) combine_bwd_kern
   int64_t t = blockIdx.x * static_cast<int64_t>(TEAMS) + team;
   fetch(t, 0);
   for (; t < a.tokens; t += stride) {
-    const TY* const dy = static_cast<const TY*>(a.dy) + (a.dy_rows > 1 ? t / a.dy_rows : t) * a.ld_dy;
+    const TY* const dy = static_cast<const TY*>(a.dy) + (a.shared > 1 ? t / a.shared : t) * a.ld_dy;
     float d[NV][VE];
     const bool whole = !ANY && a.cols <= G * 32 * NV * VE;       // dy is read once
     if (whole) {
@@ -911,11 +911,22 @@ int64_t walk_ctas(const RowArgs& a) {
   return ((a.tokens + per - 1) / per * a.pieces + ROW_WARPS - 1) / ROW_WARPS;
 }
 
+// Warps of tokens per SM up to which a warp takes slots instead of tokens, each of
+// which reads its token again: a token's rows are then written by as many warps, not
+// one after another.  1024 bf16 columns, 4 slots: 1216 tokens (8 warps) 4.5 us against
+// 6.0, 2432 6.0 and 7.2, 4864 8.8 and 8.2.  1021 columns, which are read again for
+// every row either way, but in more instructions: 1216 tokens 6.9 and 8.4, 2432 9.3
+// and 8.9, 9728 40 and 24.
+constexpr int gather_apart(bool any) { return any ? 12 : 24; }
+
 template <typename T, int VE, bool ANY>
 int run_gather(RowArgs a, cudaStream_t st) {
   static std::atomic<int> known[64];
   set_lanes(a, VE);
   unsigned grid = 0;
+  a.shared = 1;
+  if (a.top > 1 && walk_ctas(a) * ROW_WARPS < gather_apart(ANY) * static_cast<int64_t>(sm_count()))
+    a.shared = a.top, a.tokens *= a.top, a.top = 1;
   const int64_t want = std::max<int64_t>(walk_ctas(a), (a.rows * a.cols + ROW_T * VE - 1) / (ROW_T * VE));
   if (const int rc = stay(gather_kernel<T, VE, ANY>, want, known, &grid)) return rc;
   return launch_pdl(gather_kernel<T, VE, ANY>, dim3(grid), dim3(ROW_T), 0, st, a);
@@ -970,8 +981,8 @@ template <typename T, typename TY, int VE, int G, int NV, bool ANY>
 int launch_backward(RowArgs a, cudaStream_t st) {
   static std::atomic<int> known[64];
   unsigned grid = 0;
-  a.dy_rows = 1;
-  if (a.top > 1 && a.tokens * G < apart(ANY) * sm_count()) a.dy_rows = a.top, a.tokens *= a.top, a.top = 1;
+  a.shared = 1;
+  if (a.top > 1 && a.tokens * G < apart(ANY) * sm_count()) a.shared = a.top, a.tokens *= a.top, a.top = 1;
   const int64_t want = std::max<int64_t>((a.tokens * G + BWD_WARPS - 1) / BWD_WARPS,
                                          (a.rows * a.cols + BWD_T * VE - 1) / (BWD_T * VE));
   if (const int rc = stay(combine_bwd_kernel<T, TY, VE, G, NV, ANY>, want, known, &grid, 0, BWD_T)) return rc;

@@ -286,6 +286,23 @@ def test_combine_backward_of_many_tokens(lib, tokens, top, experts, cols, dtype,
     assert torch.equal(again[0], drows) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols", [11, 128, 1021, 4096])
+@pytest.mark.parametrize("tokens", [37, 1300, 5000])
+def test_gather_bit_for_bit(lib, tokens, cols, dtype):
+    """Fewer and more tokens than fill the GPU, every bit pattern (NaN, too), rows
+    with gaps between them."""
+    g = torch.Generator(device=dev).manual_seed(tokens + cols)
+    bits, size = (torch.int16, 2) if dtype == BF else (torch.int32, 4)
+    x = torch.randint(-2 ** 15, 2 ** 15, (tokens, (cols + 5) * size // 2), generator=g, device=dev).to(torch.int16).view(dtype)[:, :cols]
+    plan = lib.expert_sort(torch.randint(-1, 7, (tokens, 3), generator=g, device=dev), 7, 128)
+    got = lib.expert_gather(x, plan).view(bits)
+    want = torch.zeros(plan.rows, cols, dtype=bits, device=dev)
+    live = plan.row_slot >= 0
+    want[live] = x.contiguous().view(bits)[(plan.row_slot[live] // 3).long()]
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("cols", [512, 4096, 509, 2049])
 @pytest.mark.parametrize("dtype,dytype", [(BF, F32), (F32, BF)])
 def test_combine_backward_of_few_tokens(lib, cols, dtype, dytype):
