@@ -418,7 +418,10 @@ __global__ void __launch_bounds__(ROW_T) gather_kernel(const RowArgs a) {
 
 // ---------------------------------------------------------------- combine
 // Few tokens, or rows that have no vectors: a warp takes a stretch of a token
-// and reads its slots' rows straight into registers.
+// and reads its slots' rows straight into registers, two slots at a time where they
+// are vectors (one token of 8 slots, 4096 bf16 columns: 4.3 us, one at a time 6.8), one
+// where they are elements (515 x 2049 of 3 slots 3.5 us, two at a time 3.8; 2000 x
+// 1021 of 8 9.1 and 9.9).
 template <typename T, typename TY, int VE>
 __global__ void __launch_bounds__(ROW_T) combine_direct_kernel(const RowArgs a) {
   grid_dep_launch();
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(ROW_T) combine_direct_kernel(const RowArgs a) 
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < VE; ++i) acc[u][i] = 0.f;
-#pragma unroll 2
+#pragma unroll (VE == 1 ? 1 : 2)
   for (int j = 0; j < a.top; ++j) {
     const int64_t slot = t * a.top + j, r = row_of(a, slot);
     if (r < 0) continue;
@@ -952,7 +955,7 @@ int run_combine_direct(RowArgs a, cudaStream_t st) {
 }
 
 // The ring pays from about 2^21 elements of y on (8192 x 4096 bf16: 32 us, read
-// directly 47; 515 x 2049 float32: 8.9 and 3.7).  Rows without a common alignment
+// directly 47; 515 x 2049 float32: 8.9 and 3.5).  Rows without a common alignment
 // take it as bf16 of DIRECT_COLS columns or more (8192 x 4095: 26 us, element by
 // element 49), as their single elements go round apart (16384 x 77, 4 slots: 40
 // and 6); float32 ones are read element by element as fast (5238 x 1023, 5
