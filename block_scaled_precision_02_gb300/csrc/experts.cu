@@ -1158,8 +1158,8 @@ extern "C" int mxq_expert_combine_backward(const void* dy, int64_t ld_dy, int dy
   if (!valid_type(type) || !valid_type(dy_type) || !valid_type(w_type)) return MXQ_ERR_BAD_ARG;
   if (!plan_sizes(tokens, top, rows) || cols < 1 || cols > kMaxCols || ld < cols || ld_dy < cols) return MXQ_ERR_BAD_SHAPE;
   if (experts < 1 || experts > kMaxExperts) return MXQ_ERR_BAD_SHAPE;
-  if ((rows && (!rows_in || !offsets || !counts || !drows)) || (tokens && (!dy || !slot_row || !weights || !dweights)))
-    return MXQ_ERR_BAD_ARG;
+  if ((rows && (!rows_in || !drows)) || (tokens && (!dy || !slot_row || !weights || !dweights))) return MXQ_ERR_BAD_ARG;
+  if ((rows || tokens) && (!offsets || !counts)) return MXQ_ERR_BAD_ARG;     // every launch reads the stretches' ends
   if (!aligned_to(rows_in, type_size(type)) || !aligned_to(dy, type_size(dy_type)) || !aligned_to(drows, type_size(type)) ||
       !aligned_to(slot_row, 4) || !aligned_to(offsets, 4) || !aligned_to(counts, 4) || !aligned_to(weights, type_size(w_type)) ||
       !aligned_to(dweights, 4))

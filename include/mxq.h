@@ -557,6 +557,7 @@ int mxq_expert_combine(const void* rows_in, int64_t rows, int64_t cols,
  *                 for a dropped slot
  * dy       [tokens][ld_dy] of dy_type; drows [rows][cols] of type; must overlap
  *          neither dy nor rows_in.  dweights float [tokens][top].
+ * offsets, counts  needed wherever rows or tokens is not 0.
  * Sums in a fixed order. */
 int mxq_expert_combine_backward(const void* dy, int64_t ld_dy, int dy_type,
                                 const void* rows_in, int64_t ld, int type,

@@ -219,3 +219,16 @@ def test_plan_is_not_copied():
     for call in (copy.copy, copy.deepcopy, pickle.dumps):
         with pytest.raises(TypeError, match="copied or pickled"):
             call(p)
+
+
+def test_c_backward_reads_the_stretches_whenever_it_runs(so):
+    # tokens without rows, rows without tokens: both launch, and every launch reads offsets and counts
+    none = [P, 8, 0, None, 8, 1, 0, 8, P, 4, 2, P, P, 3, P, 1, None, P, None]
+    rest = [None, 8, 0, P, 8, 1, 384, 8, None, 0, 2, P, P, 3, None, 1, P, None, None]
+    for ok in (none, rest):
+        for at in (11, 12):
+            assert so.mxq_expert_combine_backward(*[None if i == at else v for i, v in enumerate(ok)]) == BAD_ARG, at
+        assert so.mxq_expert_combine_backward(*ok) == NO_DEVICE
+    # nothing to do: nothing is needed
+    idle = [None, 8, 0, None, 8, 1, 0, 8, None, 0, 2, None, None, 3, None, 1, None, None, None]
+    assert so.mxq_expert_combine_backward(*idle) in (0, NO_DEVICE)
