@@ -554,19 +554,36 @@ int launch(Args& g, cudaStream_t st) {
 //    on (2048 rows, 8 experts: 194 and 212; 256 rows of 2048 x 2048: 72 and 55);
 //  * 128 x 256, from two tiles an SM on (8192 tokens of 2, align 128: 210 us, 266
 //    on 128 x 128; 512 tokens over 8 experts of 1024 x 1024: 7.6 and 6.0);
-//  * both for an odd multiple of 128 columns only where half a tile's waste is
-//    small: pairs from 640 on (6127 tokens of 2, 5 experts: 23.3 us against 24.4; 384
-//    columns 19.4 and 16.6; the gradient of 2816 x 6272: 161 and 224), 128 x 256
-//    from 896 on (28.0 and 29.5; 1664: 44.5 and 49.7), for gradients from 2048 on
-//    (4224 x 3200: 25.1 and 26.2; 1024 x 1152: 26.7 and 23.1).
+//  * both for an odd multiple of 128 columns only where the half of a last tile that
+//    is wasted, and the longer tile ends, are small against the contraction (a step:
+//    128 bytes of it; float32 outputs, whose tile ends take twice as long, count half).
+//    6127 tokens of 2, 5 experts, against 128 x 128:
+//      pairs from 12 steps and 640 columns on (1536 x 640: 17.7 us and 18.9; 1024 x 640
+//      14.3 and 14.0), from 8 and 1152 (1024 x 1920: 29.0 and 30.1; 512 x 1920 24.7
+//      and 22.3); E2M1, with one storing group, from 16 and 640 (4096 x 640: 22.1 and
+//      23.3; 2048 x 640 16.6 and 14.2), from 8 and 2048 (2048 x 4224: 58.5 and 62.7;
+//      1024 x 4224 54.5 and 43.9);
+//      128 x 256 from 8 steps and 896 columns on (1024 x 1920: 27.5 and 29.4; 512 x 1920
+//      22.9 and 21.5), from 2048 whatever the steps (512 x 4224: 40.5 and 42.5);
+//    gradients: pairs from 640 on (8192 tokens of 2, 8 experts, 2048 x 896: 33.2 and
+//    37.3; of small ones the rounds of tiles decide, 1024 x 640 22.8 and 20.3), 128 x 256 from
+//    2048 on (4224 x 3200: 25.1 and 26.2; 1024 x 1152: 26.7 and 23.1).
 template <int KIND, int MODE>
 int choose(Args& g, bool pair, cudaStream_t st) {
   const int64_t sms = sm_count(), rows = MODE == PRODUCT ? g.c_rows : g.p.m_rows * static_cast<int64_t>(g.p.experts);
   const int64_t wide = (g.c_cols + 255) / 256;                    // columns of 256-wide tiles
   const bool even = g.c_cols % 256 == 0;
-  if (pair && (even || g.c_cols >= 640) && 2 * (rows / 256 * wide) >= sms && (MODE == PRODUCT || g.p.rows >= 1536ll * g.p.experts))
+  // columns from which odd multiples of 128 take pairs, and 128 x 256
+  int64_t odd_pair = 640, odd_wide = 2048;
+  if (MODE == PRODUCT) {
+    constexpr bool FP4 = KIND == mxq::gemm::KIND_MXF4;
+    const int64_t steps = g.ka / (FP4 ? 256 : 128) / (g.p.out_fp32 ? 2 : 1);
+    odd_pair = steps >= (FP4 ? 16 : 12) ? 640 : steps < 8 ? INT64_MAX : FP4 ? 2048 : 1152;
+    odd_wide = steps >= 8 ? 896 : 2048;
+  }
+  if (pair && (even || g.c_cols >= odd_pair) && 2 * (rows / 256 * wide) >= sms && (MODE == PRODUCT || g.p.rows >= 1536ll * g.p.experts))
     return launch<KIND, 2, 256, MODE>(g, st);
-  if ((even || g.c_cols >= (MODE == PRODUCT ? 896 : 2048)) && rows / 128 * wide >= 2 * sms) return launch<KIND, 1, 256, MODE>(g, st);
+  if ((even || g.c_cols >= odd_wide) && rows / 128 * wide >= 2 * sms) return launch<KIND, 1, 256, MODE>(g, st);
   return launch<KIND, 1, 128, MODE>(g, st);
 }
 

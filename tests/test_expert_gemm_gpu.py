@@ -127,6 +127,39 @@ def test_products_of_many_tiles_exactly(lib, align, n, fmt, b_fmt, out):
     assert lib.last_device_status() == 0
 
 
+def blocks_of(rng, rows, k, fmt):
+    """integer_operand's codes, scales and float64 values, of few blocks of 128
+    rows that come again in a random order."""
+    q, s = integer_operand(rng, 7 * 128, k, fmt)
+    pick = torch.from_numpy(rng.integers(0, 7, size=rows // 128)).to(dev)
+    v = decoded(q, s, fmt).reshape(7, 128, k)[pick.cpu().numpy()].reshape(rows, k)
+    return q.view(7, 128, -1)[pick].view(rows, -1), s.view(7, -1)[pick].view(-1), v
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("fmt,b_fmt", PAIRS)
+@pytest.mark.parametrize("align,n,steps", [(128, 1152, 8), (256, 1152, 7), (256, 1152, 16), (256, 640, 16), (256, 2176, 8)])
+def test_products_of_odd_multiples_of_128_columns(lib, align, n, steps, fmt, b_fmt, out):
+    """Contractions on both sides of where such products take 128 x 256 tiles and
+    pairs, whose last tile reaches beyond C: exact sums, zeros behind the tokens."""
+    experts = 5
+    k = steps * (256 if fmt == b_fmt == "e2m1" else 128) * (2 if out == F32 else 1)
+    rng = np.random.default_rng(n + steps)
+    e = rng.integers(0, experts, size=(4300, 2))
+    e[e == 3] = 4
+    e[:300] = -1                                     # leaves blocks behind the last stretch
+    p = lib.expert_sort(torch.from_numpy(e).int().to(dev), experts, align)
+    off = p.offsets.tolist()
+    assert off[experts] + 256 <= p.rows
+    aq, as_, a = blocks_of(rng, p.rows, k, fmt)
+    bq, bs, b = blocks_of(rng, experts * n, k, b_fmt)
+    ref = products(a, b.reshape(experts, n, k), off, p.rows)
+    for _ in range(2):
+        c = lib.mx_expert_gemm(aq, as_, bq.view(experts, n, -1), bs, p, fmt, b_fmt, out)
+        assert np.array_equal(c.double().cpu().numpy(), rounded(ref, out))
+    assert lib.last_device_status() == 0
+
+
 @pytest.mark.parametrize("out", [BF, F32])
 @pytest.mark.parametrize("fmt,b_fmt", PAIRS)
 @pytest.mark.parametrize("tokens,experts,n,k", [(700, 5, 1024, 2048), (700, 5, 1024, 2176), (1600, 2, 1536, 1792),
