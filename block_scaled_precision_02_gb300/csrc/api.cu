@@ -126,7 +126,7 @@ extern "C" const char* mxq_strerror(int s) {
 }
 
 extern "C" int mxq_test_stall_next_launch(int which) {
-  if (which != 0 && which != 1 && which != 2) return MXQ_ERR_BAD_ARG;
+  if (which < 0 || which > 3) return MXQ_ERR_BAD_ARG;
   std::lock_guard<std::mutex> lk(mxq_host::g_mu);
   mxq_host::g_test_stall = which;
   return MXQ_OK;

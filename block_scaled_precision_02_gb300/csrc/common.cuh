@@ -496,7 +496,7 @@ int launch_pdl_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 int* status_ptr();
 
 // Failure-detection test hook: true (once) if mxq_test_stall_next_launch(which)
-// armed it (which: 1 quantizer, 2 GEMM).
+// armed it (which: 1 quantizer, 2 GEMM, 3 the experts' products).
 bool take_test_stall(int which);
 
 }  // namespace mxq_host

@@ -49,6 +49,7 @@ struct Params {
   void* c;
   uint32_t a_type, b_type;
   uint32_t tx_bytes;              // of a stage (all CTAs of a pair)
+  int stall;                      // failure-detection test hook: 1 where CTA 0 never loads B of its first step
   int* status;
 };
 
@@ -292,11 +293,13 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     if (lane == 0) {
       const bool a_side = warp == 0;
       const It items(p);
-      int u = 0;                                               // stage use counter
+      // stage use counter; the test hook passes over a first step, whose phase never completes
+      int u = !a_side && blockIdx.x == 0 ? p.stall : 0;
+      int k0 = u;
       for (int tile = team; tile < p.ntiles && !*abort_flag; tile += teams) {
         const Item it = items.at(tile);
         const int ar = it.m0 + static_cast<int>(rank) * 128, br = it.br + static_cast<int>(rank) * C::B_ROWS;
-        for (int k = 0; k < it.steps; ++k, ++u) {
+        for (int k = k0; k < it.steps; ++k, ++u) {
           const int s = u % STAGES;
           if (!mbar_wait_suspend(smem_u32(&empty[s]), ((u / STAGES) & 1) ^ 1, p.status)) { *abort_flag = 1; break; }
           const uint32_t fb = CTAS == 2 ? cluster_map(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
@@ -313,6 +316,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
                               (it.br / 128 + h) * p.kb4b + (it.bk + k) * C::CHUNKS);
           }
         }
+        if (it.steps) k0 = 0;
       }
       // no copy of any CTA is still landing when the kernel ends (the other
       // CTA of a pair is held at the final cluster barrier)
@@ -540,6 +544,7 @@ int launch(Args& g, cudaStream_t st) {
   p.tx_bytes = CTAS * (tx_bytes(Cf::A_BYTES, a_u4) + tx_bytes(Cf::B_BYTES, b_u4) + Cf::SFA_BYTES + Cf::SFB_BYTES);
   p.status = status_ptr();
   if (!p.status) return MXQ_ERR_CUDA;
+  p.stall = take_test_stall(3);
   const dim3 grid(CTAS * std::min(p.ntiles, teams));
   if constexpr (CTAS == 2)
     return launch_pdl_cluster(kern, grid, dim3(Cf::THREADS), Cf::SMEM, st, 2, ma, mb, msa, msb, mc, p);

@@ -604,8 +604,9 @@ const char* mxq_strerror(int status);
 int mxq_version(void);
 
 /* Failure-detection test hook (no counterpart on the pages).  which = 1 arms
- * the next mxq_quantize call, 2 the next mxq_gemm call, 0 disarms: in that
- * launch CTA 0 leaves one of its input stages unloaded, so the mbarrier phase
+ * the next mxq_quantize call, 2 the next mxq_gemm call, 3 the next
+ * mxq_expert_gemm or mxq_expert_wgrad call, 0 disarms: in that launch CTA 0
+ * leaves one of its input stages unloaded (3: its B), so the mbarrier phase
  * that stage's consumer waits on never completes.  The bounded wait expires
  * after about a second, the kernel records MXQ_ERR_TIMEOUT in the device
  * status word, winds all of its roles down (awaiting its own copies, with a

@@ -232,3 +232,7 @@ def test_c_backward_reads_the_stretches_whenever_it_runs(so):
     # nothing to do: nothing is needed
     idle = [None, 8, 0, None, 8, 1, 0, 8, None, 0, 2, None, None, 3, None, 1, None, None, None]
     assert so.mxq_expert_combine_backward(*idle) in (0, NO_DEVICE)
+
+
+def test_c_stall_hook_covers_the_products(so):
+    assert [so.mxq_test_stall_next_launch(w) for w in (3, 0, 4, -1)] == [0, 0, BAD_ARG, BAD_ARG]

@@ -11,6 +11,7 @@ from block_scaled_precision_02_gb300 import inputs
 from oracle import formats as F
 from oracle import gemm as og
 from oracle import mx as omx
+from tests.expert_reference import decoded, integer_operand
 from tests.helpers import assert_bytes_equal, f64, np_
 
 pytestmark = pytest.mark.gpu
@@ -80,3 +81,35 @@ def test_disarm(lib):
     x = inputs.activations(128, 128, seed=1).cuda()
     lib.mx_quantize(x, "e4m3", "row", "floor")
     assert lib.last_device_status() == 0
+
+
+@pytest.mark.parametrize("op,align,tokens,experts,n,k", [("products", 128, 300, 3, 256, 1024), ("products", 128, 2500, 5, 2048, 512),
+                                                         ("products", 256, 2500, 5, 1024, 1024), ("gradient", 128, 300, 3, 256, 256),
+                                                         ("gradient", 256, 1600, 2, 1536, 1792)])
+def test_expert_products_wait_expires_and_context_survives(lib, op, align, tokens, experts, n, k):
+    """128 x 128 and 128 x 256 tiles of single SMs and pairs: one of the two
+    loading threads leaves out a step, so every role of that team gives up."""
+    L = lib.load()
+    rng = np.random.default_rng(n)
+    e = rng.integers(0, experts, size=(tokens, 2))
+    p = lib.expert_sort(torch.from_numpy(e).int().cuda(), experts, align)
+    off = p.offsets.tolist()
+    if op == "products":
+        (aq, as_), (bq, bs) = integer_operand(rng, p.rows, k, "e4m3"), integer_operand(rng, experts * n, k, "e4m3")
+        call = lambda: lib.mx_expert_gemm(aq, as_, bq.view(experts, n, k), bs, p, out_dtype=torch.float32)
+        a, b = decoded(aq, as_, "e4m3"), decoded(bq, bs, "e4m3").reshape(experts, n, k)
+        ref = np.zeros((p.rows, n))
+        for i in range(experts):
+            ref[off[i]:off[i + 1]] = a[off[i]:off[i + 1]] @ b[i].T
+    else:
+        (aq, as_), (bq, bs) = integer_operand(rng, n, p.rows, "e4m3"), integer_operand(rng, k, p.rows, "e4m3")
+        call = lambda: lib.mx_expert_wgrad(aq, as_, bq, bs, p)
+        a, b = decoded(aq, as_, "e4m3"), decoded(bq, bs, "e4m3")
+        ref = np.stack([a[:, off[i]:off[i + 1]] @ b[:, off[i]:off[i + 1]].T for i in range(experts)])
+    assert lib.last_device_status() == 0
+    assert L.mxq_test_stall_next_launch(3) == 0
+    call()
+    assert lib.last_device_status() == MXQ_ERR_TIMEOUT
+    assert lib.last_device_status() == 0                        # read clears it
+    c = call()
+    assert np.array_equal(c.double().cpu().numpy(), ref) and lib.last_device_status() == 0
