@@ -303,6 +303,24 @@ def test_gather_bit_for_bit(lib, tokens, cols, dtype):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("gap", [0, 8])
+@pytest.mark.parametrize("tokens,cols", [(40, 1024), (1000, 128), (30000, 128), (5000, 1024), (4001, 2080), (5000, 4096)])
+def test_gather_of_aligned_rows_bit_for_bit(lib, tokens, cols, gap, dtype):
+    """Rows of whole words, on both sides of where slots go apart: a token read
+    once and stored to the rows of all its slots, in one stretch and in several."""
+    g = torch.Generator(device=dev).manual_seed(tokens + cols)
+    bits, size = (torch.int16, 2) if dtype == BF else (torch.int32, 4)
+    x = torch.randint(-2 ** 15, 2 ** 15, (tokens, (cols + gap) * size // 2), generator=g, device=dev).to(torch.int16).view(dtype)[:, :cols]
+    assert x.data_ptr() % 16 == 0 and x.stride(0) * size % 16 == 0 and cols * size % 16 == 0
+    plan = lib.expert_sort(torch.randint(-1, 7, (tokens, 3), generator=g, device=dev), 7, 128)
+    got = lib.expert_gather(x, plan).view(bits)
+    want = torch.zeros(plan.rows, cols, dtype=bits, device=dev)
+    live = plan.row_slot >= 0
+    want[live] = x.contiguous().view(bits)[(plan.row_slot[live] // 3).long()]
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("cols", [512, 4096, 509, 2049])
 @pytest.mark.parametrize("dtype,dytype", [(BF, F32), (F32, BF)])
 def test_combine_backward_of_few_tokens(lib, cols, dtype, dytype):
