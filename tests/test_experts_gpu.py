@@ -353,6 +353,38 @@ def test_combine_backward_of_few_tokens(lib, cols, dtype, dytype):
     assert ((wa - wb).abs().double() <= 2 * cols * 2.0 ** -24 * mag).all()
 
 
+@pytest.mark.parametrize("gap", [0, 8])
+@pytest.mark.parametrize("dtype,dytype", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
+@pytest.mark.parametrize("tokens,top,cols", [(2000, 2, 128), (2000, 5, 256), (1000, 3, 512), (2000, 2, 1024), (2000, 5, 1024),
+                                             (700, 8, 2048), (500, 3, 4096), (300, 2, 8192), (4000, 5, 512), (6000, 4, 520)])
+def test_combine_backward_of_aligned_rows(lib, tokens, top, cols, dtype, dytype, gap):
+    """Aligned rows, several slots to a token and tokens enough that a team takes
+    all of a token's slots: dy in registers over pairs of slots, an odd one among
+    them, rows longer than that, and dy of another type than the rows."""
+    g = torch.Generator(device=dev).manual_seed(tokens + cols)
+    plan = lib.expert_sort(torch.randint(-1, 6, (tokens, top), generator=g, device=dev), 6, 128)
+    rows = torch.randn(plan.rows, cols + gap, generator=g, device=dev).to(dtype)[:, :cols]
+    rows[plan.row_slot < 0] = float("nan")                            # padding is not looked at
+    dy = torch.randn(tokens, cols + gap, generator=g, device=dev).to(dytype)[:, :cols]
+    w = torch.rand(tokens, top, generator=g, device=dev)
+    drows, dw = lib.expert_combine_backward(dy, rows, plan, w)
+    ref = torch.zeros(plan.rows, cols, dtype=torch.float64, device=dev)
+    # a product, sums of 8 within a vector, of a thread's vectors, of 32 lanes, of 8 warps
+    steps = 1 + 3 + cols // 256 + 1 + 5 + 8
+    for j in range(top):
+        live = plan.slot_row[:, j] >= 0
+        at, d = plan.slot_row[live, j].long(), dy[live].double()
+        ref[at] = d * w[live, j].double()[:, None]
+        prod = d * rows[at].double()
+        assert bool(((dw[live, j].double() - prod.sum(1)).abs() <= steps * 2.0 ** -24 * 1.001 * prod.abs().sum(1)).all())
+        assert not bool(dw[~live, j].any())
+    # the product rounded to float32, and once more to bf16
+    tol = ref.abs() * (2.0 ** -24 + (2.0 ** -8 * (1 + 2.0 ** -24) if dtype == BF else 0.0))
+    assert bool(((drows.double() - ref).abs() <= tol).all())
+    again = lib.expert_combine_backward(dy, rows, plan, w)
+    assert torch.equal(again[0], drows) and torch.equal(again[1], dw)
+
+
 def test_gradients_against_differences(lib):
     """The sum is linear in the rows and in the weights: a difference over a
     step h is the gradient up to the float32 rounding of both sums, 4 steps of
