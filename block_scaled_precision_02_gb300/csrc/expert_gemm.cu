@@ -10,13 +10,17 @@
 // half of B.  CTAS == 1: 128 x 256, or 128 x 128 with two accumulators in tensor
 // memory, one of which drains while the other fills.
 // Roles (one CTA per SM, persistent over tiles), as in the plain products:
-// warp 0 loads by TMA into a ring of stages, warp 6 copies the stages' scales
-// to tensor memory, warp 1 issues the MMAs; warps 2-5, and 7-10 where a tile
-// has 256 columns, store 128 columns each.
-// Measured: 8192 tokens, 2 of 8 experts, 14336 x 4096 E4M3 587 us (3.28 PFLOP/s, the
-// tensor pipe active 81 % of the time; a plain product of 16384 such rows 617),
-// the gradient of 4096 x 4096 187 us; with few tokens the weights' bytes (64 tokens, 16
-// experts of 4096 x 4096: 51 us, 86 % of the copy rate).
+// warp 0 loads A and its scales by TMA into a ring of stages, the last warp B and
+// its; warp 6 copies the stages' scales to tensor memory, warp 1 issues the MMAs;
+// warps 2-5, and 7-10 where two groups share 256 columns, store.
+// Measured: 8192 tokens, 2 of 8 experts, 14336 x 4096 E4M3 590 us at full clocks (3.26
+// PFLOP/s, the tensor pipe active 81 % of the time; a plain product of 16384 such rows
+// 617), 650 to 690 among others under the power cap; the gradient of 4096 x 4096 188 us.
+// Short contractions are bound by tile ends (4096 x 1024, 16 experts: 72 us, half the
+// rate).  Few tokens: the weights' bytes (64 tokens, 16 experts of 4096 x 4096: 51 us, 86 %
+// of the copy rate), fewer still a tile's own steps, 0.25 us each even from L2 (one tile,
+// K = 14336: 31.1 us; 31.0 with a quarter of A's or B's rows loaded or without copies of
+// scales, 24.8 with one MMA of four).
 // Columns are a multiple of 128: the last of wider tiles can reach beyond C.  Its
 // loads then bring the next expert's weights or zeros, and what they give is not
 // stored.

@@ -7,10 +7,13 @@
 //             dw[t][j] = sum_c dy[t][c] rows[row(t, j)][c]
 //
 // The sort is a counting sort of small integers: latency and launches bound
-// it (3.3 us for one token, 6.1 for 8192 of 2).  The others move rows and are
+// it (3.3 us for one token, 6.7 for 8192 of 2).  The others move rows and are
 // bound by HBM; of 8192 x 4096 bf16 with 2 of 16 experts, against the bytes that
-// each must move once at the measured copy rate: gather 36 us (95 % of it with its
-// padding), combine 32 (94 %), its backward pass 64 (85 %; one expert a token 98 %).
+// each must move once at the measured copy rate: gather 37 us (87 % of it with its
+// padding), combine 32 (94 %), its backward pass 64 (85 %; one expert a token 96 %).
+// Rows without a common alignment wait for loads: a gather of 8192 x 4095 takes 48 us
+// (67 %), its schedulers issuing in 34 % of the cycles, 70 % of the warps' time a wait for
+// global memory; the backward pass of 3648 x 1021, 4 slots, 17 us (61 %) with 61 % and 52 %.
 #include <algorithm>
 #include <atomic>
 
@@ -362,8 +365,10 @@ __device__ __forceinline__ void zero_padding(const RowArgs& a) {
   zero_rows<T, VE, ANY, THREADS>(a, last, a.rows - last, blockIdx.x, gridDim.x);
 }
 
-// A token's stretch is read once and written to the row of each of its slots (read
-// once a row instead, many tokens of several experts would come twice from HBM).
+// Aligned rows: a token's stretch is read once and written to the row of each of its
+// slots (read once a row instead, many tokens of several experts would come twice from
+// HBM).  Where slots go apart, and in rows without a common alignment, whose vectors
+// lie on what is written, every slot reads its token again.
 template <typename T, int VE, bool ANY>
 __global__ void __launch_bounds__(ROW_T) gather_kernel(const RowArgs a) {
   grid_dep_launch();
@@ -625,7 +630,9 @@ constexpr int BWD_T = 256, BWD_WARPS = BWD_T / 32;
 // lane stay in registers while the rows of its slots pass, two at a time.  Longer
 // rows, and those without alignment, go round in stretches, whose parts of the sums
 // are added up.  Four CTAs an SM, although some forms then spill: what counts is rows
-// in flight (8192 x 4096: 65 us, at three CTAs 71, at two of 512 threads 77).  Without
+// in flight (8192 x 4096 float32 rows of 2 slots, bf16 dy: 109 us, at three CTAs 120, at
+// two 146; 8192 x 14336 bf16 204, 222, 264; but bf16 rows with float32 dy, 8192 x 4096: 88,
+// 77, 87, and 8192 x 1024 22, 25, 32).  Without
 // alignment and G = 8 six (3047 x 14335, 4 slots: 152 us, at four 173), else four
 // (1021 bf16 columns: 18.4 us, at five 20.1).
 template <typename T, typename TY, int VE, int G, int NV, bool ANY>
@@ -956,7 +963,7 @@ int run_combine_direct(RowArgs a, cudaStream_t st) {
 
 // The ring pays from about 2^21 elements of y on (8192 x 4096 bf16: 32 us, read
 // directly 47; 515 x 2049 float32: 8.9 and 3.5).  Rows without a common alignment
-// take it as bf16 of DIRECT_COLS columns or more (8192 x 4095: 26 us, element by
+// take it as bf16 of DIRECT_COLS columns or more (8192 x 4095, one slot: 27 us, element by
 // element 49), as their single elements go round apart (16384 x 77, 4 slots: 40
 // and 6); float32 ones are read element by element as fast (5238 x 1023, 5
 // slots: 23 us, 31 in the ring).

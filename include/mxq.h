@@ -519,7 +519,7 @@ int mxq_expert_gather_mx(const void* x, int64_t tokens, int64_t cols, int64_t ld
  *          copy that mxq_quantize makes of stacked weights, which the backward
  *          pass multiplies with.
  * formats, alignment as mxq_gemm_mixed; N, K multiples of 128 (K of 256 where
- * both are E2M1).  align 256 runs on pairs of SMs.
+ * both are E2M1).  align 256 allows pairs of SMs.
  * rows, experts, align, offsets, block_expert  of the plan; rows == 0 is MXQ_OK.
  * c        [rows][N] bf16 or float32, 16-byte aligned. */
 int mxq_expert_gemm(const void* a_q, const uint8_t* a_s, int a_fmt,
