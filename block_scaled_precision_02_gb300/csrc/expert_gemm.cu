@@ -565,8 +565,9 @@ int launch(Args& g, cudaStream_t st) {
 //    on 128 x 128; 512 tokens over 8 experts of 1024 x 1024: 7.6 and 6.0);
 //  * both for an odd multiple of 128 columns only where the half of a last tile that
 //    is wasted, and the longer tile ends, are small against the contraction (a step:
-//    128 bytes of it; float32 outputs, whose tile ends take twice as long, count half).
-//    6127 tokens of 2, 5 experts, against 128 x 128:
+//    128 bytes of it; float32 outputs, whose tile ends take twice as long, count half:
+//    K = 1024, 640 columns 19.3 us on pairs, 16.1 on 128 x 128).  6127 tokens of 2, 5
+//    experts, K x columns, bf16, against 128 x 128:
 //      pairs from 12 steps and 640 columns on (1536 x 640: 17.7 us and 18.9; 1024 x 640
 //      14.3 and 14.0), from 8 and 1152 (1024 x 1920: 29.0 and 30.1; 512 x 1920 24.7
 //      and 22.3); E2M1, with one storing group, from 16 and 640 (4096 x 640: 22.1 and

@@ -7,9 +7,9 @@
 // before is encoded; a thread encodes whole blocks, from 16 words of a row or
 // from 32 of two columns.  8192 x 4096, 2 of 16 experts, rows and columns: 54 us for
 // 20224 rows (35.5 of bytes at the copy rate); rows alone 35, columns alone 38 (22.8).
-// No unit is full (issue ports 57 %, ALU 49 %, memory 55 %): the registers of 24 warps
-// an SM, and each of them waits in turn for its own results, for a port, for the
-// tile's two barriers and for shared memory (1.4, 1.4, 1.3 and 1.0 of 9 cycles an
+// No unit is full (issue ports 57 %, ALU 49 %, memory 55 %): the registers allow 24
+// warps an SM, and each waits in turn for its own results, for a port, for the tile's
+// two barriers and for shared memory (1.4, 1.4, 1.3 and 1.0 of 9 cycles an
 // instruction).  Three CTAs an SM against two: 54 and 62 us.
 #include <algorithm>
 #include <atomic>
